@@ -20,6 +20,8 @@ backward reduce-scatter and the next forward all-gather):
   dynamic scales.
 * ``oracle.accum``   -- gradient accumulation over micro-batches, with a
   reduce-scatter every micro-batch or once at the end (no_sync).
+* ``oracle.linear``  -- the linear layer that reads the all-gathered copy and
+  gives the gradients, and the dropout mask.
 
 Sources (the pages this follows; cited by page title and section):
 
@@ -37,4 +39,4 @@ force; none is "parity unpinned" except where the function's docstring says
 so.
 """
 
-from . import accum, clip, fp8, layout, step  # noqa: F401
+from . import accum, clip, fp8, layout, linear, step  # noqa: F401

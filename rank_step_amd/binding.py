@@ -1,4 +1,5 @@
-"""ctypes binding of librank_step.so (C ABI in include/fsdp_step.h).
+"""ctypes binding of librank_step.so (C ABI in include/fsdp_step.h and
+include/fsdp_linear.h).
 
 Argument marshalling only: every function here converts its Python arguments
 (torch tensors, ints, dicts) to the C types of the entry point of the same
@@ -24,6 +25,8 @@ FSDP_OK = 0
 ERRORS = {-1: "FSDP_E_ARG", -2: "FSDP_E_DTYPE", -3: "FSDP_E_ALIGN", -4: "FSDP_E_ALIAS",
           -5: "FSDP_E_HIP", -6: "FSDP_E_CAPACITY", -7: "FSDP_E_STATE"}
 DTYPES = {"f32": 0, "bf16": 1}
+WEIGHT_DTYPES = {"bf16": 1, "e4m3": 2}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 LAYOUTS = {"flat": 0, "shard0": 1, "owner": 2}
 
 # Every function the header declares; the CPU tests check each is exported.
@@ -34,10 +37,15 @@ EXPORTS = ("fsdp_last_error", "fsdp_shard_layout", "fsdp_rank_buffer_layout", "f
            "fsdp_mt_plan_get_info", "fsdp_mt_plan_destroy",
            "fsdp_mt_reduce_sqnorm", "fsdp_clip_coef", "fsdp_mt_step_clipped",
            "fsdp_mt_step_amax", "fsdp_mt_cast_fp8", "fsdp_mt_step_fp8",
-           "fsdp_mt_reduce_accumulate", "fsdp_grad_accumulate", "fsdp_reduce_sqnorm_noalloc")
+           "fsdp_mt_reduce_accumulate", "fsdp_grad_accumulate", "fsdp_reduce_sqnorm_noalloc",
+           "fsdp_linear_forward", "fsdp_linear_epilogue_backward", "fsdp_linear_grad_input",
+           "fsdp_linear_grad_weight", "fsdp_dropout")
 
 # fsdp_reduce_sqnorm_noalloc's limit (FSDP_NOALLOC_MAX_NUMEL in the header)
 NOALLOC_MAX_NUMEL = 33_292_288
+
+# The most workspace that a linear call uses (FSDP_LINEAR_WORKSPACE_BYTES in the header)
+LINEAR_WORKSPACE_BYTES = 64 << 20
 
 
 class FsdpError(RuntimeError):
@@ -94,6 +102,24 @@ class MtPlanInfo(ctypes.Structure):
         ("step_one_range", ctypes.c_int32), ("store_policy", ctypes.c_int32)]
 
 
+class DropoutMask(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("offset_dev", ctypes.c_void_p)]
+
+
+class Linear(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("w_scale", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("dropout", ctypes.POINTER(DropoutMask)),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                ("w_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 def lib_path():
     return _LIB_PATH
 
@@ -137,6 +163,12 @@ def lib():
             "fsdp_mt_reduce_accumulate": [vp, i32, vp, vp],
             "fsdp_grad_accumulate": [vp, vp, i32, i64, i32, vp],
             "fsdp_reduce_sqnorm_noalloc": [vp, vp, vp, i32, i64, i32, i64, i64, vp],
+            "fsdp_linear_forward": [ctypes.POINTER(Linear), vp],
+            "fsdp_linear_epilogue_backward": [vp, i64, vp, i32, i32, vp, i64, vp, i64, i32,
+                                              ctypes.POINTER(DropoutMask), i64, i64, vp, i64, vp],
+            "fsdp_linear_grad_input": [vp, i64, vp, i64, vp, i64, i32, vp, i64, i64, i64, vp, i64, vp],
+            "fsdp_linear_grad_weight": [vp, i64, i32, i32, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp],
+            "fsdp_dropout": [vp, i64, vp, i64, vp, i64, i32, i64, i64, ctypes.POINTER(DropoutMask), vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -336,6 +368,80 @@ def fsdp_reduce_sqnorm_noalloc(grad_shard_out, sqnorm_out, grad_slices, slice_dt
     _check(lib().fsdp_reduce_sqnorm_noalloc(_ptr(grad_shard_out), _ptr(sqnorm_out), _ptr(grad_slices),
                                             _dtype(slice_dtype), int(slice_stride), int(n_slices),
                                             int(shard_numel), int(valid), _stream(stream)))
+
+
+# ---------------------------------------------------------------- the linear layer
+#
+# Row strides (ld*) default to the row's length.  ``dropout``: None or a dict
+# with p, seed and offset, and optionally offset_dev (a device int64 [1]).
+# ``workspace``: None or a device tensor, all of which the call may use.
+
+def _mask(d):
+    if d is None:
+        return None
+    m64 = (1 << 64) - 1
+    return ctypes.pointer(DropoutMask(float(d["p"]), d["seed"] & m64, d["offset"] & m64,
+                                      _ptr(d.get("offset_dev"))))
+
+
+def _workspace(w):
+    return (None, 0) if w is None else (w.data_ptr(), w.numel() * w.element_size())
+
+
+def _ld(ld, cols):
+    return cols if ld is None else int(ld)
+
+
+def fsdp_linear_forward(y, x, w, m, n, k, w_dtype="bf16", w_scale=None, y_dtype="bf16", bias=None,
+                        residual=None, act="none", z=None, dropout=None, workspace=None, ldy=None,
+                        ldx=None, ldw=None, ldr=None, ldz=None, stream=None):
+    """z = x W^T + bias; y = dropout(act(z)) + residual."""
+    m, n, k = int(m), int(n), int(k)
+    ws, ws_bytes = _workspace(workspace)
+    a = Linear(m, n, k, _ptr(x), _ld(ldx, k), _ptr(w), _ld(ldw, k), _ptr(w_scale), _ptr(bias),
+               _ptr(residual), _ld(ldr, n), _ptr(y), _ld(ldy, n), _ptr(z), _ld(ldz, n), _mask(dropout), ws, ws_bytes,
+               WEIGHT_DTYPES.get(w_dtype, w_dtype), DTYPES.get(y_dtype, y_dtype),
+               ACTIVATIONS.get(act, act), 0)
+    _check(lib().fsdp_linear_forward(ctypes.byref(a), _stream(stream)))
+
+
+def fsdp_linear_epilogue_backward(dz, dy, m, n, z=None, act="none", dropout=None, db=None, db_dtype="f32",
+                                  accumulate=False, workspace=None, lddz=None, lddy=None, ldz=None,
+                                  stream=None):
+    """dz = dropout(dy) act'(z), and db = its column sums."""
+    m, n = int(m), int(n)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib().fsdp_linear_epilogue_backward(
+        _ptr(dz), _ld(lddz, n), _ptr(db), DTYPES.get(db_dtype, db_dtype), int(accumulate), _ptr(dy),
+        _ld(lddy, n), _ptr(z), _ld(ldz, n), ACTIVATIONS.get(act, act), _mask(dropout), m, n, ws, ws_bytes,
+        _stream(stream)))
+
+
+def fsdp_linear_grad_input(dx, dz, w, m, n, k, w_dtype="bf16", w_scale=None, workspace=None, lddx=None,
+                           lddz=None, ldw=None, stream=None):
+    """dx = dz W."""
+    m, n, k = int(m), int(n), int(k)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib().fsdp_linear_grad_input(_ptr(dx), _ld(lddx, k), _ptr(dz), _ld(lddz, n), _ptr(w), _ld(ldw, k),
+                                        WEIGHT_DTYPES.get(w_dtype, w_dtype), _ptr(w_scale), m, n, k, ws,
+                                        ws_bytes, _stream(stream)))
+
+
+def fsdp_linear_grad_weight(dw, dz, x, m, n, k, dw_dtype="bf16", accumulate=False, workspace=None, lddw=None,
+                            lddz=None, ldx=None, stream=None):
+    """dW = dz^T x, stored or added to what dw holds."""
+    m, n, k = int(m), int(n), int(k)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib().fsdp_linear_grad_weight(_ptr(dw), _ld(lddw, k), DTYPES.get(dw_dtype, dw_dtype), int(accumulate),
+                                         _ptr(dz), _ld(lddz, n), _ptr(x), _ld(ldx, k), m, n, k, ws, ws_bytes,
+                                         _stream(stream)))
+
+
+def fsdp_dropout(y, x, rows, cols, dtype, dropout, residual=None, ldy=None, ldx=None, ldr=None, stream=None):
+    """y = dropout(x) + residual; with dy for x and no residual, its gradient."""
+    cols = int(cols)
+    _check(lib().fsdp_dropout(_ptr(y), _ld(ldy, cols), _ptr(x), _ld(ldx, cols), _ptr(residual), _ld(ldr, cols),
+                              _dtype(dtype), int(rows), cols, _mask(dropout), _stream(stream)))
 
 
 class MtPlan:

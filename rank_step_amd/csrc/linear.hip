@@ -1,0 +1,1260 @@
+// The linear layer's kernels and entry points (gfx950 / MI355X): the product
+// that reads the all-gathered weight copy, with bias, activation, dropout and
+// residual in its epilogue, the gradients of both, and dropout alone.  The
+// arithmetic of each call is stated in include/fsdp_linear.h.
+//
+// Every product is C(i, j) = sum_l A(i, l) B(j, l) for output row i, output
+// column j and contraction index l:
+//   forward       i = token,  j = output feature, l = input feature: A = x,    B = W
+//   input grad    i = token,  j = input feature,  l = output feature: A = dz,  B = W
+//   weight grad   i = output feature, j = input feature, l = token:  A = dz,   B = x
+// An operand whose rows run along l ("l-major": x, W of the forward product,
+// dz of the input gradient) has the 8 consecutive l that one lane of a matrix
+// instruction takes in one 16-byte LDS read; one whose rows run along i or j
+// (W of the input gradient, both operands of the weight gradient) is read
+// through the LDS transpose read (ds_read_b64_tr_b16), so no operand is ever
+// transposed in memory.
+//
+// Floating point: bf16 matrix instructions accumulating in fp32, the epilogue
+// in fp32, FMA only where written (built with -ffp-contract=off).
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "fsdp_linear.h"
+#include "internal.h"
+
+using fsdp::fail;
+
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Vectors that may start at any element: gfx950's global accesses take any
+// alignment, so these are still single instructions.
+struct __attribute__((packed, aligned(2))) Bytes16 { u32x4 v; };
+struct __attribute__((packed, aligned(1))) Bytes8 { uint32_t v[2]; };
+
+constexpr int kXcds = 8;
+constexpr int kBK = 64;  // contraction elements of one LDS tile: 128 bytes of bf16
+
+// ---------------------------------------------------------------- dropout
+
+struct Mask {
+    uint64_t seed, offset;
+    const int64_t* offset_dev;
+    uint32_t t;   // keep where the 16 bits are at least t; 0: no dropout
+    float scale;  // 65536 / (65536 - t)
+};
+
+// The counter's high half: which mask of the seed's sequence.
+__device__ __forceinline__ uint64_t mask_offset(const Mask& m) {
+    return m.offset + (m.offset_dev ? static_cast<uint64_t>(*m.offset_dev) : 0);
+}
+
+// Philox-4x32-10 (Salmon et al. 2011): ten rounds of two 32x32 -> 64 bit
+// products.  One block serves the 8 elements of one 16-byte store: at 16 bits
+// an element the generator costs about half of what 32 would, which is what
+// lets the elementwise kernels stay on memory's side of the balance.
+__device__ __forceinline__ u32x4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
+    uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32);
+    uint32_t c2 = static_cast<uint32_t>(offset), c3 = static_cast<uint32_t>(offset >> 32);
+    uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t p0 = static_cast<uint64_t>(c0) * 0xD2511F53u;
+        const uint64_t p1 = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+        c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+        c1 = static_cast<uint32_t>(p1);
+        c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+        c3 = static_cast<uint32_t>(p0);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return u32x4{c0, c1, c2, c3};
+}
+
+// A dropped element is +0 whatever it held, so this selects.
+__device__ __forceinline__ void drop8(float (&v)[8], const Mask& m, uint64_t off, uint64_t block) {
+    const u32x4 w = philox(block, off, m.seed);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t bits = (i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
+        v[i] = bits >= m.t ? v[i] * m.scale : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------- activations
+
+constexpr float kLog2e = 1.44269504f;
+
+// exp through the hardware's base-2 exponential: off by about (|x| + 1) 2^-23
+// relative, from the rounding of x log2(e).
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// 1 / x within 1 ulp, without the division's refinement steps.
+__device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
+
+__device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + exp_fast(-z)); }
+
+// The normal distribution function and exp(-z^2/2).  With u = |z| / sqrt(2),
+// erfc(u) = exp(-u^2) g(u) and g(u) = t P(t), t = 1 / (1 + 0.4 u): g is smooth
+// and falls like 1/u, so a polynomial of degree 8 in t holds its relative
+// error under 1.3e-7 for every u >= 0 (coefficients fitted to erfc by weighted
+// least squares); evaluated in fp32 it is 4.4e-7.  erfc itself, and not
+// 1 + erf, so that the lower tail keeps its relative precision.  It shares its
+// exponential with the density that the gradient needs, and costs about a
+// third of separate erf and exp calls.
+__device__ __forceinline__ void normal(float z, float* phi, float* gauss) {
+    const float u = fabsf(z) * 0.70710678f;
+    const float t = rcp_fast(fmaf(0.4f, u, 1.0f));
+    float p = 0.050265517f;
+    p = fmaf(p, t, -0.18291515f);
+    p = fmaf(p, t, 0.16910799f);
+    p = fmaf(p, t, -0.0056271204f);
+    p = fmaf(p, t, 0.14144103f);
+    p = fmaf(p, t, 0.16853935f);
+    p = fmaf(p, t, 0.20784308f);
+    p = fmaf(p, t, 0.22566958f);
+    p = fmaf(p, t, 0.22567587f);
+    const float e = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
+    const float tail = 0.5f * p * t * e;
+    *phi = z > 0.0f ? 1.0f - tail : tail;
+    *gauss = e;
+}
+
+// act is the same for the whole launch: one uniform branch for 8 elements.
+__device__ __forceinline__ void activate8(float (&v)[8], int act) {
+    if (act == FSDP_ACT_RELU) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = v[q] <= 0.0f ? 0.0f : v[q];  // NaN stays
+    } else if (act == FSDP_ACT_GELU) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float phi, e;
+            normal(v[q], &phi, &e);
+            v[q] *= phi;
+        }
+    } else if (act == FSDP_ACT_SILU) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] *= sigmoid(v[q]);
+    }
+}
+
+// d *= act'(z)
+__device__ __forceinline__ void activation_grad8(float (&d)[8], const float (&z)[8], int act) {
+    if (act == FSDP_ACT_RELU) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d[q] = z[q] <= 0.0f ? 0.0f : d[q];
+    } else if (act == FSDP_ACT_GELU) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float phi, e;
+            normal(z[q], &phi, &e);
+            d[q] *= fmaf(z[q] * 0.39894228f, e, phi);  // 1 / sqrt(2 pi)
+        }
+    } else if (act == FSDP_ACT_SILU) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float s = sigmoid(z[q]);
+            d[q] *= s * fmaf(z[q], 1.0f - s, 1.0f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- 8 elements of a row
+
+__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
+__device__ __forceinline__ void unpack8(const u32x4& w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bf16x2 p = {static_cast<__bf16>(v[2 * i]), static_cast<__bf16>(v[2 * i + 1])};
+        w[i] = __builtin_bit_cast(uint32_t, p);
+    }
+    return w;
+}
+
+// The `cnt` (1 to 8) elements at p, zeros in the places behind them.
+__device__ __forceinline__ void load8(const uint16_t* p, int cnt, float (&v)[8]) {
+    if (cnt >= 8) {
+        unpack8(reinterpret_cast<const Bytes16*>(p)->v, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < cnt ? widen(p[i]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void load8(const float* p, int cnt, float (&v)[8]) {
+    if (cnt >= 8) {
+        const u32x4 a = reinterpret_cast<const Bytes16*>(p)->v, b = reinterpret_cast<const Bytes16*>(p + 4)->v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(a[i]);
+            v[4 + i] = __uint_as_float(b[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < cnt ? p[i] : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, int cnt, const float (&v)[8]) {
+    if (cnt >= 8) {
+        reinterpret_cast<Bytes16*>(p)->v = pack8(v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < cnt) p[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
+    }
+}
+
+__device__ __forceinline__ void store8(float* p, int cnt, const float (&v)[8]) {
+    if (cnt >= 8) {
+        reinterpret_cast<Bytes16*>(p)->v = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+        reinterpret_cast<Bytes16*>(p + 4)->v = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < cnt) p[i] = v[i];
+    }
+}
+
+// ---------------------------------------------------------------- epilogue
+
+struct Epilogue {
+    void* out;
+    const void* res;  // of out's type: the residual, or out itself to accumulate
+    uint16_t* z;
+    const uint16_t* bias;
+    const float* scale;  // the product is divided by it; null: 1
+    int64_t ldo, ldr, ldz;
+    Mask mask;
+    int32_t out_f32, act;
+};
+
+// Elements (i, j .. j + cnt) of the output, j a multiple of 8: the forward
+// call's bias, activation, dropout and residual; the gradients use the
+// division, the accumulation and the store.
+__device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t i, int64_t j, int cnt, int64_t n,
+                                          float recip, uint64_t off, float (&v)[8]) {
+    if (e.scale) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] *= recip;
+    }
+    if (e.bias) {
+        float b[8];
+        load8(e.bias + j, cnt, b);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += b[q];
+    }
+    if (e.z) store8(e.z + i * e.ldz + j, cnt, v);
+    activate8(v, e.act);
+    if (e.mask.t) drop8(v, e.mask, off, static_cast<uint64_t>(i) * ((n + 7) >> 3) + (j >> 3));
+    if (e.out_f32) {
+        if (e.res) {
+            float r[8];
+            load8(static_cast<const float*>(e.res) + i * e.ldr + j, cnt, r);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += r[q];
+        }
+        store8(static_cast<float*>(e.out) + i * e.ldo + j, cnt, v);
+    } else {
+        if (e.res) {
+            float r[8];
+            load8(static_cast<const uint16_t*>(e.res) + i * e.ldr + j, cnt, r);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += r[q];
+        }
+        store8(static_cast<uint16_t*>(e.out) + i * e.ldo + j, cnt, v);
+    }
+}
+
+// ---------------------------------------------------------------- tiled product
+
+struct Product {
+    const void* a;
+    const void* b;
+    int64_t lda, ldb;
+    int32_t m, n, k;        // output rows and columns, contraction length
+    int32_t splits, kper;   // the contraction in `splits` parts of kper (a multiple of kBK)
+    int32_t tm, tn;         // output tiles
+    float* part;            // splits > 1: [splits][m][pitch] partial sums
+    int32_t pitch;          // n rounded up to 8
+    Epilogue e;
+};
+
+// Workgroup b runs on XCD b mod 8, and each XCD has its own L2: consecutive
+// ids go to one XCD, so that the tiles it works on at a time are neighbours
+// and share operand rows in its L2.
+__device__ __forceinline__ int tile_id(int b, int total) {
+    const int x = b % kXcds, q = total / kXcds, r = total % kXcds;
+    return x * q + min(x, r) + b / kXcds;
+}
+
+// Tile `id` in bands of `kBand` tile rows walked column by column: any run of
+// consecutive ids covers a nearly square patch of the output.
+constexpr int kBand = 4;
+__device__ __forceinline__ void tile_at(int id, int tm, int tn, int* ti, int* tj) {
+    const int band = id / (kBand * tn), first = band * kBand, rows = min(kBand, tm - first);
+    const int in = id - band * (kBand * tn);
+    *ti = first + in % rows;
+    *tj = in / rows;
+}
+
+// LDS images of one operand's tile of `kBK` contraction elements, in 16-byte
+// slots.  l-major: slot = row * 8 + place, and place holds chunk place ^ (row
+// mod 8) of the row, so that the 8 rows which 8 lanes read at one chunk lie on
+// different banks.
+__device__ __forceinline__ int lmajor_chunk(int slot) { return (slot & 7) ^ ((slot >> 3) & 7); }
+// Row-of-outputs ("o-major"): slot = l * (width / 8) + place.  A transpose
+// read takes 32 bytes (16 outputs) of 4 consecutive l in each 16 lanes, so
+// whole 32-byte pairs of chunks are moved, by l mod 4 and bit 3 of l: the 8
+// rows that half a wave reads lie on different banks.
+__device__ __forceinline__ int omajor_swizzle(int l) { return (l & 3) | ((l >> 1) & 4); }
+template <int W>
+__device__ __forceinline__ int omajor_chunk(int slot) {
+    constexpr int kRow = W / 8;
+    const int l = slot / kRow, place = slot % kRow;
+    return place ^ ((omajor_swizzle(l) & (W / 16 - 1)) << 1);
+}
+
+using Lds = __attribute__((address_space(3))) uint8_t;
+
+constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset past every range used here
+
+// Copies one operand's tile from memory to LDS without passing through
+// registers.  Rows and chunks outside the matrix come as zeros from the
+// buffer's range check.  Needs 16-byte aligned rows and lengths that are
+// multiples of 8, so that no 16-byte chunk is partly outside.
+template <int W, int THREADS, bool LMAJOR>
+struct DirectTile {
+    static constexpr int kLoads = W * (kBK / 8) / THREADS;
+    const uint8_t* base;  // the tile's first row and column at contraction index l0
+    int64_t left;         // bytes from base to the matrix's end
+    int64_t step;         // bytes per kBK contraction elements
+    uint32_t off[kLoads];
+    int chunk;            // l-major: this thread's chunk (the same in all its loads)
+
+    __device__ __forceinline__ void init(const void* p, int64_t ld, int o0, int no, int l0, int nl, int tid) {
+        const int64_t row = ld * 2;
+        if (LMAJOR) {
+            base = static_cast<const uint8_t*>(p) + o0 * row + static_cast<int64_t>(l0) * 2;
+            left = (static_cast<int64_t>(no) - 1 - o0) * row + (static_cast<int64_t>(nl) - l0) * 2;
+            step = kBK * 2;
+            chunk = lmajor_chunk(tid);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int r = (i * THREADS + tid) >> 3;
+                off[i] = o0 + r < no ? static_cast<uint32_t>(r * row + chunk * 16) : kOutside;
+            }
+        } else {
+            base = static_cast<const uint8_t*>(p) + l0 * row + static_cast<int64_t>(o0) * 2;
+            left = (static_cast<int64_t>(nl) - 1 - l0) * row + (static_cast<int64_t>(no) - o0) * 2;
+            step = kBK * row;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int slot = i * THREADS + tid, c = omajor_chunk<W>(slot);
+                off[i] = o0 + c * 8 < no ? static_cast<uint32_t>(slot / (W / 8) * row + c * 16) : kOutside;
+            }
+        }
+    }
+
+    // Issues the tile's loads; lleft: contraction elements left from here on.
+    __device__ __forceinline__ void load(Lds* dst, int wave, int lleft) {
+        const uint32_t range = static_cast<uint32_t>(left < 0 ? 0 : min(left, static_cast<int64_t>(0x7fffffff)));
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(range), 0x00020000);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            uint32_t o = off[i];
+            if (LMAJOR) o = chunk * 8 < lleft ? o : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (__attribute__((address_space(3))) void*)(dst + (i * THREADS + wave * 64) * 16), 16, o, 0, 0, 0);
+        }
+        base += step;
+        left -= step;
+    }
+};
+
+// The same through registers, for rows that start anywhere, lengths that are
+// no multiple of 8, and E4M3 codes, which become bf16 on the way.
+template <int W, int THREADS, bool LMAJOR, bool FP8>
+struct StagedTile {
+    static constexpr int kLoads = W * (kBK / 8) / THREADS;
+    const uint8_t* p;
+    int64_t ld;
+    int o0, no, nl, tid;
+    u32x4 reg[kLoads];
+
+    __device__ __forceinline__ void init(const void* ptr, int64_t ld_, int o0_, int no_, int, int nl_, int tid_) {
+        p = static_cast<const uint8_t*>(ptr);
+        ld = ld_;
+        o0 = o0_;
+        no = no_;
+        nl = nl_;
+        tid = tid_;
+    }
+
+    // l0: the tile's first contraction index; nl: the end of this part's.
+    __device__ __forceinline__ void load(int l0) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int slot = i * THREADS + tid;
+            int64_t row, col;
+            int cnt;  // elements of this chunk inside the matrix
+            if (LMAJOR) {
+                row = o0 + (slot >> 3);
+                col = l0 + lmajor_chunk(slot) * 8;
+                cnt = row < no ? static_cast<int>(min(static_cast<int64_t>(8), nl - col)) : 0;
+            } else {
+                row = l0 + slot / (W / 8);
+                col = o0 + omajor_chunk<W>(slot) * 8;
+                cnt = row < nl ? static_cast<int>(min(static_cast<int64_t>(8), no - col)) : 0;
+            }
+            if (FP8) {
+                const uint8_t* q = p + row * ld + col;
+                uint32_t w0 = 0, w1 = 0;
+                if (cnt >= 8) {
+                    const Bytes8 b = *reinterpret_cast<const Bytes8*>(q);
+                    w0 = b.v[0];
+                    w1 = b.v[1];
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        const uint32_t c = s < cnt ? q[s] : 0u;
+                        if (s < 4) w0 |= c << (8 * s);
+                        else w1 |= c << (8 * (s - 4));
+                    }
+                }
+                reg[i][0] = w0;
+                reg[i][1] = w1;
+            } else {
+                const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + row * ld + col;
+                if (cnt >= 8) {
+                    reg[i] = reinterpret_cast<const Bytes16*>(q)->v;
+                } else {
+                    u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        const uint32_t c = s < cnt ? q[s] : 0u;
+                        w[s / 2] |= c << (16 * (s & 1));
+                    }
+                    reg[i] = w;
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(Lds* dst) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            u32x4 w = reg[i];
+            if (FP8) {
+                const uint32_t c0 = w[0], c1 = w[1];
+                w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, false));
+                w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, true));
+                w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, false));
+                w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, true));
+            }
+            *(__attribute__((address_space(3))) u32x4*)(dst + (i * THREADS + tid) * 16) = w;
+        }
+    }
+};
+
+// One lane's operand of a 16x16x32 matrix instruction from a tile's LDS image:
+// lane l holds output o0 + l mod 16 and contraction elements 8 (l / 16) + 0..7
+// of the 32 that start at 32 * kk.
+template <int W, bool LMAJOR, int NF>
+struct Fragments {
+    int at[LMAJOR ? 1 : NF];
+
+    __device__ __forceinline__ void init(int o0, int lane) {
+        const int lo = lane & 15, g = lane >> 4;
+        if (LMAJOR) {
+            at[0] = (o0 + lo) * 128 + ((g ^ (lo & 7)) << 4);
+        } else {
+            const int sw = ((lo >> 2) | ((g & 1) << 2)) & (W / 16 - 1);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                at[f] = (g * 8 + (lo >> 2)) * (W * 2) + (((o0 >> 4) + f) ^ sw) * 32 + (lo & 3) * 8;
+        }
+    }
+
+    __device__ __forceinline__ bf16x8 get(const Lds* tile, int f, int kk) const {
+        if (LMAJOR) {
+            // chunk 4 kk + g: kk flips bit 2 of the place
+            return *(const __attribute__((address_space(3))) bf16x8*)(tile + (at[0] ^ (kk << 6)) + f * (16 * 128));
+        } else {
+            using P = __attribute__((address_space(3))) s16x4*;
+            const Lds* q = tile + at[f] + kk * 32 * (W * 2);
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)q);
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 4 * (W * 2)));
+            const struct { s16x4 x, y; } xy = {x, y};
+            return __builtin_bit_cast(bf16x8, xy);
+        }
+    }
+};
+
+// BM x BN output tile by WI x WJ waves, two LDS stages of kBK contraction
+// elements: while one is multiplied the next arrives.
+template <int BM, int BN, int WI, int WJ, bool AL, bool BL, bool DIRECT, bool FP8>
+__global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
+    constexpr int kThreads = WI * WJ * 64, kWM = BM / WI, kWN = BN / WJ, kFI = kWM / 16, kFJ = kWN / 16;
+    constexpr int kStage = (BM + BN) * kBK * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t s1[kStage];
+    Lds* const l0 = (Lds*)s0;
+    Lds* const l1 = (Lds*)s1;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tiles = g.tm * g.tn;
+    const int id = tile_id(blockIdx.x, tiles * g.splits);
+    const int split = id / tiles;
+    int ti, tj;
+    tile_at(id - split * tiles, g.tm, g.tn, &ti, &tj);
+    const int i0 = ti * BM, j0 = tj * BN;
+    const int kbeg = split * g.kper, kend = min(g.k, kbeg + g.kper);
+    const int steps = kend > kbeg ? (kend - kbeg + kBK - 1) / kBK : 0;
+    const int wi = wave / WJ, wj = wave % WJ;
+
+    f32x4 acc[kFI][kFJ];
+#pragma unroll
+    for (int i = 0; i < kFI; ++i)
+#pragma unroll
+        for (int j = 0; j < kFJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    Fragments<BM, AL, kFI> fa;
+    Fragments<BN, BL, kFJ> fb;
+    fa.init(wi * kWM, lane);
+    fb.init(wj * kWN, lane);
+
+    auto multiply = [&](const Lds* stage) {
+#pragma unroll
+        for (int kk = 0; kk < kBK / 32; ++kk) {
+            bf16x8 a[kFI], b[kFJ];
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j) b[j] = fb.get(stage + BM * kBK * 2, j, kk);
+#pragma unroll
+            for (int i = 0; i < kFI; ++i) a[i] = fa.get(stage, i, kk);
+#pragma unroll
+            for (int i = 0; i < kFI; ++i)
+#pragma unroll
+                for (int j = 0; j < kFJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+        }
+    };
+
+    if constexpr (DIRECT) {
+        DirectTile<BM, kThreads, AL> ta;
+        DirectTile<BN, kThreads, BL> tb;
+        ta.init(g.a, g.lda, i0, g.m, kbeg, AL ? g.k : kend, tid);
+        tb.init(g.b, g.ldb, j0, g.n, kbeg, BL ? g.k : kend, tid);
+        int lleft = kend - kbeg;
+        auto fetch = [&](Lds* stage) {
+            ta.load(stage, wave, lleft);
+            tb.load(stage + BM * kBK * 2, wave, lleft);
+            lleft -= kBK;
+        };
+        // One step: this stage's loads have arrived in every wave, and every
+        // wave is done with the other stage, which the next loads then fill.
+        auto step = [&](int s, Lds* cur, Lds* nxt) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (s + 1 < steps) fetch(nxt);
+            multiply(cur);
+        };
+        if (steps > 0) fetch(l0);
+        int s = 0;
+        for (; s + 1 < steps; s += 2) {
+            step(s, l0, l1);
+            step(s + 1, l1, l0);
+        }
+        if (s < steps) step(s, l0, l1);
+    } else {
+        StagedTile<BM, kThreads, AL, false> ta;
+        StagedTile<BN, kThreads, BL, FP8> tb;
+        ta.init(g.a, g.lda, i0, g.m, kbeg, kend, tid);
+        tb.init(g.b, g.ldb, j0, g.n, kbeg, kend, tid);
+        auto step = [&](int s, Lds* cur, Lds* nxt) {
+            __syncthreads();
+            const bool more = s + 1 < steps;
+            if (more) {
+                ta.load(kbeg + (s + 1) * kBK);
+                tb.load(kbeg + (s + 1) * kBK);
+            }
+            multiply(cur);
+            if (more) {
+                ta.store(nxt);
+                tb.store(nxt + BM * kBK * 2);
+            }
+        };
+        if (steps > 0) {
+            ta.load(kbeg);
+            tb.load(kbeg);
+            ta.store(l0);
+            tb.store(l0 + BM * kBK * 2);
+        }
+        int s = 0;
+        for (; s + 1 < steps; s += 2) {
+            step(s, l0, l1);
+            step(s + 1, l1, l0);
+        }
+        if (s < steps) step(s, l0, l1);
+    }
+
+    // Lane l holds of each 16x16 block output row l mod 16 and columns
+    // 4 (l / 16) + 0..3.
+    const int lo = lane & 15, hi = lane >> 4;
+    if (g.splits > 1) {
+        float* part = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
+#pragma unroll
+        for (int i = 0; i < kFI; ++i) {
+            const int row = i0 + wi * kWM + i * 16 + lo;
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j) {
+                const int col = j0 + wj * kWN + j * 16 + hi * 4;
+                if (row < g.m && col < g.pitch)
+                    *reinterpret_cast<f32x4*>(part + static_cast<int64_t>(row) * g.pitch + col) = acc[i][j];
+            }
+        }
+        return;
+    }
+    // 64 rows at a time through the wave's own 16 KB of LDS, so that a lane has
+    // 8 consecutive columns: one 16-byte store and one mask block.  A row's
+    // 16-byte chunks are permuted by the row, which spreads the 16 rows that
+    // one write touches over the banks.
+    __syncthreads();  // the last stage is being read until here
+    static_assert(kWN == 64 && kWM % 64 == 0 && kStage == WI * WJ / 2 * 16384, "a piece of 64 x 64 floats a wave");
+    constexpr int kHalf = WI * WJ / 2;
+    Lds* const piece = (wave < kHalf ? l0 : l1) + wave % kHalf * 16384;
+    using Quad = __attribute__((address_space(3))) f32x4;
+    const float recip = g.e.scale ? 1.0f / *g.e.scale : 1.0f;
+    const uint64_t off = mask_offset(g.e.mask);
+    const int c = lane & 7, col = j0 + wj * kWN + c * 8;
+#pragma unroll
+    for (int h = 0; h < kWM / 64; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j)
+                *(Quad*)(piece + (i * 16 + lo) * 256 + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int r = lane >> 3; r < 64; r += 8) {
+            const f32x4 x = *(const Quad*)(piece + r * 256 + (((c * 2) ^ (r & 15)) << 4));
+            const f32x4 y = *(const Quad*)(piece + r * 256 + (((c * 2 + 1) ^ (r & 15)) << 4));
+            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+            const int row = i0 + wi * kWM + h * 64 + r;
+            if (row < g.m && col < g.n) epilogue8(g.e, row, col, g.n - col, g.n, recip, off, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// The sum of a split product's parts, in order, and the epilogue.
+constexpr int kJoinBlock = 256;
+__global__ __launch_bounds__(kJoinBlock) void join_kernel(Product g) {
+    const int chunks = g.pitch / 8;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kJoinBlock + threadIdx.x;
+    if (id >= static_cast<int64_t>(g.m) * chunks) return;
+    const int64_t i = id / chunks;
+    const int j = static_cast<int>(id - i * chunks) * 8;
+    const float* p = g.part + id * 8;
+    const int64_t stride = static_cast<int64_t>(g.m) * g.pitch;
+    f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s) {
+        x += *reinterpret_cast<const f32x4*>(p + s * stride);
+        y += *reinterpret_cast<const f32x4*>(p + s * stride + 4);
+    }
+    float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    epilogue8(g.e, i, j, g.n - j, g.n, g.e.scale ? 1.0f / *g.e.scale : 1.0f, mask_offset(g.e.mask), v);
+}
+
+// ---------------------------------------------------------------- elementwise passes
+
+// 2^tx lanes take one row's chunks of 8 elements (as many as the row has, up
+// to a wave), the block's 256 >> tx other places take rows.
+constexpr int kElemBlock = 256;
+struct Grid {
+    int32_t tx, cblocks;  // lanes a row (log2), column blocks
+    int64_t rows;         // rows a block takes in all (a multiple of 256 >> tx)
+};
+
+struct DropoutArgs {
+    void* y;
+    const void* x;
+    const void* res;
+    int64_t ldy, ldx, ldr, m, n;
+    Mask mask;
+    Grid g;
+};
+
+template <typename T>
+__global__ __launch_bounds__(kElemBlock) void dropout_kernel(DropoutArgs a) {
+    const int tid = threadIdx.x, per = kElemBlock >> a.g.tx;
+    const int64_t rb = blockIdx.x / a.g.cblocks;
+    const int64_t j = ((static_cast<int64_t>(blockIdx.x % a.g.cblocks) << a.g.tx) + (tid & ((1 << a.g.tx) - 1))) * 8;
+    if (j >= a.n) return;
+    const int cnt = static_cast<int>(min(a.n - j, static_cast<int64_t>(8)));
+    const int64_t chunks = (a.n + 7) >> 3, end = min(a.m, (rb + 1) * a.g.rows);
+    const uint64_t off = mask_offset(a.mask);
+    for (int64_t i = rb * a.g.rows + (tid >> a.g.tx); i < end; i += per) {
+        float v[8];
+        load8(static_cast<const T*>(a.x) + i * a.ldx + j, cnt, v);
+        if (a.mask.t) drop8(v, a.mask, off, static_cast<uint64_t>(i * chunks + (j >> 3)));
+        if (a.res) {
+            float r[8];
+            load8(static_cast<const T*>(a.res) + i * a.ldr + j, cnt, r);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += r[q];
+        }
+        store8(static_cast<T*>(a.y) + i * a.ldy + j, cnt, v);
+    }
+}
+
+struct BackwardArgs {
+    uint16_t* dz;
+    const uint16_t* dy;
+    const uint16_t* z;
+    int64_t lddz, lddy, ldz, m, n;
+    float* part;  // [row blocks][n] column sums, or null
+    void* db;     // with one row block: the result
+    int32_t db_f32, accumulate, act, sums;
+    Mask mask;
+    Grid g;
+};
+
+__device__ __forceinline__ void put_db(void* db, int f32, int accumulate, int64_t j, float s) {
+    if (f32) {
+        float* p = static_cast<float*>(db) + j;
+        *p = accumulate ? *p + s : s;
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(db) + j;
+        *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(accumulate ? widen(*p) + s : s));
+    }
+}
+
+__global__ __launch_bounds__(kElemBlock) void epilogue_backward_kernel(BackwardArgs a) {
+    __shared__ float sums[kElemBlock][9];
+    const int tid = threadIdx.x, per = kElemBlock >> a.g.tx, width = 1 << a.g.tx;
+    const int64_t rb = blockIdx.x / a.g.cblocks;
+    const int64_t j = ((static_cast<int64_t>(blockIdx.x % a.g.cblocks) << a.g.tx) + (tid & (width - 1))) * 8;
+    const int cnt = static_cast<int>(min(a.n - j, static_cast<int64_t>(8)));  // <= 0 outside
+    const int64_t chunks = (a.n + 7) >> 3, end = cnt > 0 ? min(a.m, (rb + 1) * a.g.rows) : 0;
+    const uint64_t off = mask_offset(a.mask);
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int64_t i = rb * a.g.rows + (tid >> a.g.tx); i < end; i += per) {
+        float v[8];
+        load8(a.dy + i * a.lddy + j, cnt, v);
+        float z[8];
+        if (a.act != FSDP_ACT_NONE) load8(a.z + i * a.ldz + j, cnt, z);
+        if (a.mask.t) drop8(v, a.mask, off, static_cast<uint64_t>(i * chunks + (j >> 3)));
+        if (a.act != FSDP_ACT_NONE) activation_grad8(v, z, a.act);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] += v[q];
+        if (a.dz) store8(a.dz + i * a.lddz + j, cnt, v);
+    }
+    if (!a.sums) return;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sums[tid][q] = sum[q];
+    __syncthreads();
+    // thread t of the block's first ones: column t of the block, over its rows in order
+    for (int t = tid; t < width * 8; t += kElemBlock) {
+        const int64_t col = (static_cast<int64_t>(blockIdx.x % a.g.cblocks) << a.g.tx) * 8 + t;
+        if (col >= a.n) break;
+        float s = 0;
+        for (int r = 0; r < per; ++r) s += sums[r * width + (t >> 3)][t & 7];
+        if (a.part) a.part[rb * a.n + col] = s;
+        else put_db(a.db, a.db_f32, a.accumulate, col, s);
+    }
+}
+
+// db from the row blocks' sums: 64 columns a block, four threads a column.
+__global__ __launch_bounds__(kElemBlock) void column_sum_kernel(const float* part, int64_t n, int32_t blocks,
+                                                                void* db, int32_t f32, int32_t accumulate) {
+    __shared__ float sums[4][64];
+    const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + c;
+    float s = 0;
+    if (col < n) {
+#pragma unroll 8
+        for (int r = q; r < blocks; r += 4) s += part[r * n + col];
+    }
+    sums[q][c] = s;
+    __syncthreads();
+    if (q == 0 && col < n) put_db(db, f32, accumulate, col, (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]));
+}
+
+// ---------------------------------------------------------------- host: arguments
+
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// One matrix (or vector: rows = 1) of a call.
+struct Matrix {
+    const void* p;
+    int64_t rows, cols, ld;
+    int elem;
+    const char* what;
+    bool written;
+
+    bool empty() const { return !p || rows == 0 || cols == 0; }
+    uintptr_t lo() const { return reinterpret_cast<uintptr_t>(p); }
+    uintptr_t hi() const { return lo() + static_cast<uintptr_t>(((rows - 1) * ld + cols) * elem); }
+};
+
+int32_t check_matrix(const Matrix& x, bool may_be_null, const char* who) {
+    if (!x.p) {
+        if (may_be_null || x.rows == 0 || x.cols == 0) return FSDP_OK;
+        return fail(FSDP_E_ARG, "%s: null %s", who, x.what);
+    }
+    if (x.rows > 1 && x.ld < x.cols)
+        return fail(FSDP_E_ARG, "%s: row stride %lld of %s is below its %lld columns", who,
+                    static_cast<long long>(x.ld), x.what, static_cast<long long>(x.cols));
+    if (!aligned(x.p, static_cast<uintptr_t>(x.elem)))
+        return fail(FSDP_E_ALIGN, "%s: %s misaligned", who, x.what);
+    int64_t bytes;
+    if (x.rows > 0 && (x.ld < 0 || !fsdp::mul_i64(x.rows, x.ld, &bytes) || !fsdp::mul_i64(bytes, x.elem, &bytes) ||
+                       !fsdp::add_i64(bytes, x.cols * x.elem, &bytes)))
+        return fail(FSDP_E_ARG, "%s: size of %s overflows", who, x.what);
+    return FSDP_OK;
+}
+
+// Whether two matrices share a byte.  Of one row stride, they do unless their
+// columns differ everywhere; of different strides, when their extents meet.
+bool overlap(const Matrix& a, const Matrix& b) {
+    if (a.empty() || b.empty() || a.hi() <= b.lo() || b.hi() <= a.lo()) return false;
+    const int64_t row = a.ld * a.elem;
+    if (a.rows == 1 || b.rows == 1 || row != b.ld * b.elem) return true;
+    const uintptr_t span = static_cast<uintptr_t>(row);
+    const uintptr_t d = a.lo() <= b.lo() ? (b.lo() - a.lo()) % span : (span - (a.lo() - b.lo()) % span) % span;
+    // columns [0, wa) of a against [d, d + wb) of b, on a circle of one row
+    return d < static_cast<uintptr_t>(a.cols * a.elem) || d + static_cast<uintptr_t>(b.cols * b.elem) > span;
+}
+
+bool same(const Matrix& a, const Matrix& b) { return a.p == b.p && a.ld == b.ld && a.elem == b.elem; }
+
+// twin(a, b): whether written a may be b itself
+template <typename F>
+int32_t check_overlaps(const std::vector<Matrix>& ms, const char* who, F&& twin) {
+    for (size_t i = 0; i < ms.size(); ++i)
+        for (size_t j = i + 1; j < ms.size(); ++j) {
+            const Matrix &a = ms[i], &b = ms[j];
+            if (!(a.written || b.written) || !overlap(a, b)) continue;
+            if (same(a, b) && twin(a, b)) continue;
+            return fail(FSDP_E_ALIAS, "%s: %s overlaps %s", who, a.what, b.what);
+        }
+    return FSDP_OK;
+}
+
+int32_t check_sizes(int64_t m, int64_t n, int64_t k, const char* who) {
+    if (m < 0 || n < 0 || k < 0) return fail(FSDP_E_ARG, "%s: negative size", who);
+    if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return fail(FSDP_E_CAPACITY, "%s: a size exceeds 2^30", who);
+    return FSDP_OK;
+}
+
+int32_t check_workspace(const void* p, int64_t bytes, const char* who) {
+    if (bytes < 0 || (!p && bytes > 0)) return fail(FSDP_E_ARG, "%s: bad workspace", who);
+    if (!aligned(p, 16)) return fail(FSDP_E_ALIGN, "%s: workspace misaligned", who);
+    return FSDP_OK;
+}
+
+int32_t make_mask(const fsdp_dropout_mask* d, Mask* out, const char* who) {
+    *out = Mask{0, 0, nullptr, 0, 1.0f};
+    if (!d) return FSDP_OK;
+    if (!(d->p >= 0.0 && d->p <= 1.0)) return fail(FSDP_E_ARG, "%s: dropout p outside [0, 1]", who);
+    if (!aligned(d->offset_dev, 8)) return fail(FSDP_E_ALIGN, "%s: offset_dev misaligned", who);
+    out->seed = d->seed;
+    out->offset = d->offset;
+    out->offset_dev = d->offset_dev;
+    out->t = static_cast<uint32_t>(std::rint(d->p * 65536.0));
+    out->scale = out->t < 65536 ? static_cast<float>(65536.0 / (65536.0 - out->t)) : 0.0f;
+    return FSDP_OK;
+}
+
+Matrix vector(const void* p, int64_t n, int elem, const char* what, bool written = false) {
+    return Matrix{p, 1, n, n, elem, what, written};
+}
+
+Matrix bytes_of(const void* p, int64_t bytes, const char* what, bool written) {
+    return Matrix{p, 1, bytes, bytes, 1, what, written};
+}
+
+// The workspace that the call will actually write is within its first bytes.
+Matrix workspace_of(const void* p, int64_t bytes) {
+    return bytes_of(p, std::min(bytes, FSDP_LINEAR_WORKSPACE_BYTES), "workspace", true);
+}
+
+int32_t launched(const char* who) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(FSDP_E_HIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+    return FSDP_OK;
+}
+
+// ---------------------------------------------------------------- host: products
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Rows on 16-byte boundaries and lengths in whole 16-byte chunks; a tile's
+// rows within the 31 bits of a buffer offset.
+bool direct_ok(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+    return aligned(p, 16) && cols % 8 == 0 && (ld % 8 == 0 || rows <= 1) && ld <= (int64_t(1) << 21);
+}
+
+template <int BM, int BN, int WI, int WJ, bool AL, bool BL, bool DIRECT, bool FP8>
+int32_t launch_product(Product& g, hipStream_t stream, const char* who) {
+    g.tm = static_cast<int32_t>(ceil_div(g.m, BM));
+    g.tn = static_cast<int32_t>(ceil_div(g.n, BN));
+    const int64_t blocks = static_cast<int64_t>(g.tm) * g.tn * g.splits;
+    const int64_t joins = ceil_div(static_cast<int64_t>(g.m) * (g.pitch / 8), kJoinBlock);
+    if (blocks > 0x7fffff || (g.splits > 1 && joins > 0x7fffff))
+        return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
+    product_kernel<BM, BN, WI, WJ, AL, BL, DIRECT, FP8>
+        <<<dim3(static_cast<uint32_t>(blocks)), dim3(WI * WJ * 64), 0, stream>>>(g);
+    int32_t st = launched(who);
+    if (st != FSDP_OK || g.splits == 1) return st;
+    join_kernel<<<dim3(static_cast<uint32_t>(joins)), dim3(kJoinBlock), 0, stream>>>(g);
+    return launched(who);
+}
+
+constexpr int kCus = 256;
+
+// Parts of the contraction: enough workgroups for the chip's CUs, at least
+// four LDS tiles each, partial sums within the workspace.
+void choose_splits(Product& g, int64_t tiles, void* workspace, int64_t bytes) {
+    const int64_t steps = std::max<int64_t>(1, ceil_div(g.k, kBK));
+    const int64_t one = static_cast<int64_t>(g.m) * g.pitch * 4;
+    int64_t splits = std::min<int64_t>(ceil_div(kCus, std::max<int64_t>(1, tiles)), steps / 4);
+    splits = std::min(splits, std::min(bytes, FSDP_LINEAR_WORKSPACE_BYTES) / std::max<int64_t>(1, one));
+    if (splits < 2) splits = 1;
+    const int64_t per = ceil_div(steps, splits);
+    g.splits = static_cast<int32_t>(ceil_div(steps, per));
+    g.kper = static_cast<int32_t>(per * kBK);
+    g.part = static_cast<float*>(workspace);
+}
+
+template <bool AL, bool BL>
+int32_t run_product(Product& g, bool fp8, bool direct, void* workspace, int64_t bytes, hipStream_t stream,
+                    const char* who) {
+    if (g.m == 0 || g.n == 0) return FSDP_OK;
+    g.pitch = (g.n + 7) / 8 * 8;
+    const int64_t big = ceil_div(g.m, 256) * ceil_div(g.n, 256);
+    if (direct && big >= kCus / 2) {
+        choose_splits(g, big, workspace, 0);
+        return launch_product<256, 256, 2, 4, AL, BL, true, false>(g, stream, who);
+    }
+    choose_splits(g, ceil_div(g.m, 128) * ceil_div(g.n, 128), workspace, bytes);
+    if (direct) return launch_product<128, 128, 2, 2, AL, BL, true, false>(g, stream, who);
+    if constexpr (AL) {
+        if (fp8) return launch_product<128, 128, 2, 2, AL, BL, false, true>(g, stream, who);
+    }
+    return launch_product<128, 128, 2, 2, AL, BL, false, false>(g, stream, who);
+}
+
+int32_t check_weight(int32_t w_dtype, const float* w_scale, const char* who) {
+    if (w_dtype != FSDP_DT_BF16 && w_dtype != FSDP_DT_E4M3)
+        return fail(FSDP_E_DTYPE, "%s: weights are bf16 or E4M3", who);
+    if (w_dtype == FSDP_DT_E4M3 && !w_scale) return fail(FSDP_E_ARG, "%s: E4M3 weights need w_scale", who);
+    if (w_dtype == FSDP_DT_BF16 && w_scale) return fail(FSDP_E_ARG, "%s: w_scale is for E4M3 weights", who);
+    if (!aligned(w_scale, 4)) return fail(FSDP_E_ALIGN, "%s: w_scale misaligned", who);
+    return FSDP_OK;
+}
+
+int32_t check_act(int32_t act, const char* who) {
+    if (act < FSDP_ACT_NONE || act > FSDP_ACT_SILU) return fail(FSDP_E_ARG, "%s: unknown activation", who);
+    return FSDP_OK;
+}
+
+int32_t check_flag(int32_t v, const char* what, const char* who) {
+    if (v != 0 && v != 1) return fail(FSDP_E_ARG, "%s: %s must be 0 or 1", who, what);
+    return FSDP_OK;
+}
+
+int32_t check_float_dtype(int32_t d, const char* what, const char* who) {
+    if (d != FSDP_DT_F32 && d != FSDP_DT_BF16) return fail(FSDP_E_DTYPE, "%s: %s must be fp32 or bf16", who, what);
+    return FSDP_OK;
+}
+
+#define TRY(x)                                     \
+    do {                                           \
+        const int32_t st_ = (x);                   \
+        if (st_ != FSDP_OK) return st_;            \
+    } while (0)
+
+int32_t forward_impl(const fsdp_linear* a, hipStream_t stream) {
+    const char* who = "fsdp_linear_forward";
+    if (!a) return fail(FSDP_E_ARG, "%s: null argument", who);
+    if (a->reserved != 0) return fail(FSDP_E_ARG, "%s: reserved must be 0", who);
+    TRY(check_sizes(a->m, a->n, a->k, who));
+    TRY(check_weight(a->w_dtype, a->w_scale, who));
+    TRY(check_float_dtype(a->y_dtype, "y", who));
+    TRY(check_act(a->act, who));
+    TRY(check_workspace(a->workspace, a->workspace_bytes, who));
+    const int we = a->w_dtype == FSDP_DT_BF16 ? 2 : 1, ye = a->y_dtype == FSDP_DT_BF16 ? 2 : 4;
+    const Matrix x{a->x, a->m, a->k, a->ldx, 2, "x", false}, w{a->w, a->n, a->k, a->ldw, we, "w", false};
+    const Matrix y{a->y, a->m, a->n, a->ldy, ye, "y", true}, z{a->z, a->m, a->n, a->ldz, 2, "z", true};
+    const Matrix r{a->residual, a->m, a->n, a->ldr, ye, "residual", false};
+    const Matrix b = vector(a->bias, a->n, 2, "bias");
+    TRY(check_matrix(x, false, who));
+    TRY(check_matrix(w, false, who));
+    TRY(check_matrix(y, false, who));
+    TRY(check_matrix(z, true, who));
+    TRY(check_matrix(r, true, who));
+    TRY(check_matrix(b, true, who));
+    Product g{};
+    TRY(make_mask(a->dropout, &g.e.mask, who));
+    TRY(check_overlaps({y, z, workspace_of(a->workspace, a->workspace_bytes), x, w, r, b, bytes_of(a->w_scale, 4, "w_scale", false),
+                        bytes_of(g.e.mask.offset_dev, 8, "offset_dev", false)},
+                       who, [&](const Matrix& p, const Matrix& q) { return p.what == y.what && q.what == r.what; }));
+    g.a = a->x;
+    g.b = a->w;
+    g.lda = a->ldx;
+    g.ldb = a->ldw;
+    g.m = static_cast<int32_t>(a->m);
+    g.n = static_cast<int32_t>(a->n);
+    g.k = static_cast<int32_t>(a->k);
+    g.e.out = a->y;
+    g.e.ldo = a->ldy;
+    g.e.out_f32 = a->y_dtype == FSDP_DT_F32;
+    g.e.res = a->residual;
+    g.e.ldr = a->ldr;
+    g.e.z = a->z;
+    g.e.ldz = a->ldz;
+    g.e.bias = a->bias;
+    g.e.scale = a->w_scale;
+    g.e.act = a->act;
+    const bool direct = we == 2 && direct_ok(a->x, a->ldx, a->m, a->k) && direct_ok(a->w, a->ldw, a->n, a->k);
+    return run_product<true, true>(g, we == 1, direct, a->workspace, a->workspace_bytes, stream, who);
+}
+
+int32_t grad_input_impl(uint16_t* dx, int64_t lddx, const uint16_t* dz, int64_t lddz, const void* w, int64_t ldw,
+                        int32_t w_dtype, const float* w_scale, int64_t m, int64_t n, int64_t k, void* workspace,
+                        int64_t workspace_bytes, hipStream_t stream) {
+    const char* who = "fsdp_linear_grad_input";
+    TRY(check_sizes(m, n, k, who));
+    TRY(check_weight(w_dtype, w_scale, who));
+    TRY(check_workspace(workspace, workspace_bytes, who));
+    const int we = w_dtype == FSDP_DT_BF16 ? 2 : 1;
+    const Matrix x{dx, m, k, lddx, 2, "dx", true}, z{dz, m, n, lddz, 2, "dz", false}, wm{w, n, k, ldw, we, "w", false};
+    TRY(check_matrix(x, false, who));
+    TRY(check_matrix(z, false, who));
+    TRY(check_matrix(wm, false, who));
+    TRY(check_overlaps({x, workspace_of(workspace, workspace_bytes), z, wm, bytes_of(w_scale, 4, "w_scale", false)}, who,
+                       [](const Matrix&, const Matrix&) { return false; }));
+    Product g{};
+    g.a = dz;
+    g.b = w;
+    g.lda = lddz;
+    g.ldb = ldw;
+    g.m = static_cast<int32_t>(m);
+    g.n = static_cast<int32_t>(k);
+    g.k = static_cast<int32_t>(n);
+    g.e.out = dx;
+    g.e.ldo = lddx;
+    g.e.scale = w_scale;
+    g.e.mask.scale = 1.0f;
+    const bool direct = we == 2 && direct_ok(dz, lddz, m, n) && direct_ok(w, ldw, n, k);
+    return run_product<true, false>(g, we == 1, direct, workspace, workspace_bytes, stream, who);
+}
+
+int32_t grad_weight_impl(void* dw, int64_t lddw, int32_t dw_dtype, int32_t accumulate, const uint16_t* dz,
+                         int64_t lddz, const uint16_t* x, int64_t ldx, int64_t m, int64_t n, int64_t k,
+                         void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    const char* who = "fsdp_linear_grad_weight";
+    TRY(check_sizes(m, n, k, who));
+    TRY(check_float_dtype(dw_dtype, "dw", who));
+    TRY(check_flag(accumulate, "accumulate", who));
+    TRY(check_workspace(workspace, workspace_bytes, who));
+    const int we = dw_dtype == FSDP_DT_BF16 ? 2 : 4;
+    const Matrix d{dw, n, k, lddw, we, "dw", true}, z{dz, m, n, lddz, 2, "dz", false}, xm{x, m, k, ldx, 2, "x", false};
+    TRY(check_matrix(d, false, who));
+    TRY(check_matrix(z, false, who));
+    TRY(check_matrix(xm, false, who));
+    TRY(check_overlaps({d, workspace_of(workspace, workspace_bytes), z, xm}, who,
+                       [](const Matrix&, const Matrix&) { return false; }));
+    Product g{};
+    g.a = dz;
+    g.b = x;
+    g.lda = lddz;
+    g.ldb = ldx;
+    g.m = static_cast<int32_t>(n);
+    g.n = static_cast<int32_t>(k);
+    g.k = static_cast<int32_t>(m);
+    g.e.out = dw;
+    g.e.ldo = lddw;
+    g.e.out_f32 = dw_dtype == FSDP_DT_F32;
+    g.e.res = accumulate ? dw : nullptr;
+    g.e.ldr = lddw;
+    g.e.mask.scale = 1.0f;
+    const bool direct = direct_ok(dz, lddz, m, n) && direct_ok(x, ldx, m, k);
+    return run_product<false, false>(g, false, direct, workspace, workspace_bytes, stream, who);
+}
+
+// ---------------------------------------------------------------- host: elementwise passes
+
+// rows_max: the most row blocks wanted.
+Grid elementwise_grid(int64_t m, int64_t n, int64_t rows_max, int64_t* blocks) {
+    Grid g{};
+    const int64_t chunks = ceil_div(n, 8);
+    while (g.tx < 6 && (int64_t(1) << g.tx) < chunks) ++g.tx;
+    g.cblocks = static_cast<int32_t>(ceil_div(chunks, int64_t(1) << g.tx));
+    const int64_t per = kElemBlock >> g.tx;
+    g.rows = std::max<int64_t>(1, ceil_div(ceil_div(m, per), std::max<int64_t>(1, rows_max))) * per;
+    *blocks = ceil_div(m, g.rows);
+    return g;
+}
+
+int32_t epilogue_backward_impl(uint16_t* dz, int64_t lddz, void* db, int32_t db_dtype, int32_t accumulate,
+                               const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int32_t act,
+                               const fsdp_dropout_mask* dropout, int64_t m, int64_t n, void* workspace,
+                               int64_t workspace_bytes, hipStream_t stream) {
+    const char* who = "fsdp_linear_epilogue_backward";
+    TRY(check_sizes(m, n, 0, who));
+    TRY(check_act(act, who));
+    TRY(check_float_dtype(db_dtype, "db", who));
+    TRY(check_flag(accumulate, "accumulate", who));
+    TRY(check_workspace(workspace, workspace_bytes, who));
+    const int be = db_dtype == FSDP_DT_BF16 ? 2 : 4;
+    const Matrix mdz{dz, m, n, lddz, 2, "dz", true}, mdy{dy, m, n, lddy, 2, "dy", false};
+    const Matrix mz{act == FSDP_ACT_NONE ? nullptr : z, m, n, ldz, 2, "z", false}, mdb = vector(db, n, be, "db", true);
+    TRY(check_matrix(mdz, true, who));
+    TRY(check_matrix(mdy, false, who));
+    TRY(check_matrix(mz, act == FSDP_ACT_NONE, who));
+    TRY(check_matrix(mdb, true, who));
+    BackwardArgs a{};
+    TRY(make_mask(dropout, &a.mask, who));
+    TRY(check_overlaps({mdz, mdb, workspace_of(workspace, workspace_bytes), mdy, mz,
+                        bytes_of(a.mask.offset_dev, 8, "offset_dev", false)},
+                       who, [&](const Matrix& p, const Matrix& q) {
+                           return p.what == mdz.what && (q.what == mdy.what || q.what == mz.what);
+                       }));
+    if (n == 0 || (m == 0 && (!db || accumulate))) return FSDP_OK;
+    if (!dz && !db) return FSDP_OK;
+    a.dz = dz;
+    a.dy = dy;
+    a.z = z;
+    a.lddz = lddz;
+    a.lddy = lddy;
+    a.ldz = ldz;
+    a.m = m;
+    a.n = n;
+    a.db = db;
+    a.db_f32 = db_dtype == FSDP_DT_F32;
+    a.accumulate = accumulate;
+    a.act = act;
+    a.sums = db != nullptr;
+    const int64_t cblocks = ceil_div(ceil_div(n, 8), 64);
+    int64_t want = ceil_div(8 * kCus, cblocks);
+    if (db) want = std::min(want, std::min(workspace_bytes, FSDP_LINEAR_WORKSPACE_BYTES) / (4 * n));
+    int64_t blocks;
+    a.g = elementwise_grid(m, n, std::max<int64_t>(1, want), &blocks);
+    if (m == 0) blocks = 1;  // db = 0
+    a.part = db && blocks > 1 ? static_cast<float*>(workspace) : nullptr;
+    if (blocks * a.g.cblocks > 0x7fffff) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
+    epilogue_backward_kernel<<<dim3(static_cast<uint32_t>(blocks * a.g.cblocks)), dim3(kElemBlock), 0, stream>>>(a);
+    TRY(launched(who));
+    if (!a.part) return FSDP_OK;
+    column_sum_kernel<<<dim3(static_cast<uint32_t>(ceil_div(n, 64))), dim3(kElemBlock), 0, stream>>>(
+        a.part, n, static_cast<int32_t>(blocks), db, a.db_f32, accumulate);
+    return launched(who);
+}
+
+int32_t dropout_impl(void* y, int64_t ldy, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                     int32_t dtype, int64_t rows, int64_t cols, const fsdp_dropout_mask* mask, hipStream_t stream) {
+    const char* who = "fsdp_dropout";
+    TRY(check_sizes(rows, cols, 0, who));
+    TRY(check_float_dtype(dtype, "dtype", who));
+    if (!mask) return fail(FSDP_E_ARG, "%s: null mask", who);
+    const int e = dtype == FSDP_DT_BF16 ? 2 : 4;
+    const Matrix my{y, rows, cols, ldy, e, "y", true}, mx{x, rows, cols, ldx, e, "x", false};
+    const Matrix mr{residual, rows, cols, ldr, e, "residual", false};
+    TRY(check_matrix(my, false, who));
+    TRY(check_matrix(mx, false, who));
+    TRY(check_matrix(mr, true, who));
+    DropoutArgs a{};
+    TRY(make_mask(mask, &a.mask, who));
+    TRY(check_overlaps({my, mx, mr, bytes_of(a.mask.offset_dev, 8, "offset_dev", false)}, who,
+                       [&](const Matrix&, const Matrix& q) { return q.what == mx.what || q.what == mr.what; }));
+    if (rows == 0 || cols == 0) return FSDP_OK;
+    a.y = y;
+    a.x = x;
+    a.res = residual;
+    a.ldy = ldy;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.m = rows;
+    a.n = cols;
+    int64_t blocks;
+    a.g = elementwise_grid(rows, cols, ceil_div(16 * kCus, ceil_div(ceil_div(cols, 8), 64)), &blocks);
+    if (blocks * a.g.cblocks > 0x7fffff) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
+    const dim3 grid(static_cast<uint32_t>(blocks * a.g.cblocks));
+    if (e == 2) dropout_kernel<uint16_t><<<grid, dim3(kElemBlock), 0, stream>>>(a);
+    else dropout_kernel<float><<<grid, dim3(kElemBlock), 0, stream>>>(a);
+    return launched(who);
+}
+
+#undef TRY
+
+}  // namespace
+
+// ---------------------------------------------------------------- entry points
+
+extern "C" int32_t fsdp_linear_forward(const fsdp_linear* a, hipStream_t stream) {
+    return fsdp::guarded("fsdp_linear_forward", [&] { return forward_impl(a, stream); });
+}
+
+extern "C" int32_t fsdp_linear_epilogue_backward(uint16_t* dz, int64_t lddz, void* db, int32_t db_dtype,
+                                                 int32_t accumulate, const uint16_t* dy, int64_t lddy,
+                                                 const uint16_t* z, int64_t ldz, int32_t act,
+                                                 const fsdp_dropout_mask* dropout, int64_t m, int64_t n,
+                                                 void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    return fsdp::guarded("fsdp_linear_epilogue_backward", [&] {
+        return epilogue_backward_impl(dz, lddz, db, db_dtype, accumulate, dy, lddy, z, ldz, act, dropout, m, n,
+                                      workspace, workspace_bytes, stream);
+    });
+}
+
+extern "C" int32_t fsdp_linear_grad_input(uint16_t* dx, int64_t lddx, const uint16_t* dz, int64_t lddz, const void* w,
+                                          int64_t ldw, int32_t w_dtype, const float* w_scale, int64_t m, int64_t n,
+                                          int64_t k, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    return fsdp::guarded("fsdp_linear_grad_input", [&] {
+        return grad_input_impl(dx, lddx, dz, lddz, w, ldw, w_dtype, w_scale, m, n, k, workspace, workspace_bytes,
+                               stream);
+    });
+}
+
+extern "C" int32_t fsdp_linear_grad_weight(void* dw, int64_t lddw, int32_t dw_dtype, int32_t accumulate,
+                                           const uint16_t* dz, int64_t lddz, const uint16_t* x, int64_t ldx,
+                                           int64_t m, int64_t n, int64_t k, void* workspace, int64_t workspace_bytes,
+                                           hipStream_t stream) {
+    return fsdp::guarded("fsdp_linear_grad_weight", [&] {
+        return grad_weight_impl(dw, lddw, dw_dtype, accumulate, dz, lddz, x, ldx, m, n, k, workspace, workspace_bytes,
+                                stream);
+    });
+}
+
+extern "C" int32_t fsdp_dropout(void* y, int64_t ldy, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                int32_t dtype, int64_t rows, int64_t cols, const fsdp_dropout_mask* mask,
+                                hipStream_t stream) {
+    return fsdp::guarded("fsdp_dropout",
+                         [&] { return dropout_impl(y, ldy, x, ldx, residual, ldr, dtype, rows, cols, mask, stream); });
+}

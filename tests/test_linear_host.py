@@ -1,0 +1,199 @@
+"""The linear layer's calls refuse what they cannot do (CPU only): every bad
+argument comes back with its code before any device work.  The cases carry
+device addresses that are never touched."""
+
+import ctypes
+
+import pytest
+
+from rank_step_amd import binding as B
+
+X, W, Y, Z, R, DZ, DB, WS = (0x10000000 * i for i in range(1, 9))
+S = 0  # the null stream, never used
+
+
+def forward(**kw):
+    a = dict(y=Y, x=X, w=W, m=4, n=8, k=16, stream=S)
+    a.update(kw)
+    B.fsdp_linear_forward(**a)
+
+
+def backward(**kw):
+    a = dict(dz=DZ, dy=Y, m=4, n=8, z=Z, act="gelu", db=DB, stream=S)
+    a.update(kw)
+    B.fsdp_linear_epilogue_backward(**a)
+
+
+def grad_input(**kw):
+    a = dict(dx=X, dz=DZ, w=W, m=4, n=8, k=16, stream=S)
+    a.update(kw)
+    B.fsdp_linear_grad_input(**a)
+
+
+def grad_weight(**kw):
+    a = dict(dw=W, dz=DZ, x=X, m=4, n=8, k=16, stream=S)
+    a.update(kw)
+    B.fsdp_linear_grad_weight(**a)
+
+
+def dropout(**kw):
+    a = dict(y=Y, x=X, rows=4, cols=8, dtype="bf16", dropout={"p": 0.5, "seed": 1, "offset": 2}, stream=S)
+    a.update(kw)
+    B.fsdp_dropout(**a)
+
+
+P = {"p": 0.5, "seed": 1, "offset": 2}
+
+
+class Space:
+    """A workspace as the binding takes it: an address and a size."""
+
+    def __init__(self, ptr, size):
+        self.ptr, self.size = ptr, size
+
+    def data_ptr(self):
+        return self.ptr
+
+    def numel(self):
+        return self.size
+
+    def element_size(self):
+        return 1
+
+
+BAD = [
+    (forward, dict(x=None), "FSDP_E_ARG"),
+    (forward, dict(w=None), "FSDP_E_ARG"),
+    (forward, dict(y=None), "FSDP_E_ARG"),
+    (forward, dict(m=-1), "FSDP_E_ARG"),
+    (forward, dict(k=-1), "FSDP_E_ARG"),
+    (forward, dict(ldx=15), "FSDP_E_ARG"),
+    (forward, dict(ldw=15), "FSDP_E_ARG"),
+    (forward, dict(ldy=7), "FSDP_E_ARG"),
+    (forward, dict(z=Z, ldz=7), "FSDP_E_ARG"),
+    (forward, dict(residual=R, ldr=7), "FSDP_E_ARG"),
+    (forward, dict(m=(1 << 30) + 1), "FSDP_E_CAPACITY"),
+    (forward, dict(n=1 << 31), "FSDP_E_CAPACITY"),
+    (forward, dict(ldx=1 << 62), "FSDP_E_ARG"),
+    (forward, dict(w_dtype=0), "FSDP_E_DTYPE"),
+    (forward, dict(w_dtype=3), "FSDP_E_DTYPE"),
+    (forward, dict(y_dtype=2), "FSDP_E_DTYPE"),
+    (forward, dict(w_dtype="e4m3"), "FSDP_E_ARG"),
+    (forward, dict(w_scale=R), "FSDP_E_ARG"),
+    (forward, dict(w_dtype="e4m3", w_scale=R + 2), "FSDP_E_ALIGN"),
+    (forward, dict(act=4), "FSDP_E_ARG"),
+    (forward, dict(act=-1), "FSDP_E_ARG"),
+    (forward, dict(x=X + 1), "FSDP_E_ALIGN"),
+    (forward, dict(y=Y + 2, y_dtype="f32"), "FSDP_E_ALIGN"),
+    (forward, dict(bias=R + 1), "FSDP_E_ALIGN"),
+    (forward, dict(residual=R + 2, y_dtype="f32"), "FSDP_E_ALIGN"),
+    (forward, dict(workspace=Space(WS + 8, 64)), "FSDP_E_ALIGN"),
+    (forward, dict(workspace=Space(0, 64)), "FSDP_E_ARG"),
+    (forward, dict(workspace=Space(WS, -1)), "FSDP_E_ARG"),
+    (forward, dict(dropout={**P, "p": 1.5}), "FSDP_E_ARG"),
+    (forward, dict(dropout={**P, "p": -0.1}), "FSDP_E_ARG"),
+    (forward, dict(dropout={**P, "p": float("nan")}), "FSDP_E_ARG"),
+    (forward, dict(dropout={**P, "offset_dev": R + 4}), "FSDP_E_ALIGN"),
+    (forward, dict(y=X), "FSDP_E_ALIAS"),
+    (forward, dict(y=X + 4 * 16 * 2 - 2), "FSDP_E_ALIAS"),
+    (forward, dict(y=W + 16), "FSDP_E_ALIAS"),
+    (forward, dict(z=Y), "FSDP_E_ALIAS"),
+    (forward, dict(z=X), "FSDP_E_ALIAS"),
+    (forward, dict(bias=Y + 6), "FSDP_E_ALIAS"),
+    (forward, dict(residual=Y + 2), "FSDP_E_ALIAS"),
+    (forward, dict(residual=Y, ldr=9), "FSDP_E_ALIAS"),
+    (forward, dict(residual=Z, z=Z), "FSDP_E_ALIAS"),
+    (forward, dict(workspace=Space(Y, 1 << 20)), "FSDP_E_ALIAS"),
+    (forward, dict(workspace=Space(X - 1024, 1 << 20)), "FSDP_E_ALIAS"),
+    (forward, dict(w_dtype="e4m3", w_scale=Y + 4), "FSDP_E_ALIAS"),
+    (forward, dict(dropout={**P, "offset_dev": Y + 8}), "FSDP_E_ALIAS"),
+    # columns of one row stride: y takes [8, 16) and x [0, 16) of rows of 32
+    (forward, dict(ldx=32, y=X + 16, ldy=32), "FSDP_E_ALIAS"),
+    (forward, dict(ldx=32, y=X + 64 - 14, ldy=32), "FSDP_E_ALIAS"),
+    (backward, dict(dy=None), "FSDP_E_ARG"),
+    (backward, dict(z=None), "FSDP_E_ARG"),
+    (backward, dict(n=-1), "FSDP_E_ARG"),
+    (backward, dict(act=9), "FSDP_E_ARG"),
+    (backward, dict(db_dtype=2), "FSDP_E_DTYPE"),
+    (backward, dict(accumulate=2), "FSDP_E_ARG"),
+    (backward, dict(db=DB + 2), "FSDP_E_ALIGN"),
+    (backward, dict(lddz=7), "FSDP_E_ARG"),
+    (backward, dict(dz=Y + 2), "FSDP_E_ALIAS"),
+    (backward, dict(dz=Y, lddz=9), "FSDP_E_ALIAS"),
+    (backward, dict(db=Y), "FSDP_E_ALIAS"),
+    (backward, dict(db=DZ + 16), "FSDP_E_ALIAS"),
+    (backward, dict(workspace=Space(DZ, 64)), "FSDP_E_ALIAS"),
+    (backward, dict(dropout={**P, "p": 2}), "FSDP_E_ARG"),
+    (backward, dict(dropout={**P, "offset_dev": DZ}), "FSDP_E_ALIAS"),
+    (grad_input, dict(dx=None), "FSDP_E_ARG"),
+    (grad_input, dict(dz=None), "FSDP_E_ARG"),
+    (grad_input, dict(w=None), "FSDP_E_ARG"),
+    (grad_input, dict(lddx=15), "FSDP_E_ARG"),
+    (grad_input, dict(w_dtype="e4m3"), "FSDP_E_ARG"),
+    (grad_input, dict(w_dtype=0), "FSDP_E_DTYPE"),
+    (grad_input, dict(dx=DZ), "FSDP_E_ALIAS"),
+    (grad_input, dict(dx=W), "FSDP_E_ALIAS"),
+    (grad_input, dict(workspace=Space(DZ, 1 << 20)), "FSDP_E_ALIAS"),
+    (grad_input, dict(k=(1 << 30) + 1), "FSDP_E_CAPACITY"),
+    (grad_weight, dict(dw=None), "FSDP_E_ARG"),
+    (grad_weight, dict(x=None), "FSDP_E_ARG"),
+    (grad_weight, dict(dw_dtype=2), "FSDP_E_DTYPE"),
+    (grad_weight, dict(accumulate=-1), "FSDP_E_ARG"),
+    (grad_weight, dict(dw=W + 2, dw_dtype="f32"), "FSDP_E_ALIGN"),
+    (grad_weight, dict(dw=X), "FSDP_E_ALIAS"),
+    (grad_weight, dict(lddz=7), "FSDP_E_ARG"),
+    (dropout, dict(x=None), "FSDP_E_ARG"),
+    (dropout, dict(y=None), "FSDP_E_ARG"),
+    (dropout, dict(dropout=None), "FSDP_E_ARG"),
+    (dropout, dict(dtype=2), "FSDP_E_DTYPE"),
+    (dropout, dict(dtype="f32", x=X + 2), "FSDP_E_ALIGN"),
+    (dropout, dict(y=X + 2), "FSDP_E_ALIAS"),
+    (dropout, dict(y=X, ldy=9), "FSDP_E_ALIAS"),
+    (dropout, dict(residual=Y + 4), "FSDP_E_ALIAS"),
+    (dropout, dict(ldx=7), "FSDP_E_ARG"),
+    (dropout, dict(rows=-1), "FSDP_E_ARG"),
+    (dropout, dict(dropout={**P, "offset_dev": Y}), "FSDP_E_ALIAS"),
+]
+
+
+@pytest.mark.parametrize("call,kw,code", BAD)
+def test_refusals(call, kw, code):
+    with pytest.raises(B.FsdpError) as e:
+        call(**kw)
+    assert e.value.name == code, str(e.value)
+
+
+def test_reserved_and_null_record():
+    L = B.lib()
+    assert L.fsdp_linear_forward(None, None) == -1
+    a = B.Linear(4, 8, 16, X, 16, W, 16, None, None, None, 8, Y, 8, None, 8, None, None, 0, 1, 1, 0, 1)
+    assert L.fsdp_linear_forward(ctypes.byref(a), None) == -1
+    assert b"reserved" in L.fsdp_last_error()
+
+
+def test_empty_outputs_are_no_ops():
+    """Nothing is queued (there is no device here to queue on), null or not."""
+    forward(m=0, x=None, y=None)
+    forward(n=0, w=None, y=None)
+    grad_input(m=0, dx=None, dz=None)
+    grad_input(k=0, dx=None, w=None)
+    grad_weight(n=0, dw=None, dz=None)
+    grad_weight(k=0, dw=None, x=None)
+    backward(n=0, dz=None, dy=None, z=None, db=None)
+    backward(m=0, dz=None, dy=None, z=None, db=None)
+    backward(m=0, dz=None, dy=None, z=None, accumulate=True)
+    backward(dz=None, db=None)
+    dropout(rows=0, x=None, y=None)
+    dropout(cols=0, x=None, y=None)
+
+
+def test_exports_and_constants():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "fsdp_linear.h")).read()
+    assert re.search(r"FSDP_LINEAR_WORKSPACE_BYTES \(\(int64_t\)64 << 20\)", text)
+    assert B.LINEAR_WORKSPACE_BYTES == 64 << 20
+    for name, value in B.ACTIVATIONS.items():
+        assert re.search(r"FSDP_ACT_%s = %d\b" % (name.upper(), value), text), name
+    assert B.WEIGHT_DTYPES["e4m3"] == int(re.search(r"FSDP_DT_E4M3 = (\d+)", text).group(1))
