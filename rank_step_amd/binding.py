@@ -15,6 +15,7 @@ current device so that the work is ordered with torch's own.
 
 import ctypes
 import os
+import struct
 import threading
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librank_step.so")
@@ -163,12 +164,12 @@ def lib():
             "fsdp_mt_reduce_accumulate": [vp, i32, vp, vp],
             "fsdp_grad_accumulate": [vp, vp, i32, i64, i32, vp],
             "fsdp_reduce_sqnorm_noalloc": [vp, vp, vp, i32, i64, i32, i64, i64, vp],
-            "fsdp_linear_forward": [ctypes.POINTER(Linear), vp],
+            "fsdp_linear_forward": [vp, vp],
             "fsdp_linear_epilogue_backward": [vp, i64, vp, i32, i32, vp, i64, vp, i64, i32,
-                                              ctypes.POINTER(DropoutMask), i64, i64, vp, i64, vp],
+                                              vp, i64, i64, vp, i64, vp],
             "fsdp_linear_grad_input": [vp, i64, vp, i64, vp, i64, i32, vp, i64, i64, i64, vp, i64, vp],
             "fsdp_linear_grad_weight": [vp, i64, i32, i32, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp],
-            "fsdp_dropout": [vp, i64, vp, i64, vp, i64, i32, i64, i64, ctypes.POINTER(DropoutMask), vp],
+            "fsdp_dropout": [vp, i64, vp, i64, vp, i64, i32, i64, i64, vp, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -375,13 +376,20 @@ def fsdp_reduce_sqnorm_noalloc(grad_shard_out, sqnorm_out, grad_slices, slice_dt
 # Row strides (ld*) default to the row's length.  ``dropout``: None or a dict
 # with p, seed and offset, and optionally offset_dev (a device int64 [1]).
 # ``workspace``: None or a device tensor, all of which the call may use.
+#
+# The records go to the library as packed bytes: a small call's time is mostly
+# the host's, and a packed record takes a fifth of a ctypes structure's.
+
+_M64 = (1 << 64) - 1
+_MASK = struct.Struct("=dQQQ")
+_LINEAR = struct.Struct("=3q" + "Qq" + "QqQ" + "Q" + "Qq" + "Qq" + "Qq" + "Q" + "Qq" + "4i")
+assert _MASK.size == ctypes.sizeof(DropoutMask) and _LINEAR.size == ctypes.sizeof(Linear)
+
 
 def _mask(d):
     if d is None:
         return None
-    m64 = (1 << 64) - 1
-    return ctypes.pointer(DropoutMask(float(d["p"]), d["seed"] & m64, d["offset"] & m64,
-                                      _ptr(d.get("offset_dev"))))
+    return _MASK.pack(d["p"], d["seed"] & _M64, d["offset"] & _M64, _ptr(d.get("offset_dev")) or 0)
 
 
 def _workspace(w):
@@ -389,27 +397,28 @@ def _workspace(w):
 
 
 def _ld(ld, cols):
-    return cols if ld is None else int(ld)
+    return cols if ld is None else ld
 
 
 def fsdp_linear_forward(y, x, w, m, n, k, w_dtype="bf16", w_scale=None, y_dtype="bf16", bias=None,
                         residual=None, act="none", z=None, dropout=None, workspace=None, ldy=None,
                         ldx=None, ldw=None, ldr=None, ldz=None, stream=None):
     """z = x W^T + bias; y = dropout(act(z)) + residual."""
-    m, n, k = int(m), int(n), int(k)
     ws, ws_bytes = _workspace(workspace)
-    a = Linear(m, n, k, _ptr(x), _ld(ldx, k), _ptr(w), _ld(ldw, k), _ptr(w_scale), _ptr(bias),
-               _ptr(residual), _ld(ldr, n), _ptr(y), _ld(ldy, n), _ptr(z), _ld(ldz, n), _mask(dropout), ws, ws_bytes,
-               WEIGHT_DTYPES.get(w_dtype, w_dtype), DTYPES.get(y_dtype, y_dtype),
-               ACTIVATIONS.get(act, act), 0)
-    _check(lib().fsdp_linear_forward(ctypes.byref(a), _stream(stream)))
+    mask = None if dropout is None else ctypes.create_string_buffer(_mask(dropout), _MASK.size)
+    a = _LINEAR.pack(m, n, k, _ptr(x) or 0, k if ldx is None else ldx, _ptr(w) or 0, k if ldw is None else ldw,
+                     _ptr(w_scale) or 0, _ptr(bias) or 0, _ptr(residual) or 0, n if ldr is None else ldr,
+                     _ptr(y) or 0, n if ldy is None else ldy, _ptr(z) or 0, n if ldz is None else ldz,
+                     0 if mask is None else ctypes.addressof(mask), ws or 0, ws_bytes,
+                     WEIGHT_DTYPES.get(w_dtype, w_dtype), DTYPES.get(y_dtype, y_dtype),
+                     ACTIVATIONS.get(act, act), 0)
+    _check(lib().fsdp_linear_forward(a, _stream(stream)))
 
 
 def fsdp_linear_epilogue_backward(dz, dy, m, n, z=None, act="none", dropout=None, db=None, db_dtype="f32",
                                   accumulate=False, workspace=None, lddz=None, lddy=None, ldz=None,
                                   stream=None):
     """dz = dropout(dy) act'(z), and db = its column sums."""
-    m, n = int(m), int(n)
     ws, ws_bytes = _workspace(workspace)
     _check(lib().fsdp_linear_epilogue_backward(
         _ptr(dz), _ld(lddz, n), _ptr(db), DTYPES.get(db_dtype, db_dtype), int(accumulate), _ptr(dy),
@@ -420,7 +429,6 @@ def fsdp_linear_epilogue_backward(dz, dy, m, n, z=None, act="none", dropout=None
 def fsdp_linear_grad_input(dx, dz, w, m, n, k, w_dtype="bf16", w_scale=None, workspace=None, lddx=None,
                            lddz=None, ldw=None, stream=None):
     """dx = dz W."""
-    m, n, k = int(m), int(n), int(k)
     ws, ws_bytes = _workspace(workspace)
     _check(lib().fsdp_linear_grad_input(_ptr(dx), _ld(lddx, k), _ptr(dz), _ld(lddz, n), _ptr(w), _ld(ldw, k),
                                         WEIGHT_DTYPES.get(w_dtype, w_dtype), _ptr(w_scale), m, n, k, ws,
@@ -430,7 +438,6 @@ def fsdp_linear_grad_input(dx, dz, w, m, n, k, w_dtype="bf16", w_scale=None, wor
 def fsdp_linear_grad_weight(dw, dz, x, m, n, k, dw_dtype="bf16", accumulate=False, workspace=None, lddw=None,
                             lddz=None, ldx=None, stream=None):
     """dW = dz^T x, stored or added to what dw holds."""
-    m, n, k = int(m), int(n), int(k)
     ws, ws_bytes = _workspace(workspace)
     _check(lib().fsdp_linear_grad_weight(_ptr(dw), _ld(lddw, k), DTYPES.get(dw_dtype, dw_dtype), int(accumulate),
                                          _ptr(dz), _ld(lddz, n), _ptr(x), _ld(ldx, k), m, n, k, ws, ws_bytes,
@@ -439,9 +446,8 @@ def fsdp_linear_grad_weight(dw, dz, x, m, n, k, dw_dtype="bf16", accumulate=Fals
 
 def fsdp_dropout(y, x, rows, cols, dtype, dropout, residual=None, ldy=None, ldx=None, ldr=None, stream=None):
     """y = dropout(x) + residual; with dy for x and no residual, its gradient."""
-    cols = int(cols)
     _check(lib().fsdp_dropout(_ptr(y), _ld(ldy, cols), _ptr(x), _ld(ldx, cols), _ptr(residual), _ld(ldr, cols),
-                              _dtype(dtype), int(rows), cols, _mask(dropout), _stream(stream)))
+                              DTYPES.get(dtype, dtype), rows, cols, _mask(dropout), _stream(stream)))
 
 
 class MtPlan:

@@ -22,7 +22,7 @@
 
 #include <algorithm>
 #include <cmath>
-#include <vector>
+#include <initializer_list>
 
 #include "fsdp_linear.h"
 #include "internal.h"
@@ -375,18 +375,23 @@ struct DirectTile {
         }
     }
 
-    // Issues the tile's loads; lleft: contraction elements left from here on.
-    __device__ __forceinline__ void load(Lds* dst, int wave, int lleft) {
+    // Issues part i of n of the tile's loads; lleft: contraction elements left
+    // from here on (none: every load is out of range, touches no memory and
+    // gives zeros).
+    __device__ __forceinline__ void load(Lds* dst, int wave, int lleft, int i, int n) {
         const uint32_t range = static_cast<uint32_t>(left < 0 ? 0 : min(left, static_cast<int64_t>(0x7fffffff)));
         const __amdgpu_buffer_rsrc_t rsrc =
             __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(range), 0x00020000);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            uint32_t o = off[i];
+        for (int q = i * kLoads / n; q < (i + 1) * kLoads / n; ++q) {
+            uint32_t o = off[q];
             if (LMAJOR) o = chunk * 8 < lleft ? o : kOutside;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (__attribute__((address_space(3))) void*)(dst + (i * THREADS + wave * 64) * 16), 16, o, 0, 0, 0);
+                rsrc, (__attribute__((address_space(3))) void*)(dst + (q * THREADS + wave * 64) * 16), 16, o, 0, 0, 0);
         }
+    }
+
+    __device__ __forceinline__ void advance() {
         base += step;
         left -= step;
     }
@@ -402,7 +407,7 @@ struct StagedTile {
     int o0, no, nl, tid;
     u32x4 reg[kLoads];
 
-    __device__ __forceinline__ void init(const void* ptr, int64_t ld_, int o0_, int no_, int, int nl_, int tid_) {
+    __device__ __forceinline__ void init(const void* ptr, int64_t ld_, int o0_, int no_, int tid_, int nl_) {
         p = static_cast<const uint8_t*>(ptr);
         ld = ld_;
         o0 = o0_;
@@ -511,6 +516,37 @@ struct Fragments {
     }
 };
 
+// acc += the 16x16 product of two fragments.  Written as assembly for its
+// register classes: accumulators in AGPRs, operands in VGPRs.  Left to choose,
+// the compiler mixes the two for 256 accumulators a lane and moves them about
+// between the products.  What it then cannot see is the wait of a few cycles
+// between a product and another unit's read or write of its accumulator:
+// settle() stands where accumulators change hands, before the first product
+// and after the last, and names them all, so that neither their zeros nor
+// their uses can move across it.
+__device__ __forceinline__ void mfma(f32x4& acc, const bf16x8& b, const bf16x8& a) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+template <int FI, int FJ>
+__device__ __forceinline__ void settle(f32x4 (&acc)[FI][FJ]) {
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+// Everything this wave has asked of memory and LDS has come, in every wave.
+__device__ __forceinline__ void arrive() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // BM x BN output tile by WI x WJ waves, two LDS stages of kBK contraction
 // elements: while one is multiplied the next arrives.
 template <int BM, int BN, int WI, int WJ, bool AL, bool BL, bool DIRECT, bool FP8>
@@ -545,80 +581,97 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
     fa.init(wi * kWM, lane);
     fb.init(wj * kWN, lane);
 
-    auto multiply = [&](const Lds* stage) {
+    // A step multiplies one LDS stage in two halves of 32 contraction elements.
+    // Each half's fragments are read from LDS while the half before is being
+    // multiplied, and a stage is refilled as soon as its second half has been
+    // read, a whole step ahead of its use; so the one barrier of a step, in
+    // its middle, finds everything that it waits for already there.
+    bf16x8 a[2][kFI], b[2][kFJ];
+    // Fragment f of a half, in the order in which multiplying needs them.
+    auto read = [&](const Lds* stage, int kk, int f) {
+        if (f < kFJ) b[kk][f] = fb.get(stage + BM * kBK * 2, f, kk);
+        else a[kk][f - kFJ] = fa.get(stage, f - kFJ, kk);
+    };
+    // Half kk row by row, the reads of the other half (of `stage`) and the
+    // refill's loads placed between the rows: 3 fragments a row, so that the
+    // last rows leave them time to come.
+    auto multiply = [&](int kk, const Lds* stage, auto&& between) {
+        constexpr int kReads = kFI == 8 ? 3 : (kFI + kFJ) / kFI + 1;
 #pragma unroll
-        for (int kk = 0; kk < kBK / 32; ++kk) {
-            bf16x8 a[kFI], b[kFJ];
+        for (int i = 0; i < kFI; ++i) {
 #pragma unroll
-            for (int j = 0; j < kFJ; ++j) b[j] = fb.get(stage + BM * kBK * 2, j, kk);
+            for (int f = i * kReads; f < (i + 1) * kReads && f < kFI + kFJ; ++f) read(stage, 1 - kk, f);
+            between(i);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < kFI; ++i) a[i] = fa.get(stage, i, kk);
-#pragma unroll
-            for (int i = 0; i < kFI; ++i)
-#pragma unroll
-                for (int j = 0; j < kFJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < kFJ; ++j) mfma(acc[i][j], b[kk][j], a[kk][i]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-
-    if constexpr (DIRECT) {
-        DirectTile<BM, kThreads, AL> ta;
-        DirectTile<BN, kThreads, BL> tb;
-        ta.init(g.a, g.lda, i0, g.m, kbeg, AL ? g.k : kend, tid);
-        tb.init(g.b, g.ldb, j0, g.n, kbeg, BL ? g.k : kend, tid);
-        int lleft = kend - kbeg;
-        auto fetch = [&](Lds* stage) {
-            ta.load(stage, wave, lleft);
-            tb.load(stage + BM * kBK * 2, wave, lleft);
-            lleft -= kBK;
+    // refill(stage, i, n): part i of n of the loads that fill a stage.
+    auto run = [&](auto&& refill) {
+        auto step = [&](Lds* cur, Lds* nxt) {
+            multiply(0, cur, [](int) {});
+            arrive();
+            multiply(1, nxt, [&](int i) { refill(cur, i, kFI); });
         };
-        // One step: this stage's loads have arrived in every wave, and every
-        // wave is done with the other stage, which the next loads then fill.
-        auto step = [&](int s, Lds* cur, Lds* nxt) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-            if (s + 1 < steps) fetch(nxt);
-            multiply(cur);
-        };
-        if (steps > 0) fetch(l0);
-        int s = 0;
-        for (; s + 1 < steps; s += 2) {
-            step(s, l0, l1);
-            step(s + 1, l1, l0);
+        arrive();
+        settle(acc);
+#pragma unroll
+        for (int f = 0; f < kFI + kFJ; ++f) read(l0, 0, f);
+        // Two steps a turn, so that each LDS access names its stage.  An odd
+        // count takes one more step, over zeros.
+        int turns = (steps + 1) / 2;
+        do {
+            step(l0, l1);
+            step(l1, l0);
+        } while (--turns > 0);
+    };
+    if (steps > 0) {
+        if constexpr (DIRECT) {
+            DirectTile<BM, kThreads, AL> ta;
+            DirectTile<BN, kThreads, BL> tb;
+            ta.init(g.a, g.lda, i0, g.m, kbeg, AL ? g.k : kend, tid);
+            tb.init(g.b, g.ldb, j0, g.n, kbeg, BL ? g.k : kend, tid);
+            int lleft = kend - kbeg;
+            auto fetch = [&](Lds* stage, int i, int n) {
+                ta.load(stage, wave, lleft, i, n);
+                tb.load(stage + BM * kBK * 2, wave, lleft, i, n);
+                if (i == n - 1) {
+                    ta.advance();
+                    tb.advance();
+                    lleft -= kBK;
+                }
+            };
+            fetch(l0, 0, 1);
+            fetch(l1, 0, 1);
+            run(fetch);
+        } else {
+            StagedTile<BM, kThreads, AL, false> ta;
+            StagedTile<BN, kThreads, BL, FP8> tb;
+            ta.init(g.a, g.lda, i0, g.m, tid, kend);
+            tb.init(g.b, g.ldb, j0, g.n, tid, kend);
+            int l = kbeg;
+            auto fetch = [&] {
+                ta.load(l);
+                tb.load(l);
+                l += kBK;
+            };
+            auto store = [&](Lds* stage) {
+                ta.store(stage);
+                tb.store(stage + BM * kBK * 2);
+                fetch();
+            };
+            fetch();
+            store(l0);
+            store(l1);
+            run([&](Lds* stage, int i, int) {
+                if (i == 0) store(stage);
+            });
         }
-        if (s < steps) step(s, l0, l1);
-    } else {
-        StagedTile<BM, kThreads, AL, false> ta;
-        StagedTile<BN, kThreads, BL, FP8> tb;
-        ta.init(g.a, g.lda, i0, g.m, kbeg, kend, tid);
-        tb.init(g.b, g.ldb, j0, g.n, kbeg, kend, tid);
-        auto step = [&](int s, Lds* cur, Lds* nxt) {
-            __syncthreads();
-            const bool more = s + 1 < steps;
-            if (more) {
-                ta.load(kbeg + (s + 1) * kBK);
-                tb.load(kbeg + (s + 1) * kBK);
-            }
-            multiply(cur);
-            if (more) {
-                ta.store(nxt);
-                tb.store(nxt + BM * kBK * 2);
-            }
-        };
-        if (steps > 0) {
-            ta.load(kbeg);
-            tb.load(kbeg);
-            ta.store(l0);
-            tb.store(l0 + BM * kBK * 2);
-        }
-        int s = 0;
-        for (; s + 1 < steps; s += 2) {
-            step(s, l0, l1);
-            step(s + 1, l1, l0);
-        }
-        if (s < steps) step(s, l0, l1);
     }
 
+    settle(acc);
     // Lane l holds of each 16x16 block output row l mod 16 and columns
     // 4 (l / 16) + 0..3.
     const int lo = lane & 15, hi = lane >> 4;
@@ -636,30 +689,30 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
         }
         return;
     }
-    // 64 rows at a time through the wave's own 16 KB of LDS, so that a lane has
+    // 64 rows at a time through the wave's own piece of LDS, so that a lane has
     // 8 consecutive columns: one 16-byte store and one mask block.  A row's
     // 16-byte chunks are permuted by the row, which spreads the 16 rows that
     // one write touches over the banks.
-    __syncthreads();  // the last stage is being read until here
-    static_assert(kWN == 64 && kWM % 64 == 0 && kStage == WI * WJ / 2 * 16384, "a piece of 64 x 64 floats a wave");
-    constexpr int kHalf = WI * WJ / 2;
-    Lds* const piece = (wave < kHalf ? l0 : l1) + wave % kHalf * 16384;
+    arrive();  // the last stages are being read and filled until here
+    constexpr int kHalf = WI * WJ / 2, kPiece = 64 * kWN * 4, kLanes = kWN / 8;
+    static_assert(kWM % 64 == 0 && kWN >= 64 && kHalf * kPiece <= kStage, "a piece of 64 x kWN floats a wave");
+    Lds* const piece = (wave < kHalf ? l0 : l1) + wave % kHalf * kPiece;
     using Quad = __attribute__((address_space(3))) f32x4;
     const float recip = g.e.scale ? 1.0f / *g.e.scale : 1.0f;
     const uint64_t off = mask_offset(g.e.mask);
-    const int c = lane & 7, col = j0 + wj * kWN + c * 8;
+    const int c = lane % kLanes, col = j0 + wj * kWN + c * 8;
 #pragma unroll
     for (int h = 0; h < kWM / 64; ++h) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < kFJ; ++j)
-                *(Quad*)(piece + (i * 16 + lo) * 256 + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
+                *(Quad*)(piece + (i * 16 + lo) * (kWN * 4) + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-        for (int r = lane >> 3; r < 64; r += 8) {
-            const f32x4 x = *(const Quad*)(piece + r * 256 + (((c * 2) ^ (r & 15)) << 4));
-            const f32x4 y = *(const Quad*)(piece + r * 256 + (((c * 2 + 1) ^ (r & 15)) << 4));
+        for (int r = lane / kLanes; r < 64; r += 64 / kLanes) {
+            const f32x4 x = *(const Quad*)(piece + r * (kWN * 4) + (((c * 2) ^ (r & 15)) << 4));
+            const f32x4 y = *(const Quad*)(piece + r * (kWN * 4) + (((c * 2 + 1) ^ (r & 15)) << 4));
             float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
             const int row = i0 + wi * kWM + h * 64 + r;
             if (row < g.m && col < g.n) epilogue8(g.e, row, col, g.n - col, g.n, recip, off, v);
@@ -855,10 +908,10 @@ bool same(const Matrix& a, const Matrix& b) { return a.p == b.p && a.ld == b.ld 
 
 // twin(a, b): whether written a may be b itself
 template <typename F>
-int32_t check_overlaps(const std::vector<Matrix>& ms, const char* who, F&& twin) {
-    for (size_t i = 0; i < ms.size(); ++i)
-        for (size_t j = i + 1; j < ms.size(); ++j) {
-            const Matrix &a = ms[i], &b = ms[j];
+int32_t check_overlaps(std::initializer_list<Matrix> ms, const char* who, F&& twin) {
+    for (auto i = ms.begin(); i != ms.end(); ++i)
+        for (auto j = i + 1; j != ms.end(); ++j) {
+            const Matrix &a = *i, &b = *j;
             if (!(a.written || b.written) || !overlap(a, b)) continue;
             if (same(a, b) && twin(a, b)) continue;
             return fail(FSDP_E_ALIAS, "%s: %s overlaps %s", who, a.what, b.what);
@@ -960,7 +1013,7 @@ int32_t run_product(Product& g, bool fp8, bool direct, void* workspace, int64_t 
     const int64_t big = ceil_div(g.m, 256) * ceil_div(g.n, 256);
     if (direct && big >= kCus / 2) {
         choose_splits(g, big, workspace, 0);
-        return launch_product<256, 256, 2, 4, AL, BL, true, false>(g, stream, who);
+        return launch_product<256, 256, 2, 2, AL, BL, true, false>(g, stream, who);
     }
     choose_splits(g, ceil_div(g.m, 128) * ceil_div(g.n, 128), workspace, bytes);
     if (direct) return launch_product<128, 128, 2, 2, AL, BL, true, false>(g, stream, who);
