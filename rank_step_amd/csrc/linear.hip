@@ -248,40 +248,64 @@ struct Epilogue {
     int32_t out_f32, act;
 };
 
-// Elements (i, j .. j + cnt) of the output, j a multiple of 8: the forward
-// call's bias, activation, dropout and residual; the gradients use the
-// division, the accumulation and the store.
-__device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t i, int64_t j, int cnt, int64_t n,
-                                          float recip, uint64_t off, float (&v)[8]) {
+// Elements (i, j .. j + cnt) of the output for the NB rows i = row, row + step,
+// ... below m, j a multiple of 8: the forward call's bias, activation, dropout
+// and residual; the gradients use the division, the accumulation and the
+// store.  Every row's residual is read before the first row is stored, so that
+// the reads wait once (the output may be the residual, element for element).
+template <int NB>
+__device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int step, int64_t m, int64_t j, int cnt,
+                                          int64_t n, float recip, uint64_t off, float (&v)[NB][8]) {
+    float r[NB][8];
+    if (e.res) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int64_t i = row + b * step;
+            if (i < m) {
+                if (e.out_f32) load8(static_cast<const float*>(e.res) + i * e.ldr + j, cnt, r[b]);
+                else load8(static_cast<const uint16_t*>(e.res) + i * e.ldr + j, cnt, r[b]);
+            }
+        }
+    }
     if (e.scale) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] *= recip;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[b][q] *= recip;
     }
     if (e.bias) {
-        float b[8];
-        load8(e.bias + j, cnt, b);
+        float c[8];
+        load8(e.bias + j, cnt, c);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += b[q];
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[b][q] += c[q];
     }
-    if (e.z) store8(e.z + i * e.ldz + j, cnt, v);
-    activate8(v, e.act);
-    if (e.mask.t) drop8(v, e.mask, off, static_cast<uint64_t>(i) * ((n + 7) >> 3) + (j >> 3));
-    if (e.out_f32) {
-        if (e.res) {
-            float r[8];
-            load8(static_cast<const float*>(e.res) + i * e.ldr + j, cnt, r);
+    if (e.z) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] += r[q];
-        }
-        store8(static_cast<float*>(e.out) + i * e.ldo + j, cnt, v);
-    } else {
-        if (e.res) {
-            float r[8];
-            load8(static_cast<const uint16_t*>(e.res) + i * e.ldr + j, cnt, r);
+        for (int b = 0; b < NB; ++b)
+            if (row + b * step < m) store8(e.z + (row + b * step) * e.ldz + j, cnt, v[b]);
+    }
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] += r[q];
+    for (int b = 0; b < NB; ++b) activate8(v[b], e.act);
+    if (e.mask.t) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            drop8(v[b], e.mask, off, static_cast<uint64_t>(row + b * step) * ((n + 7) >> 3) + (j >> 3));
+    }
+    if (e.res) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[b][q] += r[b][q];
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int64_t i = row + b * step;
+        if (i < m) {
+            if (e.out_f32) store8(static_cast<float*>(e.out) + i * e.ldo + j, cnt, v[b]);
+            else store8(static_cast<uint16_t*>(e.out) + i * e.ldo + j, cnt, v[b]);
         }
-        store8(static_cast<uint16_t*>(e.out) + i * e.ldo + j, cnt, v);
     }
 }
 
@@ -339,34 +363,35 @@ using Lds = __attribute__((address_space(3))) uint8_t;
 constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset past every range used here
 
 // Copies one operand's tile from memory to LDS without passing through
-// registers.  Rows and chunks outside the matrix come as zeros from the
-// buffer's range check.  Needs 16-byte aligned rows and lengths that are
-// multiples of 8, so that no 16-byte chunk is partly outside.
+// registers.  What lies outside the matrix comes as zeros: buffer loads are
+// checked against a range, and such lanes' offsets lie beyond it.  Needs
+// 16-byte aligned rows and lengths that are multiples of 8, so that no 16-byte
+// chunk is partly outside.
 template <int W, int THREADS, bool LMAJOR>
 struct DirectTile {
     static constexpr int kLoads = W * (kBK / 8) / THREADS;
-    const uint8_t* base;  // the tile's first row and column at contraction index l0
-    int64_t left;         // bytes from base to the matrix's end
+    const uint8_t* base;  // the tile's first row and column at this contraction index
     int64_t step;         // bytes per kBK contraction elements
+    int left;             // contraction elements from here to the end, may be negative
+    int row;              // bytes of a row
+    int chunk;            // l-major: this thread's first element in a row (the same in all its loads)
     uint32_t off[kLoads];
-    int chunk;            // l-major: this thread's chunk (the same in all its loads)
 
-    __device__ __forceinline__ void init(const void* p, int64_t ld, int o0, int no, int l0, int nl, int tid) {
-        const int64_t row = ld * 2;
+    __device__ __forceinline__ void init(const void* p, int64_t ld, int o0, int no, int l0, int lend, int tid) {
+        row = static_cast<int>(ld * 2);
+        left = lend - l0;
         if (LMAJOR) {
-            base = static_cast<const uint8_t*>(p) + o0 * row + static_cast<int64_t>(l0) * 2;
-            left = (static_cast<int64_t>(no) - 1 - o0) * row + (static_cast<int64_t>(nl) - l0) * 2;
+            base = static_cast<const uint8_t*>(p) + o0 * (ld * 2) + static_cast<int64_t>(l0) * 2;
             step = kBK * 2;
-            chunk = lmajor_chunk(tid);
+            chunk = lmajor_chunk(tid) * 8;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int r = (i * THREADS + tid) >> 3;
-                off[i] = o0 + r < no ? static_cast<uint32_t>(r * row + chunk * 16) : kOutside;
+                off[i] = o0 + r < no ? static_cast<uint32_t>(r * row + chunk * 2) : kOutside;
             }
         } else {
-            base = static_cast<const uint8_t*>(p) + l0 * row + static_cast<int64_t>(o0) * 2;
-            left = (static_cast<int64_t>(nl) - 1 - l0) * row + (static_cast<int64_t>(no) - o0) * 2;
-            step = kBK * row;
+            base = static_cast<const uint8_t*>(p) + l0 * (ld * 2) + static_cast<int64_t>(o0) * 2;
+            step = kBK * (ld * 2);
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int slot = i * THREADS + tid, c = omajor_chunk<W>(slot);
@@ -375,25 +400,21 @@ struct DirectTile {
         }
     }
 
-    // Issues part i of n of the tile's loads; lleft: contraction elements left
-    // from here on (none: every load is out of range, touches no memory and
-    // gives zeros).
-    __device__ __forceinline__ void load(Lds* dst, int wave, int lleft, int i, int n) {
-        const uint32_t range = static_cast<uint32_t>(left < 0 ? 0 : min(left, static_cast<int64_t>(0x7fffffff)));
+    // Load q of the tile.  Behind the contraction's end no load touches
+    // memory.  l-major: the lanes whose chunk lies there are sent out of
+    // range; else the range ends with the last row.
+    __device__ __forceinline__ void load(Lds* dst, int wave, int q) {
+        const int range = LMAJOR ? 0x7fffffff : __builtin_amdgcn_readfirstlane(max(0, min(left, kBK)) * row);
         const __amdgpu_buffer_rsrc_t rsrc =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(range), 0x00020000);
-#pragma unroll
-        for (int q = i * kLoads / n; q < (i + 1) * kLoads / n; ++q) {
-            uint32_t o = off[q];
-            if (LMAJOR) o = chunk * 8 < lleft ? o : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (__attribute__((address_space(3))) void*)(dst + (q * THREADS + wave * 64) * 16), 16, o, 0, 0, 0);
-        }
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, range, 0x00020000);
+        const uint32_t o = LMAJOR && chunk >= left ? kOutside : off[q];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc, (__attribute__((address_space(3))) void*)(dst + (q * THREADS + wave * 64) * 16), 16, o, 0, 0, 0);
     }
 
     __device__ __forceinline__ void advance() {
         base += step;
-        left -= step;
+        left -= kBK;
     }
 };
 
@@ -592,28 +613,28 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
         if (f < kFJ) b[kk][f] = fb.get(stage + BM * kBK * 2, f, kk);
         else a[kk][f - kFJ] = fa.get(stage, f - kFJ, kk);
     };
-    // Half kk row by row, the reads of the other half (of `stage`) and the
-    // refill's loads placed between the rows: 3 fragments a row, so that the
-    // last rows leave them time to come.
+    // Half kk, product by product, with the reads of the other half (of
+    // `stage`) and a refill's loads between them one at a time: a product
+    // keeps the matrix unit for 16 cycles, in which one other access can be
+    // issued, and with one wave a SIMD nothing else covers a longer run of
+    // them.  The reads end early enough to have come when the half does.
     auto multiply = [&](int kk, const Lds* stage, auto&& between) {
-        constexpr int kReads = kFI == 8 ? 3 : (kFI + kFJ) / kFI + 1;
+        constexpr int kAll = kFI * kFJ, kGap = kAll >= 64 ? 3 : 1;
 #pragma unroll
-        for (int i = 0; i < kFI; ++i) {
-#pragma unroll
-            for (int f = i * kReads; f < (i + 1) * kReads && f < kFI + kFJ; ++f) read(stage, 1 - kk, f);
-            between(i);
+        for (int t = 0; t < kAll; ++t) {
+            mfma(acc[t / kFJ][t % kFJ], b[kk][t % kFJ], a[kk][t / kFJ]);
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 0; j < kFJ; ++j) mfma(acc[i][j], b[kk][j], a[kk][i]);
+            if (t % kGap == 0 && t / kGap < kFI + kFJ) read(stage, 1 - kk, t / kGap);
+            between(t, kAll);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // refill(stage, i, n): part i of n of the loads that fill a stage.
+    // refill(stage, i, n): what of a stage's filling belongs to place i of n.
     auto run = [&](auto&& refill) {
         auto step = [&](Lds* cur, Lds* nxt) {
-            multiply(0, cur, [](int) {});
+            multiply(0, cur, [](int, int) {});
             arrive();
-            multiply(1, nxt, [&](int i) { refill(cur, i, kFI); });
+            multiply(1, nxt, [&](int i, int n) { refill(cur, i, n); });
         };
         arrive();
         settle(acc);
@@ -631,21 +652,25 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
         if constexpr (DIRECT) {
             DirectTile<BM, kThreads, AL> ta;
             DirectTile<BN, kThreads, BL> tb;
-            ta.init(g.a, g.lda, i0, g.m, kbeg, AL ? g.k : kend, tid);
-            tb.init(g.b, g.ldb, j0, g.n, kbeg, BL ? g.k : kend, tid);
-            int lleft = kend - kbeg;
-            auto fetch = [&](Lds* stage, int i, int n) {
-                ta.load(stage, wave, lleft, i, n);
-                tb.load(stage + BM * kBK * 2, wave, lleft, i, n);
-                if (i == n - 1) {
+            ta.init(g.a, g.lda, i0, g.m, kbeg, kend, tid);
+            tb.init(g.b, g.ldb, j0, g.n, kbeg, kend, tid);
+            constexpr int kLoads = ta.kLoads + tb.kLoads;
+            auto fetch = [&](Lds* stage, int q) {
+                if (q < ta.kLoads) ta.load(stage, wave, q);
+                else tb.load(stage + BM * kBK * 2, wave, q - ta.kLoads);
+                if (q == kLoads - 1) {
                     ta.advance();
                     tb.advance();
-                    lleft -= kBK;
                 }
             };
-            fetch(l0, 0, 1);
-            fetch(l1, 0, 1);
-            run(fetch);
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) fetch(l0, q);
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) fetch(l1, q);
+            run([&](Lds* stage, int i, int n) {
+                const int every = n / kLoads;
+                if (i % every == every - 1) fetch(stage, i / every);
+            });
         } else {
             StagedTile<BM, kThreads, AL, false> ta;
             StagedTile<BN, kThreads, BL, FP8> tb;
@@ -709,13 +734,23 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
             for (int j = 0; j < kFJ; ++j)
                 *(Quad*)(piece + (i * 16 + lo) * (kWN * 4) + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
         __builtin_amdgcn_wave_barrier();
+        constexpr int kBatch = 4, kStep = 64 / kLanes;
 #pragma unroll 1
-        for (int r = lane / kLanes; r < 64; r += 64 / kLanes) {
-            const f32x4 x = *(const Quad*)(piece + r * (kWN * 4) + (((c * 2) ^ (r & 15)) << 4));
-            const f32x4 y = *(const Quad*)(piece + r * (kWN * 4) + (((c * 2 + 1) ^ (r & 15)) << 4));
-            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            const int row = i0 + wi * kWM + h * 64 + r;
-            if (row < g.m && col < g.n) epilogue8(g.e, row, col, g.n - col, g.n, recip, off, v);
+        for (int r = lane / kLanes; r < 64; r += kBatch * kStep) {
+            float v[kBatch][8];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int rq = r + q * kStep;
+                const f32x4 x = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2) ^ (rq & 15)) << 4));
+                const f32x4 y = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2 + 1) ^ (rq & 15)) << 4));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    v[q][t] = x[t];
+                    v[q][4 + t] = y[t];
+                }
+            }
+            if (col < g.n)
+                epilogue8<kBatch>(g.e, i0 + wi * kWM + h * 64 + r, kStep, g.m, col, g.n - col, g.n, recip, off, v);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -737,8 +772,8 @@ __global__ __launch_bounds__(kJoinBlock) void join_kernel(Product g) {
         x += *reinterpret_cast<const f32x4*>(p + s * stride);
         y += *reinterpret_cast<const f32x4*>(p + s * stride + 4);
     }
-    float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-    epilogue8(g.e, i, j, g.n - j, g.n, g.e.scale ? 1.0f / *g.e.scale : 1.0f, mask_offset(g.e.mask), v);
+    float v[1][8] = {{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
+    epilogue8<1>(g.e, i, 0, g.m, j, g.n - j, g.n, g.e.scale ? 1.0f / *g.e.scale : 1.0f, mask_offset(g.e.mask), v);
 }
 
 // ---------------------------------------------------------------- elementwise passes
