@@ -245,6 +245,7 @@ struct Epilogue {
     const float* scale;  // the product is divided by it; null: 1
     int64_t ldo, ldr, ldz;
     Mask mask;
+    int64_t n, j0;  // the whole matrix's columns, and the first of this product's among them (a multiple of 8)
     int32_t out_f32, act;
 };
 
@@ -255,7 +256,7 @@ struct Epilogue {
 // the reads wait once (the output may be the residual, element for element).
 template <int NB>
 __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int step, int64_t m, int64_t j, int cnt,
-                                          int64_t n, float recip, uint64_t off, float (&v)[NB][8]) {
+                                          float recip, uint64_t off, float (&v)[NB][8]) {
     float r[NB][8];
     if (e.res) {
 #pragma unroll
@@ -291,7 +292,7 @@ __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int st
     if (e.mask.t) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-            drop8(v[b], e.mask, off, static_cast<uint64_t>(row + b * step) * ((n + 7) >> 3) + (j >> 3));
+            drop8(v[b], e.mask, off, static_cast<uint64_t>(row + b * step) * ((e.n + 7) >> 3) + ((e.j0 + j) >> 3));
     }
     if (e.res) {
 #pragma unroll
@@ -561,35 +562,53 @@ __device__ __forceinline__ void settle(f32x4 (&acc)[FI][FJ]) {
         for (int j = 0; j < FJ; ++j) asm volatile("" : "+a"(acc[i][j]));
 }
 
-// Everything this wave has asked of memory and LDS has come, in every wave.
+// Everything this wave has asked of memory and LDS has come; ALL: in every
+// wave of the workgroup.
+template <bool ALL>
 __device__ __forceinline__ void arrive() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    if (ALL) {
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    }
 }
 
 // BM x BN output tile by WI x WJ waves, two LDS stages of kBK contraction
 // elements: while one is multiplied the next arrives.
-template <int BM, int BN, int WI, int WJ, bool AL, bool BL, bool DIRECT, bool FP8>
-__global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
+// KW > 1 (with WI = WJ = 1): KW waves that each take a KW-th of the
+// contraction for the whole tile, through stages of their own, without a
+// barrier until their sums are added at the end.  It is the form for products
+// of few tiles: a wave's tile stays 64 x 64, which needs half the LDS reads a
+// product of 32 x 32 ones, while four times as many loads are on their way.
+template <int BM, int BN, int WI, int WJ, int KW, bool AL, bool BL, bool DIRECT, bool FP8>
+__global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
+    static_assert(KW == 1 || (WI == 1 && WJ == 1 && BM == 64 && BN == 64 && DIRECT), "");
     constexpr int kThreads = WI * WJ * 64, kWM = BM / WI, kWN = BN / WJ, kFI = kWM / 16, kFJ = kWN / 16;
     constexpr int kStage = (BM + BN) * kBK * 2;
-    __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t s1[kStage];
-    Lds* const l0 = (Lds*)s0;
-    Lds* const l1 = (Lds*)s1;
+    constexpr bool kShared = KW == 1;  // the waves share their stages
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage * KW];
+    __shared__ __attribute__((aligned(1024))) uint8_t s1[kStage * KW];
 
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tid = kShared ? threadIdx.x : lane;  // among the threads that fill a stage
+    const int part = kShared ? 0 : wave;
+    Lds* const l0 = (Lds*)s0 + part * kStage;
+    Lds* const l1 = (Lds*)s1 + part * kStage;
     const int tiles = g.tm * g.tn;
     const int id = tile_id(blockIdx.x, tiles * g.splits);
     const int split = id / tiles;
     int ti, tj;
     tile_at(id - split * tiles, g.tm, g.tn, &ti, &tj);
     const int i0 = ti * BM, j0 = tj * BN;
-    const int kbeg = split * g.kper, kend = min(g.k, kbeg + g.kper);
+    int kbeg = split * g.kper, kend = min(g.k, kbeg + g.kper);
+    if (KW > 1) {
+        const int per = (kend - kbeg + kBK * KW - 1) / (kBK * KW) * kBK;
+        kbeg += part * per;
+        kend = min(kend, kbeg + per);
+    }
     const int steps = kend > kbeg ? (kend - kbeg + kBK - 1) / kBK : 0;
-    const int wi = wave / WJ, wj = wave % WJ;
+    const int wi = kShared ? wave / WJ : 0, wj = kShared ? wave % WJ : 0;
 
     f32x4 acc[kFI][kFJ];
 #pragma unroll
@@ -633,10 +652,10 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
     auto run = [&](auto&& refill) {
         auto step = [&](Lds* cur, Lds* nxt) {
             multiply(0, cur, [](int, int) {});
-            arrive();
+            arrive<kShared>();
             multiply(1, nxt, [&](int i, int n) { refill(cur, i, n); });
         };
-        arrive();
+        arrive<kShared>();
         settle(acc);
 #pragma unroll
         for (int f = 0; f < kFI + kFJ; ++f) read(l0, 0, f);
@@ -656,8 +675,8 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
             tb.init(g.b, g.ldb, j0, g.n, kbeg, kend, tid);
             constexpr int kLoads = ta.kLoads + tb.kLoads;
             auto fetch = [&](Lds* stage, int q) {
-                if (q < ta.kLoads) ta.load(stage, wave, q);
-                else tb.load(stage + BM * kBK * 2, wave, q - ta.kLoads);
+                if (q < ta.kLoads) ta.load(stage, kShared ? wave : 0, q);
+                else tb.load(stage + BM * kBK * 2, kShared ? wave : 0, q - ta.kLoads);
                 if (q == kLoads - 1) {
                     ta.advance();
                     tb.advance();
@@ -700,8 +719,52 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
     // Lane l holds of each 16x16 block output row l mod 16 and columns
     // 4 (l / 16) + 0..3.
     const int lo = lane & 15, hi = lane >> 4;
+    using Quad = __attribute__((address_space(3))) f32x4;
+    const float recip = g.e.scale ? 1.0f / *g.e.scale : 1.0f;
+    const uint64_t off = mask_offset(g.e.mask);
+    float* const sums = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
+    // Rows of 16-byte chunks in LDS are permuted by the row, which spreads the
+    // 16 rows that one write touches over the banks.
+    if constexpr (KW > 1) {
+        arrive<false>();  // this wave's stages are being read and filled until here
+#pragma unroll
+        for (int i = 0; i < kFI; ++i)
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j)
+                *(Quad*)(l0 + (i * 16 + lo) * 256 + (((j * 4 + hi) ^ lo) << 4)) = acc[i][j];
+        __syncthreads();
+        // each wave adds the parts of its 64 / KW rows, in order
+        constexpr int kBatch = 64 / KW / 8;
+        const int c = lane & 7, col = j0 + c * 8, r0 = wave * (64 / KW) + (lane >> 3);
+        float v[kBatch][8];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int r = r0 + q * 8;
+            f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll
+            for (int p = 0; p < KW; ++p) {
+                const Lds* row = (Lds*)s0 + p * kStage + r * 256;
+                x += *(const Quad*)(row + (((c * 2) ^ (r & 15)) << 4));
+                y += *(const Quad*)(row + (((c * 2 + 1) ^ (r & 15)) << 4));
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                v[q][t] = x[t];
+                v[q][4 + t] = y[t];
+            }
+        }
+        if (g.splits > 1) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int row = i0 + r0 + q * 8;
+                if (row < g.m && col < g.pitch) store8(sums + static_cast<int64_t>(row) * g.pitch + col, 8, v[q]);
+            }
+        } else if (col < g.n) {
+            epilogue8<kBatch>(g.e, i0 + r0, 8, g.m, col, g.n - col, recip, off, v);
+        }
+        return;
+    }
     if (g.splits > 1) {
-        float* part = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
 #pragma unroll
         for (int i = 0; i < kFI; ++i) {
             const int row = i0 + wi * kWM + i * 16 + lo;
@@ -709,22 +772,17 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
             for (int j = 0; j < kFJ; ++j) {
                 const int col = j0 + wj * kWN + j * 16 + hi * 4;
                 if (row < g.m && col < g.pitch)
-                    *reinterpret_cast<f32x4*>(part + static_cast<int64_t>(row) * g.pitch + col) = acc[i][j];
+                    *reinterpret_cast<f32x4*>(sums + static_cast<int64_t>(row) * g.pitch + col) = acc[i][j];
             }
         }
         return;
     }
     // 64 rows at a time through the wave's own piece of LDS, so that a lane has
-    // 8 consecutive columns: one 16-byte store and one mask block.  A row's
-    // 16-byte chunks are permuted by the row, which spreads the 16 rows that
-    // one write touches over the banks.
-    arrive();  // the last stages are being read and filled until here
-    constexpr int kHalf = WI * WJ / 2, kPiece = 64 * kWN * 4, kLanes = kWN / 8;
-    static_assert(kWM % 64 == 0 && kWN >= 64 && kHalf * kPiece <= kStage, "a piece of 64 x kWN floats a wave");
+    // 8 consecutive columns: one 16-byte store and one mask block.
+    arrive<true>();  // the last stages are being read and filled until here
+    constexpr int kHalf = (WI * WJ + 1) / 2, kPiece = 64 * kWN * 4, kLanes = kWN / 8;
+    static_assert(KW > 1 || (kWM % 64 == 0 && kWN >= 64 && kHalf * kPiece <= kStage), "a piece of 64 x kWN floats a wave");
     Lds* const piece = (wave < kHalf ? l0 : l1) + wave % kHalf * kPiece;
-    using Quad = __attribute__((address_space(3))) f32x4;
-    const float recip = g.e.scale ? 1.0f / *g.e.scale : 1.0f;
-    const uint64_t off = mask_offset(g.e.mask);
     const int c = lane % kLanes, col = j0 + wj * kWN + c * 8;
 #pragma unroll
     for (int h = 0; h < kWM / 64; ++h) {
@@ -750,7 +808,7 @@ __global__ __launch_bounds__(WI* WJ * 64) void product_kernel(Product g) {
                 }
             }
             if (col < g.n)
-                epilogue8<kBatch>(g.e, i0 + wi * kWM + h * 64 + r, kStep, g.m, col, g.n - col, g.n, recip, off, v);
+                epilogue8<kBatch>(g.e, i0 + wi * kWM + h * 64 + r, kStep, g.m, col, g.n - col, recip, off, v);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -773,7 +831,179 @@ __global__ __launch_bounds__(kJoinBlock) void join_kernel(Product g) {
         y += *reinterpret_cast<const f32x4*>(p + s * stride + 4);
     }
     float v[1][8] = {{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
-    epilogue8<1>(g.e, i, 0, g.m, j, g.n - j, g.n, g.e.scale ? 1.0f / *g.e.scale : 1.0f, mask_offset(g.e.mask), v);
+    epilogue8<1>(g.e, i, 0, g.m, j, g.n - j, g.e.scale ? 1.0f / *g.e.scale : 1.0f, mask_offset(g.e.mask), v);
+}
+
+// ---------------------------------------------------------------- products of few rows
+
+// 8 elements of a row from k on, zeros from `len` on; any alignment.
+__device__ __forceinline__ u32x4 row8(const uint16_t* row, int k, int len) {
+    if (k + 8 <= len) return reinterpret_cast<const Bytes16*>(row + k)->v;
+    u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        const uint32_t c = k + s < len ? row[k + s] : 0u;
+        w[s / 2] |= c << (16 * (s & 1));
+    }
+    return w;
+}
+
+// 8 E4M3 codes as bf16, exactly.
+__device__ __forceinline__ u32x4 widen_e4m3(uint32_t c0, uint32_t c1) {
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, true)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, true))};
+}
+
+__device__ __forceinline__ u32x4 row16(const uint8_t* row, int k, int len) {
+    if (k + 16 <= len) return reinterpret_cast<const Bytes16*>(row + k)->v;
+    u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+        const uint32_t c = k + s < len ? row[k + s] : 0u;
+        w[s / 4] |= c << (8 * (s & 3));
+    }
+    return w;
+}
+
+// The forward product for at most 16 * MB tokens: bound by reading W once.  A
+// workgroup takes 16 * JB output features; its eight waves take every eighth
+// chunk of 64 contraction elements, from memory straight into the fragments
+// of the matrix instructions (W is used once, so LDS would only be a detour;
+// x comes from L2), several chunks on their way at a time.  Their sums are
+// added in LDS, so the call is one launch.
+constexpr int kFewWaves = 8;
+template <int MB, int JB, bool FP8>
+__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
+    constexpr int kPitch = 20;  // floats of 16, padded against bank conflicts
+    __shared__ __attribute__((aligned(16))) float sums[kFewWaves][MB][JB][16 * kPitch];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lo = lane & 15, q = lane >> 4;
+    const int j0 = blockIdx.x * (16 * JB);
+    // Rows past the end are read as the last one; what they give is not stored.
+    const uint16_t* x[MB];
+    const uint8_t* w[JB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        x[i] = static_cast<const uint16_t*>(g.a) + min(i * 16 + lo, g.m - 1) * g.lda;
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+        w[j] = static_cast<const uint8_t*>(g.b) + min(j0 + j * 16 + lo, g.n - 1) * g.ldb * (FP8 ? 1 : 2);
+    f32x4 acc[MB][JB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    // A chunk is two matrix instructions.  Lane group q takes of the chunk's
+    // contraction elements 8 q + 0..7 of each half of 32 (bf16), or 16 q + 0..15
+    // (E4M3: one 16-byte load), and the same ones of x.
+    struct Chunk {
+        u32x4 x[MB][2], w[JB][FP8 ? 1 : 2];
+    };
+    auto load = [&](Chunk& c, int k, int len) {
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            if (FP8) {
+                c.w[j][0] = row16(w[j], k + q * 16, len);
+            } else {
+                c.w[j][0] = row8(reinterpret_cast<const uint16_t*>(w[j]), k + q * 8, len);
+                c.w[j][FP8 ? 0 : 1] = row8(reinterpret_cast<const uint16_t*>(w[j]), k + 32 + q * 8, len);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            c.x[i][0] = row8(x[i], k + q * (FP8 ? 16 : 8), len);
+            c.x[i][1] = row8(x[i], k + (FP8 ? q * 16 + 8 : 32 + q * 8), len);
+        }
+    };
+    auto multiply = [&](const Chunk& c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            bf16x8 b[JB];
+#pragma unroll
+            for (int j = 0; j < JB; ++j)
+                b[j] = __builtin_bit_cast(bf16x8, FP8 ? widen_e4m3(c.w[j][0][2 * h], c.w[j][0][2 * h + 1])
+                                                      : c.w[j][FP8 ? 0 : h]);
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int j = 0; j < JB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        b[j], __builtin_bit_cast(bf16x8, c.x[i][h]), acc[i][j], 0, 0, 0);
+        }
+    };
+    constexpr int kAhead = MB * JB == 1 ? 8 : 4;
+    const int full = g.k / 64;
+    int c = wave;
+    for (; c + (kAhead - 1) * kFewWaves < full; c += kAhead * kFewWaves) {
+        Chunk r[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) load(r[u], (c + u * kFewWaves) * 64, 0x7fffffff);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) multiply(r[u]);
+    }
+    for (; c * 64 < g.k; c += kFewWaves) {
+        Chunk r;
+        load(r, c * 64, g.k);
+        multiply(r);
+    }
+    // Lane: token lo, features 4 q + 0..3.
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) *reinterpret_cast<f32x4*>(&sums[wave][i][j][lo * kPitch + q * 4]) = acc[i][j];
+    __syncthreads();
+    const int t = threadIdx.x, half = t & 1, j = (t >> 1) % JB, i = t / (2 * JB);
+    const int col = j0 + j * 16 + half * 8;
+    if (i >= g.m || i >= 16 * MB || col >= g.n) return;
+    float v[1][8] = {{0, 0, 0, 0, 0, 0, 0, 0}};
+#pragma unroll
+    for (int p = 0; p < kFewWaves; ++p) {
+        const float* s = &sums[p][i >> 4][j][(i & 15) * kPitch + half * 8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[0][u] += s[u];
+    }
+    epilogue8<1>(g.e, i, 0, g.m, col, g.n - col, g.e.scale ? 1.0f / *g.e.scale : 1.0f, mask_offset(g.e.mask), v);
+}
+
+// ---------------------------------------------------------------- operands laid out anew
+
+// A matrix as the direct loads want it: bf16 rows on 16-byte boundaries, their
+// length rounded up to 8 with zeros.
+struct Pack {
+    const void* src;
+    uint16_t* dst;
+    int64_t ld;
+    int32_t rows, cols, chunks, fp8;  // chunks: 16-byte pieces of a packed row
+};
+constexpr int kPackBlock = 256;
+__global__ __launch_bounds__(kPackBlock) void pack_kernel(Pack a, Pack b, int blocks_a) {
+    const bool second = static_cast<int>(blockIdx.x) >= blocks_a;
+    const Pack p = second ? b : a;
+    const int id = (static_cast<int>(blockIdx.x) - (second ? blocks_a : 0)) * kPackBlock + threadIdx.x;
+    const int row = id / p.chunks, c = id - row * p.chunks;
+    if (row >= p.rows) return;
+    u32x4 v;
+    if (p.fp8) {
+        const uint8_t* q = static_cast<const uint8_t*>(p.src) + row * p.ld + c * 8;
+        uint32_t w0 = 0, w1 = 0;
+        if (c * 8 + 8 <= p.cols) {
+            const Bytes8 x = *reinterpret_cast<const Bytes8*>(q);
+            w0 = x.v[0];
+            w1 = x.v[1];
+        } else {
+            for (int s = 0; s < p.cols - c * 8; ++s) {
+                if (s < 4) w0 |= static_cast<uint32_t>(q[s]) << (8 * s);
+                else w1 |= static_cast<uint32_t>(q[s]) << (8 * (s - 4));
+            }
+        }
+        v = widen_e4m3(w0, w1);
+    } else {
+        v = row8(static_cast<const uint16_t*>(p.src) + row * p.ld, c * 8, p.cols);
+    }
+    *reinterpret_cast<u32x4*>(p.dst + static_cast<int64_t>(id) * 8) = v;
 }
 
 // ---------------------------------------------------------------- elementwise passes
@@ -1008,7 +1238,7 @@ bool direct_ok(const void* p, int64_t ld, int64_t rows, int64_t cols) {
     return aligned(p, 16) && cols % 8 == 0 && (ld % 8 == 0 || rows <= 1) && ld <= (int64_t(1) << 21);
 }
 
-template <int BM, int BN, int WI, int WJ, bool AL, bool BL, bool DIRECT, bool FP8>
+template <int BM, int BN, int WI, int WJ, int KW, bool AL, bool BL, bool DIRECT, bool FP8>
 int32_t launch_product(Product& g, hipStream_t stream, const char* who) {
     g.tm = static_cast<int32_t>(ceil_div(g.m, BM));
     g.tn = static_cast<int32_t>(ceil_div(g.n, BN));
@@ -1016,8 +1246,8 @@ int32_t launch_product(Product& g, hipStream_t stream, const char* who) {
     const int64_t joins = ceil_div(static_cast<int64_t>(g.m) * (g.pitch / 8), kJoinBlock);
     if (blocks > 0x7fffff || (g.splits > 1 && joins > 0x7fffff))
         return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
-    product_kernel<BM, BN, WI, WJ, AL, BL, DIRECT, FP8>
-        <<<dim3(static_cast<uint32_t>(blocks)), dim3(WI * WJ * 64), 0, stream>>>(g);
+    product_kernel<BM, BN, WI, WJ, KW, AL, BL, DIRECT, FP8>
+        <<<dim3(static_cast<uint32_t>(blocks)), dim3(WI * WJ * KW * 64), 0, stream>>>(g);
     int32_t st = launched(who);
     if (st != FSDP_OK || g.splits == 1) return st;
     join_kernel<<<dim3(static_cast<uint32_t>(joins)), dim3(kJoinBlock), 0, stream>>>(g);
@@ -1026,36 +1256,157 @@ int32_t launch_product(Product& g, hipStream_t stream, const char* who) {
 
 constexpr int kCus = 256;
 
-// Parts of the contraction: enough workgroups for the chip's CUs, at least
-// four LDS tiles each, partial sums within the workspace.
-void choose_splits(Product& g, int64_t tiles, void* workspace, int64_t bytes) {
+// The workspace, handed out from its start.
+struct Space {
+    uint8_t* p;
+    int64_t left;
+
+    Space(void* ptr, int64_t bytes)
+        : p(static_cast<uint8_t*>(ptr)), left(std::min(bytes, FSDP_LINEAR_WORKSPACE_BYTES)) {}
+    void* take(int64_t bytes) {
+        bytes = (bytes + 255) / 256 * 256;
+        if (bytes > left) return nullptr;
+        void* q = p;
+        p += bytes;
+        left -= bytes;
+        return q;
+    }
+};
+
+// Parts of the contraction: at most `want`, at least `least` LDS tiles each,
+// partial sums within the workspace.
+void choose_splits(Product& g, int64_t want, int64_t least, const Space& space) {
     const int64_t steps = std::max<int64_t>(1, ceil_div(g.k, kBK));
     const int64_t one = static_cast<int64_t>(g.m) * g.pitch * 4;
-    int64_t splits = std::min<int64_t>(ceil_div(kCus, std::max<int64_t>(1, tiles)), steps / 4);
-    splits = std::min(splits, std::min(bytes, FSDP_LINEAR_WORKSPACE_BYTES) / std::max<int64_t>(1, one));
+    int64_t splits = std::min(want, steps / least);
+    splits = std::min(splits, space.left / std::max<int64_t>(1, one));
     if (splits < 2) splits = 1;
     const int64_t per = ceil_div(steps, splits);
     g.splits = static_cast<int32_t>(ceil_div(steps, per));
     g.kper = static_cast<int32_t>(per * kBK);
-    g.part = static_cast<float*>(workspace);
+    g.part = reinterpret_cast<float*>(space.p);
 }
 
 template <bool AL, bool BL>
-int32_t run_product(Product& g, bool fp8, bool direct, void* workspace, int64_t bytes, hipStream_t stream,
-                    const char* who) {
+int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const char* who) {
+    const int64_t big = ceil_div(g.m, 256) * ceil_div(g.n, 256);
+    const int64_t mid = ceil_div(g.m, 128) * ceil_div(g.n, 128), small = ceil_div(g.m, 64) * ceil_div(g.n, 64);
+    if (big >= kCus / 2) {
+        choose_splits(g, 1, 1, space);
+        return launch_product<256, 256, 2, 2, 1, AL, BL, true, false>(g, stream, who);
+    }
+    if (mid >= kCus) {
+        choose_splits(g, 1, 1, space);
+        return launch_product<128, 128, 2, 2, 1, AL, BL, true, false>(g, stream, who);
+    }
+    choose_splits(g, kCus / small, 8, space);
+    return launch_product<64, 64, 1, 1, 4, AL, BL, true, false>(g, stream, who);
+}
+
+template <int MB, int JB>
+int32_t launch_few(const Product& g, bool fp8, hipStream_t stream, const char* who) {
+    const dim3 grid(static_cast<uint32_t>(ceil_div(g.n, 16 * JB))), block(kFewWaves * 64);
+    if (fp8) few_rows_kernel<MB, JB, true><<<grid, block, 0, stream>>>(g);
+    else few_rows_kernel<MB, JB, false><<<grid, block, 0, stream>>>(g);
+    return launched(who);
+}
+
+// Columns [j0, j0 + n) of the product.
+template <bool BL>
+Product columns(const Product& g, bool fp8, int32_t j0, int32_t n) {
+    Product s = g;
+    const int64_t e = fp8 ? 1 : 2, oe = g.e.out_f32 ? 4 : 2;
+    s.b = static_cast<const uint8_t*>(g.b) + (BL ? j0 * g.ldb : j0) * e;
+    s.n = n;
+    s.pitch = (n + 7) / 8 * 8;
+    s.e.out = static_cast<uint8_t*>(g.e.out) + j0 * oe;
+    if (g.e.res) s.e.res = static_cast<const uint8_t*>(g.e.res) + j0 * oe;
+    if (g.e.z) s.e.z = g.e.z + j0;
+    if (g.e.bias) s.e.bias = g.e.bias + j0;
+    s.e.j0 = j0;
+    return s;
+}
+
+Pack pack_of(const void* src, int64_t ld, int64_t rows, int64_t cols, bool fp8, void* dst) {
+    return Pack{src, static_cast<uint16_t*>(dst), ld, static_cast<int32_t>(rows), static_cast<int32_t>(cols),
+                static_cast<int32_t>(ceil_div(cols, 8)), fp8};
+}
+
+// The product with operands that are not as the direct loads want them: laid
+// out anew in the workspace, B by columns of the output if it does not fit at
+// once, or staged through registers where there is no workspace for that.
+template <bool AL, bool BL>
+int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space& whole, hipStream_t stream,
+                   const char* who) {
+    const int64_t ar = AL ? g.m : g.k, ac = AL ? g.k : g.m;
+    Space space = whole;
+    void* pa = a_ok ? nullptr : space.take(ar * ceil_div(ac, 8) * 16);
+    int64_t cols = g.n;  // output columns at a time
+    if (!b_ok) {
+        const int64_t one = BL ? ceil_div(g.k, 8) * 16 : static_cast<int64_t>(g.k) * 2;  // bytes of a column's part
+        const int64_t most = (space.left - 256) / std::max<int64_t>(1, one);
+        if (most < (cols + 7) / 8 * 8) cols = most / 256 * 256;
+    }
+    if ((!a_ok && !pa) || cols < std::min<int64_t>(g.n, 256)) {
+        Product s = g;
+        const int64_t tiles = ceil_div(g.m, 128) * ceil_div(g.n, 128);
+        choose_splits(s, ceil_div(kCus, tiles), 4, whole);
+        if constexpr (AL) {
+            if (fp8) return launch_product<128, 128, 2, 2, 1, AL, BL, false, true>(s, stream, who);
+        }
+        return launch_product<128, 128, 2, 2, 1, AL, BL, false, false>(s, stream, who);
+    }
+    for (int64_t j0 = 0; j0 < g.n; j0 += cols) {
+        const int64_t n = std::min<int64_t>(cols, g.n - j0);
+        Product s = columns<BL>(g, fp8, static_cast<int32_t>(j0), static_cast<int32_t>(n));
+        Space rest = space;
+        Pack a{}, b{};
+        int64_t blocks_a = 0, blocks_b = 0;
+        if (!a_ok) {
+            if (j0 == 0) {
+                a = pack_of(g.a, g.lda, ar, ac, false, pa);
+                blocks_a = ceil_div(ar * a.chunks, kPackBlock);
+            }
+            s.a = pa;
+            s.lda = ceil_div(ac, 8) * 8;
+        }
+        if (!b_ok) {
+            const int64_t br = BL ? n : g.k, bc = BL ? g.k : n;
+            b = pack_of(s.b, g.ldb, br, bc, fp8, rest.take(br * ceil_div(bc, 8) * 16));
+            blocks_b = ceil_div(br * b.chunks, kPackBlock);
+            s.b = b.dst;
+            s.ldb = b.chunks * 8;
+        }
+        if (blocks_a + blocks_b > 0) {
+            pack_kernel<<<dim3(static_cast<uint32_t>(blocks_a + blocks_b)), dim3(kPackBlock), 0, stream>>>(
+                a, b, static_cast<int>(blocks_a));
+            const int32_t st = launched(who);
+            if (st != FSDP_OK) return st;
+        }
+        const int32_t st = run_direct<AL, BL>(s, rest, stream, who);
+        if (st != FSDP_OK) return st;
+    }
+    return FSDP_OK;
+}
+
+template <bool AL, bool BL>
+int32_t run_product(Product& g, bool fp8, void* workspace, int64_t bytes, hipStream_t stream, const char* who) {
     if (g.m == 0 || g.n == 0) return FSDP_OK;
     g.pitch = (g.n + 7) / 8 * 8;
-    const int64_t big = ceil_div(g.m, 256) * ceil_div(g.n, 256);
-    if (direct && big >= kCus / 2) {
-        choose_splits(g, big, workspace, 0);
-        return launch_product<256, 256, 2, 2, AL, BL, true, false>(g, stream, who);
+    g.e.n = g.n;
+    if constexpr (AL && BL) {
+        if (g.m <= 32) {
+            g.splits = 1;
+            const bool wide = ceil_div(g.n, 32) >= kCus;
+            if (g.m <= 16) return wide ? launch_few<1, 2>(g, fp8, stream, who) : launch_few<1, 1>(g, fp8, stream, who);
+            return wide ? launch_few<2, 2>(g, fp8, stream, who) : launch_few<2, 1>(g, fp8, stream, who);
+        }
     }
-    choose_splits(g, ceil_div(g.m, 128) * ceil_div(g.n, 128), workspace, bytes);
-    if (direct) return launch_product<128, 128, 2, 2, AL, BL, true, false>(g, stream, who);
-    if constexpr (AL) {
-        if (fp8) return launch_product<128, 128, 2, 2, AL, BL, false, true>(g, stream, who);
-    }
-    return launch_product<128, 128, 2, 2, AL, BL, false, false>(g, stream, who);
+    const Space space(workspace, bytes);
+    const bool a_ok = direct_ok(g.a, g.lda, AL ? g.m : g.k, AL ? g.k : g.m);
+    const bool b_ok = !fp8 && direct_ok(g.b, g.ldb, BL ? g.n : g.k, BL ? g.k : g.n);
+    if (a_ok && b_ok) return run_direct<AL, BL>(g, space, stream, who);
+    return run_packed<AL, BL>(g, fp8, a_ok, b_ok, space, stream, who);
 }
 
 int32_t check_weight(int32_t w_dtype, const float* w_scale, const char* who) {
@@ -1130,8 +1481,7 @@ int32_t forward_impl(const fsdp_linear* a, hipStream_t stream) {
     g.e.bias = a->bias;
     g.e.scale = a->w_scale;
     g.e.act = a->act;
-    const bool direct = we == 2 && direct_ok(a->x, a->ldx, a->m, a->k) && direct_ok(a->w, a->ldw, a->n, a->k);
-    return run_product<true, true>(g, we == 1, direct, a->workspace, a->workspace_bytes, stream, who);
+    return run_product<true, true>(g, we == 1, a->workspace, a->workspace_bytes, stream, who);
 }
 
 int32_t grad_input_impl(uint16_t* dx, int64_t lddx, const uint16_t* dz, int64_t lddz, const void* w, int64_t ldw,
@@ -1160,8 +1510,7 @@ int32_t grad_input_impl(uint16_t* dx, int64_t lddx, const uint16_t* dz, int64_t 
     g.e.ldo = lddx;
     g.e.scale = w_scale;
     g.e.mask.scale = 1.0f;
-    const bool direct = we == 2 && direct_ok(dz, lddz, m, n) && direct_ok(w, ldw, n, k);
-    return run_product<true, false>(g, we == 1, direct, workspace, workspace_bytes, stream, who);
+    return run_product<true, false>(g, we == 1, workspace, workspace_bytes, stream, who);
 }
 
 int32_t grad_weight_impl(void* dw, int64_t lddw, int32_t dw_dtype, int32_t accumulate, const uint16_t* dz,
@@ -1193,8 +1542,7 @@ int32_t grad_weight_impl(void* dw, int64_t lddw, int32_t dw_dtype, int32_t accum
     g.e.res = accumulate ? dw : nullptr;
     g.e.ldr = lddw;
     g.e.mask.scale = 1.0f;
-    const bool direct = direct_ok(dz, lddz, m, n) && direct_ok(x, ldx, m, k);
-    return run_product<false, false>(g, false, direct, workspace, workspace_bytes, stream, who);
+    return run_product<false, false>(g, false, workspace, workspace_bytes, stream, who);
 }
 
 // ---------------------------------------------------------------- host: elementwise passes
