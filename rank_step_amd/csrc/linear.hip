@@ -955,7 +955,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
 #pragma unroll
         for (int j = 0; j < JB; ++j) *reinterpret_cast<f32x4*>(&sums[wave][i][j][lo * kPitch + q * 4]) = acc[i][j];
     __syncthreads();
-    const int t = threadIdx.x, half = t & 1, j = (t >> 1) % JB, i = t / (2 * JB);
+    const int t = threadIdx.x, half = t & 1, j = (t >> 1) % JB, i = t / (2 * JB);  // 16 MB rows of 2 JB pieces
     const int col = j0 + j * 16 + half * 8;
     if (i >= g.m || i >= 16 * MB || col >= g.n) return;
     float v[1][8] = {{0, 0, 0, 0, 0, 0, 0, 0}};
@@ -1311,6 +1311,29 @@ int32_t launch_few(const Product& g, bool fp8, hipStream_t stream, const char* w
     return launched(who);
 }
 
+// The features of a workgroup: x is read again by each, W's rows once, and the
+// CU with the most workgroups ends last; so the least rounds * (bytes of x and
+// W of one).  11008 features of 4096 E4M3 codes, 16 tokens: 48 a workgroup (230
+// workgroups) %FEW%
+template <int MB>
+int32_t run_few(const Product& g, bool fp8, hipStream_t stream, const char* who) {
+    int best = 0;
+    int64_t cost = 0;
+    for (int jb = 1; jb <= 4; ++jb) {
+        const int64_t c = ceil_div(ceil_div(g.n, 16 * jb), kCus) * (16 * jb * (fp8 ? 1 : 2) + 2 * g.m);
+        if (best == 0 || c < cost) {
+            best = jb;
+            cost = c;
+        }
+    }
+    switch (best) {
+        case 1: return launch_few<MB, 1>(g, fp8, stream, who);
+        case 2: return launch_few<MB, 2>(g, fp8, stream, who);
+        case 3: return launch_few<MB, 3>(g, fp8, stream, who);
+        default: return launch_few<MB, 4>(g, fp8, stream, who);
+    }
+}
+
 // Columns [j0, j0 + n) of the product.
 template <bool BL>
 Product columns(const Product& g, bool fp8, int32_t j0, int32_t n) {
@@ -1397,9 +1420,7 @@ int32_t run_product(Product& g, bool fp8, void* workspace, int64_t bytes, hipStr
     if constexpr (AL && BL) {
         if (g.m <= 32) {
             g.splits = 1;
-            const bool wide = ceil_div(g.n, 32) >= kCus;
-            if (g.m <= 16) return wide ? launch_few<1, 2>(g, fp8, stream, who) : launch_few<1, 1>(g, fp8, stream, who);
-            return wide ? launch_few<2, 2>(g, fp8, stream, who) : launch_few<2, 1>(g, fp8, stream, who);
+            return g.m <= 16 ? run_few<1>(g, fp8, stream, who) : run_few<2>(g, fp8, stream, who);
         }
     }
     const Space space(workspace, bytes);
