@@ -43,6 +43,7 @@ struct __attribute__((packed, aligned(2))) Bytes16 { u32x4 v; };
 struct __attribute__((packed, aligned(1))) Bytes8 { uint32_t v[2]; };
 
 constexpr int kXcds = 8;
+constexpr int kCus = 256;
 constexpr int kBK = 64;  // contraction elements of one LDS tile: 128 bytes of bf16
 
 // ---------------------------------------------------------------- dropout
@@ -1323,8 +1324,6 @@ int32_t launch_product(Product& g, hipStream_t stream, const char* who) {
     return launched(who);
 }
 
-constexpr int kCus = 256;
-
 // The workspace, handed out from its start.
 struct Space {
     uint8_t* p;
@@ -1342,15 +1341,50 @@ struct Space {
     }
 };
 
-// Parts of the contraction: at most `want`, at least `least` LDS tiles each,
-// partial sums within the workspace.
-void choose_splits(Product& g, int64_t want, int64_t least, const Space& space) {
-    const int64_t steps = std::max<int64_t>(1, ceil_div(g.k, kBK));
+// A way to compute a product: the output tile's side and the parts that its
+// contraction is split into.
+struct Way {
+    int tile;
+    int64_t splits;
+    double us;
+};
+
+// What a product takes in microseconds, from times measured over products of
+// one 64 x 64 tile to 8192 x 8192 x 8192 on MI355X; within a fifth of most of
+// them, which is enough to order the ways.  A launch is a number of rounds of
+// the chip, each an entry and an epilogue and a time a step of 64.
+//   256: one workgroup a CU.  A step takes 1.5 us on a full chip, where power
+//     sets the clock, 1.0 on a near empty one.  4096 x 4096 x 4096: 105 us, by
+//     128-tiles 130.
+//   128: two workgroups a CU share its matrix units.  2048 x 4096 x 4096: 60
+//     us, by 256-tiles 81.
+//   64: one workgroup a CU, four waves on four parts of a step.  1024 x 1024 x
+//     4096: 17 us, by 128-tiles 42, by those split in four 22.
+//   A split's sums go to memory and back at 6 TB/s, and the join is a launch.
+//     64 x 1024 x 4096 by 64-tiles: 15.5 us, split in 16 9.8.
+Way way_of(int tile, int64_t splits, const Product& g) {
+    const double tiles = static_cast<double>(ceil_div(g.m, tile)) * ceil_div(g.n, tile) * splits;
+    const double steps = static_cast<double>(ceil_div(ceil_div(g.k, kBK), splits));
+    double us = 3;
+    if (tile == 256) us += std::ceil(tiles / kCus) * (10 + (1 + 0.5 * std::min(1.0, tiles / kCus)) * steps);
+    else if (tile == 64) us += std::ceil(tiles / kCus) * (3 + 0.165 * steps);
+    else if (tiles <= kCus) us += 3 + 0.57 * steps;
+    else us += std::ceil(tiles / (2 * kCus)) * (4 + 0.9 * steps);
+    if (splits > 1) us += 3 + 8.0 * splits * g.m * g.pitch / 6e6;
+    return Way{tile, splits, us};
+}
+
+// The splits that fill `fill` workgroups, at least two steps each, partial sums
+// within the workspace.
+int64_t splits_for(int tile, int64_t fill, const Product& g, const Space& space) {
+    const int64_t tiles = ceil_div(g.m, tile) * ceil_div(g.n, tile);
     const int64_t one = static_cast<int64_t>(g.m) * g.pitch * 4;
-    int64_t splits = std::min(want, steps / least);
-    splits = std::min(splits, space.left / std::max<int64_t>(1, one));
-    if (splits < 2) splits = 1;
-    const int64_t per = ceil_div(steps, splits);
+    const int64_t splits = std::min(fill / tiles, ceil_div(g.k, kBK) / (tile == 64 ? 8 : 2));
+    return std::max<int64_t>(1, std::min(splits, space.left / one));
+}
+
+void split(Product& g, int64_t splits, const Space& space) {
+    const int64_t steps = std::max<int64_t>(1, ceil_div(g.k, kBK)), per = ceil_div(steps, splits);
     g.splits = static_cast<int32_t>(ceil_div(steps, per));
     g.kper = static_cast<int32_t>(per * kBK);
     g.part = reinterpret_cast<float*>(space.p);
@@ -1358,17 +1392,15 @@ void choose_splits(Product& g, int64_t want, int64_t least, const Space& space) 
 
 template <bool AL, bool BL>
 int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const char* who) {
-    const int64_t big = ceil_div(g.m, 256) * ceil_div(g.n, 256);
-    const int64_t mid = ceil_div(g.m, 128) * ceil_div(g.n, 128), small = ceil_div(g.m, 64) * ceil_div(g.n, 64);
-    if (big >= kCus / 2) {
-        choose_splits(g, 1, 1, space);
-        return launch_product<256, 256, 2, 2, 1, AL, BL, true, false>(g, stream, who);
-    }
-    if (mid >= kCus) {
-        choose_splits(g, 1, 1, space);
-        return launch_product<128, 128, 2, 2, 1, AL, BL, true, false>(g, stream, who);
-    }
-    choose_splits(g, kCus / small, 8, space);
+    Way best = way_of(256, 1, g);
+    for (int tile : {128, 64})
+        for (int64_t fill : {int64_t(0), int64_t(kCus), int64_t(2 * kCus)}) {
+            const Way w = way_of(tile, splits_for(tile, fill, g, space), g);
+            if (w.us < best.us) best = w;
+        }
+    split(g, best.splits, space);
+    if (best.tile == 256) return launch_product<256, 256, 2, 2, 1, AL, BL, true, false>(g, stream, who);
+    if (best.tile == 128) return launch_product<128, 128, 2, 2, 1, AL, BL, true, false>(g, stream, who);
     return launch_product<64, 64, 1, 1, 4, AL, BL, true, false>(g, stream, who);
 }
 
@@ -1441,8 +1473,7 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
     }
     if ((!a_ok && !pa) || cols < std::min<int64_t>(g.n, 256)) {
         Product s = g;
-        const int64_t tiles = ceil_div(g.m, 128) * ceil_div(g.n, 128);
-        choose_splits(s, ceil_div(kCus, tiles), 4, whole);
+        split(s, splits_for(128, 2 * kCus, s, whole), whole);
         if constexpr (AL) {
             if (fp8) return launch_product<128, 128, 2, 2, 1, AL, BL, false, true>(s, stream, who);
         }
