@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 
 #include "fsdp_linear.h"
 #include "internal.h"
@@ -35,7 +36,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 // Vectors that may start at any element: gfx950's global accesses take any
 // alignment, so these are still single instructions.
@@ -238,6 +241,16 @@ __device__ __forceinline__ void store8(float* p, int cnt, const float (&v)[8]) {
     }
 }
 
+// Two of the four E4M3 codes in c (its low or high half) as bf16, exactly.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t widen2_e4m3(uint32_t c) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, HIGH));
+}
+
+__device__ __forceinline__ u32x4 widen_e4m3(uint32_t c0, uint32_t c1) {
+    return u32x4{widen2_e4m3<false>(c0), widen2_e4m3<true>(c0), widen2_e4m3<false>(c1), widen2_e4m3<true>(c1)};
+}
+
 // ---------------------------------------------------------------- epilogue
 
 struct Epilogue {
@@ -345,21 +358,31 @@ __device__ __forceinline__ void tile_at(int id, int tm, int tn, int* ti, int* tj
     *tj = in / rows;
 }
 
-// LDS images of one operand's tile of `kBK` contraction elements, in 16-byte
-// slots.  l-major: slot = row * 8 + place, and place holds chunk place ^ (row
-// mod 8) of the row, so that the 8 rows which 8 lanes read at one chunk lie on
-// different banks.
-__device__ __forceinline__ int lmajor_chunk(int slot) { return (slot & 7) ^ ((slot >> 3) & 7); }
-// Row-of-outputs ("o-major"): slot = l * (width / 8) + place.  A transpose
-// read takes 32 bytes (16 outputs) of 4 consecutive l in each 16 lanes, so
-// whole 32-byte pairs of chunks are moved, by l mod 4 and bit 3 of l: the 8
-// rows that half a wave reads lie on different banks.
-__device__ __forceinline__ int omajor_swizzle(int l) { return (l & 3) | ((l >> 1) & 4); }
-template <int W>
+// LDS images of one operand's tile of kBK contraction elements, in 16-byte
+// slots of E = 8 bf16 or 16 E4M3 codes.  l-major: slot = row * (kBK / E) +
+// place, and a row's chunks are permuted among its places by the row, so that
+// the 8 rows which 8 lanes read at one chunk lie on different banks: by row mod
+// 8 where a row is 128 bytes, by row / 2 mod 4 where two are.
+template <int E>
+__device__ __forceinline__ int lmajor_swizzle(int row) {
+    return E == 8 ? row & 7 : (row >> 1) & 3;
+}
+template <int E>
+__device__ __forceinline__ int lmajor_chunk(int slot) {
+    return (slot & (kBK / E - 1)) ^ lmajor_swizzle<E>(slot / (kBK / E));
+}
+// Row-of-outputs ("o-major"): slot = l * (width / E) + place.  A transpose
+// read takes 16 outputs of several consecutive l in each 16 lanes: 32 bytes of
+// 4 l (bf16), so pairs of chunks are moved, by l mod 4 and bit 3 of l; or 16
+// bytes of 8 l (E4M3), moved by l mod 16.  The rows that half a wave reads then
+// lie on different banks.
+template <int W, int E>
+__device__ __forceinline__ int omajor_swizzle(int l) {
+    return E == 8 ? (((l & 3) | ((l >> 1) & 4)) & (W / 16 - 1)) << 1 : l & (W / 16 - 1);
+}
+template <int W, int E>
 __device__ __forceinline__ int omajor_chunk(int slot) {
-    constexpr int kRow = W / 8;
-    const int l = slot / kRow, place = slot % kRow;
-    return place ^ ((omajor_swizzle(l) & (W / 16 - 1)) << 1);
+    return slot % (W / E) ^ omajor_swizzle<W, E>(slot / (W / E));
 }
 
 using Lds = __attribute__((address_space(3))) uint8_t;
@@ -369,11 +392,12 @@ constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset past every range 
 // Copies one operand's tile from memory to LDS without passing through
 // registers.  What lies outside the matrix comes as zeros: buffer loads are
 // checked against a range, and such lanes' offsets lie beyond it.  Needs
-// 16-byte aligned rows and lengths that are multiples of 8, so that no 16-byte
+// 16-byte aligned rows and lengths that are multiples of E, so that no 16-byte
 // chunk is partly outside.
-template <int W, int THREADS, bool LMAJOR>
+template <int W, int THREADS, bool LMAJOR, int E>
 struct DirectTile {
-    static constexpr int kLoads = W * (kBK / 8) / THREADS;
+    static constexpr int kBytes = 16 / E;  // of an element
+    static constexpr int kLoads = W * (kBK / E) / THREADS;
     const uint8_t* base;  // the tile's first row and column at this contraction index
     int64_t step;         // bytes per kBK contraction elements
     int left;             // contraction elements from here to the end, may be negative
@@ -382,24 +406,24 @@ struct DirectTile {
     uint32_t off[kLoads];
 
     __device__ __forceinline__ void init(const void* p, int64_t ld, int o0, int no, int l0, int lend, int tid) {
-        row = static_cast<int>(ld * 2);
+        row = static_cast<int>(ld * kBytes);
         left = lend - l0;
         if (LMAJOR) {
-            base = static_cast<const uint8_t*>(p) + o0 * (ld * 2) + static_cast<int64_t>(l0) * 2;
-            step = kBK * 2;
-            chunk = lmajor_chunk(tid) * 8;
+            base = static_cast<const uint8_t*>(p) + o0 * (ld * kBytes) + static_cast<int64_t>(l0) * kBytes;
+            step = kBK * kBytes;
+            chunk = lmajor_chunk<E>(tid) * E;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int r = (i * THREADS + tid) >> 3;
-                off[i] = o0 + r < no ? static_cast<uint32_t>(r * row + chunk * 2) : kOutside;
+                const int r = (i * THREADS + tid) / (kBK / E);
+                off[i] = o0 + r < no ? static_cast<uint32_t>(r * row + chunk * kBytes) : kOutside;
             }
         } else {
-            base = static_cast<const uint8_t*>(p) + l0 * (ld * 2) + static_cast<int64_t>(o0) * 2;
-            step = kBK * (ld * 2);
+            base = static_cast<const uint8_t*>(p) + l0 * (ld * kBytes) + static_cast<int64_t>(o0) * kBytes;
+            step = kBK * (ld * kBytes);
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int slot = i * THREADS + tid, c = omajor_chunk<W>(slot);
-                off[i] = o0 + c * 8 < no ? static_cast<uint32_t>(slot / (W / 8) * row + c * 16) : kOutside;
+                const int slot = i * THREADS + tid, c = omajor_chunk<W, E>(slot);
+                off[i] = o0 + c * E < no ? static_cast<uint32_t>(slot / (W / E) * row + c * 16) : kOutside;
             }
         }
     }
@@ -450,11 +474,11 @@ struct StagedTile {
             int cnt;  // elements of this chunk inside the matrix
             if (LMAJOR) {
                 row = o0 + (slot >> 3);
-                col = l0 + lmajor_chunk(slot) * 8;
+                col = l0 + lmajor_chunk<8>(slot) * 8;
                 cnt = row < no ? static_cast<int>(min(static_cast<int64_t>(8), nl - col)) : 0;
             } else {
                 row = l0 + slot / (W / 8);
-                col = o0 + omajor_chunk<W>(slot) * 8;
+                col = o0 + omajor_chunk<W, 8>(slot) * 8;
                 cnt = row < nl ? static_cast<int>(min(static_cast<int64_t>(8), no - col)) : 0;
             }
             if (FP8) {
@@ -495,13 +519,7 @@ struct StagedTile {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             u32x4 w = reg[i];
-            if (FP8) {
-                const uint32_t c0 = w[0], c1 = w[1];
-                w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, false));
-                w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, true));
-                w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, false));
-                w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, true));
-            }
+            if (FP8) w = widen_e4m3(w[0], w[1]);
             *(__attribute__((address_space(3))) u32x4*)(dst + (i * THREADS + tid) * 16) = w;
         }
     }
@@ -510,33 +528,47 @@ struct StagedTile {
 // One lane's operand of a 16x16x32 matrix instruction from a tile's LDS image:
 // lane l holds output o0 + l mod 16 and contraction elements 8 (l / 16) + 0..7
 // of the 32 that start at 32 * kk.
-template <int W, bool LMAJOR, int NF>
+template <int W, bool LMAJOR, int NF, int E>
 struct Fragments {
-    int at[LMAJOR ? 1 : NF];
+    using Raw = std::conditional_t<E == 8, bf16x8, u32x2>;  // 8 bf16 or 8 codes
+    static constexpr int kRow = LMAJOR ? kBK * (16 / E) : W * (16 / E);  // bytes of an LDS row
+    int at[LMAJOR ? (E == 8 ? 1 : 2) : NF];
 
     __device__ __forceinline__ void init(int o0, int lane) {
         const int lo = lane & 15, g = lane >> 4;
         if (LMAJOR) {
-            at[0] = (o0 + lo) * 128 + ((g ^ (lo & 7)) << 4);
+            at[0] = (o0 + lo) * kRow + ((E == 8 ? g : g >> 1) ^ lmajor_swizzle<E>(lo)) * 16;
+            if (E == 16) {
+                at[0] += (g & 1) * 8;
+                at[E == 16] = at[0] ^ 32;
+            }
         } else {
-            const int sw = ((lo >> 2) | ((g & 1) << 2)) & (W / 16 - 1);
+            const int l = E == 8 ? g * 8 + (lo >> 2) : g * 8 + (lo >> 1);
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
-                at[f] = (g * 8 + (lo >> 2)) * (W * 2) + (((o0 >> 4) + f) ^ sw) * 32 + (lo & 3) * 8;
+            for (int f = 0; f < NF; ++f) {
+                const int chunk = (o0 / 16 + f) * (16 / E) ^ omajor_swizzle<W, E>(l);
+                at[f] = l * kRow + chunk * 16 + (E == 8 ? lo & 3 : lo & 1) * 8;
+            }
         }
     }
 
-    __device__ __forceinline__ bf16x8 get(const Lds* tile, int f, int kk) const {
-        if (LMAJOR) {
+    __device__ __forceinline__ Raw get(const Lds* tile, int f, int kk) const {
+        if constexpr (LMAJOR && E == 8) {
             // chunk 4 kk + g: kk flips bit 2 of the place
-            return *(const __attribute__((address_space(3))) bf16x8*)(tile + (at[0] ^ (kk << 6)) + f * (16 * 128));
-        } else {
+            return *(const __attribute__((address_space(3))) bf16x8*)(tile + (at[0] ^ (kk << 6)) + f * (16 * kRow));
+        } else if constexpr (LMAJOR) {
+            // chunk 2 kk + g / 2: kk flips bit 1
+            return *(const __attribute__((address_space(3))) u32x2*)(tile + at[kk] + f * (16 * kRow));
+        } else if constexpr (E == 8) {
             using P = __attribute__((address_space(3))) s16x4*;
-            const Lds* q = tile + at[f] + kk * 32 * (W * 2);
+            const Lds* q = tile + at[f] + kk * 32 * kRow;
             const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)q);
-            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 4 * (W * 2)));
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 4 * kRow));
             const struct { s16x4 x, y; } xy = {x, y};
             return __builtin_bit_cast(bf16x8, xy);
+        } else {
+            using P = __attribute__((address_space(3))) i32x2*;
+            return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((P)(tile + at[f] + kk * 32 * kRow)));
         }
     }
 };
@@ -587,7 +619,8 @@ template <int BM, int BN, int WI, int WJ, int KW, bool AL, bool BL, bool DIRECT,
 __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
     static_assert(KW == 1 || (WI == 1 && WJ == 1 && BM == 64 && BN == 64 && DIRECT), "");
     constexpr int kThreads = WI * WJ * 64, kWM = BM / WI, kWN = BN / WJ, kFI = kWM / 16, kFJ = kWN / 16;
-    constexpr int kStage = (BM + BN) * kBK * 2;
+    constexpr int kEB = DIRECT && FP8 ? 16 : 8;  // elements of B in 16 bytes of LDS
+    constexpr int kStage = (BM + BN) * kBK * 2;  // B's part is half filled by codes
     constexpr bool kShared = KW == 1;  // the waves share their stages
     __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage * KW];
     __shared__ __attribute__((aligned(1024))) uint8_t s1[kStage * KW];
@@ -619,8 +652,8 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
 #pragma unroll
         for (int j = 0; j < kFJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    Fragments<BM, AL, kFI> fa;
-    Fragments<BN, BL, kFJ> fb;
+    Fragments<BM, AL, kFI, 8> fa;
+    Fragments<BN, BL, kFJ, kEB> fb;
     fa.init(wi * kWM, lane);
     fb.init(wj * kWN, lane);
 
@@ -630,23 +663,41 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
     // read, a whole step ahead of its use; so the one barrier of a step, in
     // its middle, finds everything that it waits for already there.
     bf16x8 a[2][kFI], b[2][kFJ];
+    u32x2 codes[kFJ];  // E4M3: the next half's, until they are widened
     // Fragment f of a half, in the order in which multiplying needs them.
     auto read = [&](const Lds* stage, int kk, int f) {
-        if (f < kFJ) b[kk][f] = fb.get(stage + BM * kBK * 2, f, kk);
-        else a[kk][f - kFJ] = fa.get(stage, f - kFJ, kk);
+        if (f < kFJ) {
+            if constexpr (kEB == 8) b[kk][f] = fb.get(stage + BM * kBK * 2, f, kk);
+            else codes[f] = fb.get(stage + BM * kBK * 2, f, kk);
+        } else {
+            a[kk][f - kFJ] = fa.get(stage, f - kFJ, kk);
+        }
+    };
+    // Instruction c of the 4 kFJ that widen a half's codes.
+    auto widen_step = [&](int kk, int c) {
+        u32x4 w = __builtin_bit_cast(u32x4, b[kk][c / 4]);
+        w[c % 4] = c % 2 ? widen2_e4m3<true>(codes[c / 4][c % 4 / 2]) : widen2_e4m3<false>(codes[c / 4][c % 4 / 2]);
+        b[kk][c / 4] = __builtin_bit_cast(bf16x8, w);
     };
     // Half kk, product by product, with the reads of the other half (of
     // `stage`) and a refill's loads between them one at a time: a product
     // keeps the matrix unit for 16 cycles, in which one other access can be
     // issued, and with one wave a SIMD nothing else covers a longer run of
-    // them.  The reads end early enough to have come when the half does.
+    // them.  The reads end early enough to have come when the half does, B's
+    // first, whose codes are widened between the later products.
     auto multiply = [&](int kk, const Lds* stage, auto&& between) {
         constexpr int kAll = kFI * kFJ, kGap = kAll >= 64 ? 3 : 1;
+        constexpr int kFirst = kAll >= 64 ? 28 : 8, kWiden = kFJ * 4 / (kAll - kFirst) + (kFJ * 4 % (kAll - kFirst) != 0);
 #pragma unroll
         for (int t = 0; t < kAll; ++t) {
             mfma(acc[t / kFJ][t % kFJ], b[kk][t % kFJ], a[kk][t / kFJ]);
             __builtin_amdgcn_sched_barrier(0);
             if (t % kGap == 0 && t / kGap < kFI + kFJ) read(stage, 1 - kk, t / kGap);
+            if constexpr (kEB == 16) {
+#pragma unroll
+                for (int c = (t - kFirst) * kWiden; c < (t - kFirst + 1) * kWiden; ++c)
+                    if (c >= 0 && c < kFJ * 4) widen_step(1 - kk, c);
+            }
             between(t, kAll);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -662,6 +713,16 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
         settle(acc);
 #pragma unroll
         for (int f = 0; f < kFI + kFJ; ++f) read(l0, 0, f);
+        if constexpr (kEB == 16) {
+#pragma unroll
+            for (int c = 0; c < kFJ * 4; ++c) widen_step(0, c);
+            // as settle(): operands that other units wrote, before the first product
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j) asm volatile("" : "+v"(b[0][j]));
+            asm volatile("s_nop 3" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j) asm volatile("" : "+v"(b[0][j]));
+        }
         // Two steps a turn, so that each LDS access names its stage.  An odd
         // count takes one more step, over zeros.
         int turns = (steps + 1) / 2;
@@ -669,11 +730,12 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
             step(l0, l1);
             step(l1, l0);
         } while (--turns > 0);
+        settle(acc);
     };
     if (steps > 0) {
         if constexpr (DIRECT) {
-            DirectTile<BM, kThreads, AL> ta;
-            DirectTile<BN, kThreads, BL> tb;
+            DirectTile<BM, kThreads, AL, 8> ta;
+            DirectTile<BN, kThreads, BL, kEB> tb;
             ta.init(g.a, g.lda, i0, g.m, kbeg, kend, tid);
             tb.init(g.b, g.ldb, j0, g.n, kbeg, kend, tid);
             constexpr int kLoads = ta.kLoads + tb.kLoads;
@@ -691,7 +753,7 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
             for (int q = 0; q < kLoads; ++q) fetch(l1, q);
             run([&](Lds* stage, int i, int n) {
                 const int every = n / kLoads;
-                if (i % every == every - 1) fetch(stage, i / every);
+                if (i % every == every - 1 && i / every < kLoads) fetch(stage, i / every);
             });
         } else {
             StagedTile<BM, kThreads, AL, false> ta;
@@ -718,7 +780,6 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
         }
     }
 
-    settle(acc);
     // Lane l holds of each 16x16 block output row l mod 16 and columns
     // 4 (l / 16) + 0..3.
     const int lo = lane & 15, hi = lane >> 4;
@@ -849,14 +910,6 @@ __device__ __forceinline__ u32x4 row8(const uint16_t* row, int k, int len) {
         w[s / 2] |= c << (16 * (s & 1));
     }
     return w;
-}
-
-// 8 E4M3 codes as bf16, exactly.
-__device__ __forceinline__ u32x4 widen_e4m3(uint32_t c0, uint32_t c1) {
-    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, false)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, true)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, false)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, true))};
 }
 
 __device__ __forceinline__ u32x4 row16(const uint8_t* row, int k, int len) {
@@ -1302,10 +1355,10 @@ int32_t launched(const char* who) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Rows on 16-byte boundaries and lengths in whole 16-byte chunks; a tile's
-// rows within the 31 bits of a buffer offset.
-bool direct_ok(const void* p, int64_t ld, int64_t rows, int64_t cols) {
-    return aligned(p, 16) && cols % 8 == 0 && (ld % 8 == 0 || rows <= 1) && ld <= (int64_t(1) << 21);
+// Rows on 16-byte boundaries and lengths in whole 16-byte chunks of e elements;
+// a tile's rows within the 31 bits of a buffer offset.
+bool direct_ok(const void* p, int64_t ld, int64_t rows, int64_t cols, int e) {
+    return aligned(p, 16) && cols % e == 0 && (ld % e == 0 || rows <= 1) && ld <= (int64_t(1) << 21);
 }
 
 template <int BM, int BN, int WI, int WJ, int KW, bool AL, bool BL, bool DIRECT, bool FP8>
@@ -1390,7 +1443,7 @@ void split(Product& g, int64_t splits, const Space& space) {
     g.part = reinterpret_cast<float*>(space.p);
 }
 
-template <bool AL, bool BL>
+template <bool AL, bool BL, bool FP8>
 int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const char* who) {
     Way best = way_of(256, 1, g);
     for (int tile : {128, 64})
@@ -1399,9 +1452,9 @@ int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const cha
             if (w.us < best.us) best = w;
         }
     split(g, best.splits, space);
-    if (best.tile == 256) return launch_product<256, 256, 2, 2, 1, AL, BL, true, false>(g, stream, who);
-    if (best.tile == 128) return launch_product<128, 128, 2, 2, 1, AL, BL, true, false>(g, stream, who);
-    return launch_product<64, 64, 1, 1, 4, AL, BL, true, false>(g, stream, who);
+    if (best.tile == 256) return launch_product<256, 256, 2, 2, 1, AL, BL, true, FP8>(g, stream, who);
+    if (best.tile == 128) return launch_product<128, 128, 2, 2, 1, AL, BL, true, FP8>(g, stream, who);
+    return launch_product<64, 64, 1, 1, 4, AL, BL, true, FP8>(g, stream, who);
 }
 
 template <int MB, int JB>
@@ -1469,7 +1522,8 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
     if (!b_ok) {
         const int64_t one = BL ? ceil_div(g.k, 8) * 16 : static_cast<int64_t>(g.k) * 2;  // bytes of a column's part
         const int64_t most = (space.left - 256) / std::max<int64_t>(1, one);
-        if (most < (cols + 7) / 8 * 8) cols = most / 256 * 256;
+        // equal pieces, in whole tiles
+        if (most < (cols + 7) / 8 * 8) cols = std::min<int64_t>(most, ceil_div(cols, ceil_div(cols, std::max<int64_t>(1, most))) + 255) / 256 * 256;
     }
     if ((!a_ok && !pa) || cols < std::min<int64_t>(g.n, 256)) {
         Product s = g;
@@ -1506,7 +1560,10 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
             const int32_t st = launched(who);
             if (st != FSDP_OK) return st;
         }
-        const int32_t st = run_direct<AL, BL>(s, rest, stream, who);
+        const bool codes = fp8 && b_ok;
+        int32_t st;
+        if constexpr (AL) st = codes ? run_direct<AL, BL, true>(s, rest, stream, who) : run_direct<AL, BL, false>(s, rest, stream, who);
+        else st = run_direct<AL, BL, false>(s, rest, stream, who);
         if (st != FSDP_OK) return st;
     }
     return FSDP_OK;
@@ -1524,9 +1581,14 @@ int32_t run_product(Product& g, bool fp8, void* workspace, int64_t bytes, hipStr
         }
     }
     const Space space(workspace, bytes);
-    const bool a_ok = direct_ok(g.a, g.lda, AL ? g.m : g.k, AL ? g.k : g.m);
-    const bool b_ok = !fp8 && direct_ok(g.b, g.ldb, BL ? g.n : g.k, BL ? g.k : g.n);
-    if (a_ok && b_ok) return run_direct<AL, BL>(g, space, stream, who);
+    const bool a_ok = direct_ok(g.a, g.lda, AL ? g.m : g.k, AL ? g.k : g.m, 8);
+    const bool b_ok = direct_ok(g.b, g.ldb, BL ? g.n : g.k, BL ? g.k : g.n, fp8 ? 16 : 8);
+    if (a_ok && b_ok) {
+        if constexpr (AL) {
+            if (fp8) return run_direct<AL, BL, true>(g, space, stream, who);
+        }
+        return run_direct<AL, BL, false>(g, space, stream, who);
+    }
     return run_packed<AL, BL>(g, fp8, a_ok, b_ok, space, stream, who);
 }
 
