@@ -261,7 +261,7 @@ struct Epilogue {
     const float* scale;  // the product is divided by it; null: 1
     int64_t ldo, ldr, ldz;
     Mask mask;
-    int64_t n, j0;  // the whole matrix's columns, and the first of this product's among them (a multiple of 8)
+    int64_t n, i0, j0;  // the whole matrix's columns; the first row and column of this product in it (j0 a multiple of 8)
     int32_t out_f32, act;
 };
 
@@ -308,7 +308,7 @@ __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int st
     if (e.mask.t) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-            drop8(v[b], e.mask, off, static_cast<uint64_t>(row + b * step) * ((e.n + 7) >> 3) + ((e.j0 + j) >> 3));
+            drop8(v[b], e.mask, off, static_cast<uint64_t>(e.i0 + row + b * step) * ((e.n + 7) >> 3) + ((e.j0 + j) >> 3));
     }
     if (e.res) {
 #pragma unroll
@@ -1026,13 +1026,15 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
 
 // ---------------------------------------------------------------- operands laid out anew
 
-// A matrix as the direct loads want it: bf16 rows on 16-byte boundaries, their
-// length rounded up to 8 with zeros.
+// A matrix as the direct loads want it: bf16 rows whose length is rounded up to
+// 8 with zeros, on 128-byte boundaries, so that the 128 bytes of a row which a
+// stage takes are one cache line (rows 8208 bytes apart took a 4096 x 2048 x
+// 4097 product from 60 to 101 us).
 struct Pack {
     const void* src;
     uint16_t* dst;
     int64_t ld;
-    int32_t rows, cols, chunks, fp8;  // chunks: 16-byte pieces of a packed row
+    int32_t rows, cols, chunks, pitch, fp8;  // chunks: 16-byte pieces of a row; pitch: elements between packed rows
 };
 constexpr int kPackBlock = 256;
 __global__ __launch_bounds__(kPackBlock) void pack_kernel(Pack a, Pack b, int blocks_a) {
@@ -1059,7 +1061,7 @@ __global__ __launch_bounds__(kPackBlock) void pack_kernel(Pack a, Pack b, int bl
     } else {
         v = row8(static_cast<const uint16_t*>(p.src) + row * p.ld, c * 8, p.cols);
     }
-    *reinterpret_cast<u32x4*>(p.dst + static_cast<int64_t>(id) * 8) = v;
+    *reinterpret_cast<u32x4*>(p.dst + static_cast<int64_t>(row) * p.pitch + c * 8) = v;
 }
 
 // ---------------------------------------------------------------- elementwise passes
@@ -1411,16 +1413,18 @@ struct Way {
 //     128-tiles 130.
 //   128: two workgroups a CU share its matrix units.  2048 x 4096 x 4096: 60
 //     us, by 256-tiles 81.
-//   64: one workgroup a CU, four waves on four parts of a step.  1024 x 1024 x
-//     4096: 17 us, by 128-tiles 42, by those split in four 22.
+//   64: one workgroup a CU, four waves on four parts of a step, which takes
+//     more where B is read by its columns.  1024 x 1024 x 4096: 17 us, by
+//     128-tiles 42, by those split in four 22.
 //   A split's sums go to memory and back at 6 TB/s, and the join is a launch.
 //     64 x 1024 x 4096 by 64-tiles: 15.5 us, split in 16 9.8.
+template <bool BL>
 Way way_of(int tile, int64_t splits, const Product& g) {
     const double tiles = static_cast<double>(ceil_div(g.m, tile)) * ceil_div(g.n, tile) * splits;
     const double steps = static_cast<double>(ceil_div(ceil_div(g.k, kBK), splits));
     double us = 3;
     if (tile == 256) us += std::ceil(tiles / kCus) * (10 + (1 + 0.5 * std::min(1.0, tiles / kCus)) * steps);
-    else if (tile == 64) us += std::ceil(tiles / kCus) * (3 + 0.165 * steps);
+    else if (tile == 64) us += std::ceil(tiles / kCus) * (3 + (BL ? 0.165 : 0.2) * steps);
     else if (tiles <= kCus) us += 3 + 0.57 * steps;
     else us += std::ceil(tiles / (2 * kCus)) * (4 + 0.9 * steps);
     if (splits > 1) us += 3 + 8.0 * splits * g.m * g.pitch / 6e6;
@@ -1443,14 +1447,81 @@ void split(Product& g, int64_t splits, const Space& space) {
     g.part = reinterpret_cast<float*>(space.p);
 }
 
-template <bool AL, bool BL, bool FP8>
-int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const char* who) {
-    Way best = way_of(256, 1, g);
+// Columns [j0, j0 + n) of the product.
+template <bool BL>
+Product columns(const Product& g, bool fp8, int64_t j0, int64_t n) {
+    Product s = g;
+    const int64_t e = fp8 ? 1 : 2, oe = g.e.out_f32 ? 4 : 2;
+    s.b = static_cast<const uint8_t*>(g.b) + (BL ? j0 * g.ldb : j0) * e;
+    s.n = static_cast<int32_t>(n);
+    s.pitch = (s.n + 7) / 8 * 8;
+    s.e.out = static_cast<uint8_t*>(g.e.out) + j0 * oe;
+    if (g.e.res) s.e.res = static_cast<const uint8_t*>(g.e.res) + j0 * oe;
+    if (g.e.z) s.e.z = g.e.z + j0;
+    if (g.e.bias) s.e.bias = g.e.bias + j0;
+    s.e.j0 += j0;
+    return s;
+}
+
+// Rows [i0, i0 + m) of the product.
+template <bool AL>
+Product rows(const Product& g, int64_t i0, int64_t m) {
+    Product s = g;
+    const int64_t oe = g.e.out_f32 ? 4 : 2;
+    s.a = static_cast<const uint8_t*>(g.a) + (AL ? i0 * g.lda : i0) * 2;
+    s.m = static_cast<int32_t>(m);
+    s.e.out = static_cast<uint8_t*>(g.e.out) + i0 * g.e.ldo * oe;
+    if (g.e.res) s.e.res = static_cast<const uint8_t*>(g.e.res) + i0 * g.e.ldr * oe;
+    if (g.e.z) s.e.z = g.e.z + i0 * g.e.ldz;
+    s.e.i0 += i0;
+    return s;
+}
+
+template <bool BL>
+Way best_way(const Product& g, const Space& space) {
+    Way best = way_of<BL>(256, 1, g);
     for (int tile : {128, 64})
         for (int64_t fill : {int64_t(0), int64_t(kCus), int64_t(2 * kCus)}) {
-            const Way w = way_of(tile, splits_for(tile, fill, g, space), g);
+            const Way w = way_of<BL>(tile, splits_for(tile, fill, g, space), g);
             if (w.us < best.us) best = w;
         }
+    return best;
+}
+
+// Where to cut `along` output rows (columns) into whole rounds of 256-tiles and
+// a rest: 0 if there is no such place.
+int64_t round_cut(int64_t along, int64_t across) {
+    const int64_t tiles = ceil_div(across, 256), all = ceil_div(along, 256);
+    const int64_t cut = tiles * all / kCus * kCus / tiles * 256;
+    return cut < along ? cut : 0;
+}
+
+// The whole product in its best way, or cut in two where a round of the chip
+// would be for a few tiles only (4096 x 4104 x 4096: 256 tiles and 16 of 8
+// columns each: 122 us, whole 178).
+template <bool AL, bool BL, bool FP8>
+int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const char* who) {
+    const Way best = best_way<BL>(g, space);
+    const int64_t cj = round_cut(g.n, g.m), ci = round_cut(g.m, g.n);
+    double us = best.us;
+    int cut = 0;
+    if (cj > 0) {
+        const double c = best_way<BL>(columns<BL>(g, FP8, 0, cj), space).us + best_way<BL>(columns<BL>(g, FP8, cj, g.n - cj), space).us;
+        if (c < us) {
+            us = c;
+            cut = 1;
+        }
+    }
+    if (ci > 0) {
+        const double c = best_way<BL>(rows<AL>(g, 0, ci), space).us + best_way<BL>(rows<AL>(g, ci, g.m - ci), space).us;
+        if (c < us) cut = 2;
+    }
+    if (cut != 0) {
+        Product p = cut == 1 ? columns<BL>(g, FP8, 0, cj) : rows<AL>(g, 0, ci);
+        Product q = cut == 1 ? columns<BL>(g, FP8, cj, g.n - cj) : rows<AL>(g, ci, g.m - ci);
+        const int32_t st = run_direct<AL, BL, FP8>(p, space, stream, who);
+        return st != FSDP_OK ? st : run_direct<AL, BL, FP8>(q, space, stream, who);
+    }
     split(g, best.splits, space);
     if (best.tile == 256) return launch_product<256, 256, 2, 2, 1, AL, BL, true, FP8>(g, stream, who);
     if (best.tile == 128) return launch_product<128, 128, 2, 2, 1, AL, BL, true, FP8>(g, stream, who);
@@ -1468,7 +1539,7 @@ int32_t launch_few(const Product& g, bool fp8, hipStream_t stream, const char* w
 // The features of a workgroup: x is read again by each, W's rows once, and the
 // CU with the most workgroups ends last; so the least rounds * (bytes of x and
 // W of one).  11008 features of 4096 E4M3 codes, 16 tokens: 48 a workgroup (230
-// workgroups) %FEW%
+// workgroups) take 12.4 us, 32 (344) 17.
 template <int MB>
 int32_t run_few(const Product& g, bool fp8, hipStream_t stream, const char* who) {
     int best = 0;
@@ -1488,25 +1559,11 @@ int32_t run_few(const Product& g, bool fp8, hipStream_t stream, const char* who)
     }
 }
 
-// Columns [j0, j0 + n) of the product.
-template <bool BL>
-Product columns(const Product& g, bool fp8, int32_t j0, int32_t n) {
-    Product s = g;
-    const int64_t e = fp8 ? 1 : 2, oe = g.e.out_f32 ? 4 : 2;
-    s.b = static_cast<const uint8_t*>(g.b) + (BL ? j0 * g.ldb : j0) * e;
-    s.n = n;
-    s.pitch = (n + 7) / 8 * 8;
-    s.e.out = static_cast<uint8_t*>(g.e.out) + j0 * oe;
-    if (g.e.res) s.e.res = static_cast<const uint8_t*>(g.e.res) + j0 * oe;
-    if (g.e.z) s.e.z = g.e.z + j0;
-    if (g.e.bias) s.e.bias = g.e.bias + j0;
-    s.e.j0 = j0;
-    return s;
-}
+int64_t packed_pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
 
 Pack pack_of(const void* src, int64_t ld, int64_t rows, int64_t cols, bool fp8, void* dst) {
     return Pack{src, static_cast<uint16_t*>(dst), ld, static_cast<int32_t>(rows), static_cast<int32_t>(cols),
-                static_cast<int32_t>(ceil_div(cols, 8)), fp8};
+                static_cast<int32_t>(ceil_div(cols, 8)), static_cast<int32_t>(packed_pitch(cols)), fp8};
 }
 
 // The product with operands that are not as the direct loads want them: laid
@@ -1517,13 +1574,13 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
                    const char* who) {
     const int64_t ar = AL ? g.m : g.k, ac = AL ? g.k : g.m;
     Space space = whole;
-    void* pa = a_ok ? nullptr : space.take(ar * ceil_div(ac, 8) * 16);
+    void* pa = a_ok ? nullptr : space.take(ar * packed_pitch(ac) * 2);
     int64_t cols = g.n;  // output columns at a time
     if (!b_ok) {
-        const int64_t one = BL ? ceil_div(g.k, 8) * 16 : static_cast<int64_t>(g.k) * 2;  // bytes of a column's part
+        const int64_t one = BL ? packed_pitch(g.k) * 2 : static_cast<int64_t>(g.k) * 2;  // bytes of a column's part
         const int64_t most = (space.left - 256) / std::max<int64_t>(1, one);
         // equal pieces, in whole tiles
-        if (most < (cols + 7) / 8 * 8) cols = std::min<int64_t>(most, ceil_div(cols, ceil_div(cols, std::max<int64_t>(1, most))) + 255) / 256 * 256;
+        if (most < packed_pitch(cols)) cols = std::min<int64_t>(most, ceil_div(cols, ceil_div(cols, std::max<int64_t>(1, most))) + 255) / 256 * 256;
     }
     if ((!a_ok && !pa) || cols < std::min<int64_t>(g.n, 256)) {
         Product s = g;
@@ -1535,7 +1592,7 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
     }
     for (int64_t j0 = 0; j0 < g.n; j0 += cols) {
         const int64_t n = std::min<int64_t>(cols, g.n - j0);
-        Product s = columns<BL>(g, fp8, static_cast<int32_t>(j0), static_cast<int32_t>(n));
+        Product s = columns<BL>(g, fp8, j0, n);
         Space rest = space;
         Pack a{}, b{};
         int64_t blocks_a = 0, blocks_b = 0;
@@ -1545,14 +1602,14 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
                 blocks_a = ceil_div(ar * a.chunks, kPackBlock);
             }
             s.a = pa;
-            s.lda = ceil_div(ac, 8) * 8;
+            s.lda = packed_pitch(ac);
         }
         if (!b_ok) {
             const int64_t br = BL ? n : g.k, bc = BL ? g.k : n;
-            b = pack_of(s.b, g.ldb, br, bc, fp8, rest.take(br * ceil_div(bc, 8) * 16));
+            b = pack_of(s.b, g.ldb, br, bc, fp8, rest.take(br * packed_pitch(bc) * 2));
             blocks_b = ceil_div(br * b.chunks, kPackBlock);
             s.b = b.dst;
-            s.ldb = b.chunks * 8;
+            s.ldb = b.pitch;
         }
         if (blocks_a + blocks_b > 0) {
             pack_kernel<<<dim3(static_cast<uint32_t>(blocks_a + blocks_b)), dim3(kPackBlock), 0, stream>>>(
