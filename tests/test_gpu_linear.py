@@ -83,6 +83,14 @@ def close(got, ref, err, dtype, what):
                            f"{np.argwhere(bad)[0].tolist()}, {got[bad][0]} against {ref[bad][0]}")
 
 
+def product(a, b):
+    """The oracle's product; the same two sums by the GPU in float64 where the host would take seconds."""
+    if a.shape[0] * b.shape[0] * a.shape[1] < 3e8:
+        return OL.product(a, b)
+    x, y = (torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in (a, b.T))
+    return (x @ y).cpu().numpy(), (x.abs() @ y.abs()).cpu().numpy()
+
+
 def product_err(length, s):
     return (length / 32 + 104) * 2 * U * s
 
@@ -140,7 +148,7 @@ def check_forward(m, n, k, space, wt="bf16", yt="bf16", act="none", bias=False, 
                           z=z.ptr if keep_z else None, dropout=d, workspace=space, ldy=y.ld, ldx=x.ld, ldw=w.ld,
                           ldr=r.ld if res else None, ldz=z.ld if keep_z else None)
     torch.cuda.synchronize()
-    zv, s = OL.product(x.np(), wv)
+    zv, s = product(x.np(), wv)
     if bias:
         zv = zv + b.np()
     ez = product_err(k, s) + 4 * U * (s + np.abs(zv))
@@ -176,6 +184,39 @@ def test_forward_shapes(gpu, space, m, n, k, wt):
 def test_forward_many_tiles(gpu, space, m, n, k):
     check_forward(m, n, k, space, act="gelu", bias=True, res=True, keep_z=True, p=0.1)
     check_forward(m, n, k, space, "e4m3", yt="f32")
+
+
+# Sizes for each way to compute a product: 256-tiles (ragged in every length),
+# 128-tiles, 64-tiles, split ones, and ones that are cut after their whole
+# rounds of 256-tiles, by columns and by rows.
+WAYS = [(4000, 4080, 1008), (2048, 2064, 336), (520, 1040, 1008), (300, 128, 8208), (4096, 4112, 1024), (4104, 4096, 1024)]
+
+
+@pytest.mark.parametrize("m,n,k", WAYS)
+def test_ways(gpu, space, m, n, k):
+    check_forward(m, n, k, space, act="silu", bias=True, res=True, keep_z=True, p=0.1)
+    check_forward(m, n, k, space, "e4m3", yt="f32", res=True, same=True, p=0.5)
+    check_grad_input(m, k, n, space)
+    check_grad_input(m, k, n, space, "e4m3")
+    check_grad_weight(k, m, n, space, "bf16", True)
+    check_grad_weight(k, m, n, space, "f32", False)
+
+
+@pytest.mark.parametrize("m,n,k", [(300, 1000, 1365), (600, 1543, 515), (64, 100, 333)])
+@pytest.mark.parametrize("size", [0, 1 << 10, 600 << 10, 1 << 20, 2 << 20, 5 << 20])
+def test_small_workspaces(gpu, m, n, k, size):
+    """Operands that have to be laid out anew, with room for neither, for some
+    of their columns at a time, for one, for both; what lies behind the
+    workspace stays."""
+    buf = torch.full((size + 64,), 0x5A, dtype=torch.uint8, device=gpu)
+    ws = buf[:size] if size else None
+    check_forward(m, n, k, ws, act="gelu", bias=True, res=True, keep_z=True, p=0.2)
+    check_forward(m, n, k, ws, "e4m3", off=3, pad=2)
+    check_grad_input(m, n, k, ws, "e4m3")
+    check_grad_input(m, n, k, ws, off=1)
+    check_grad_weight(m, n, k, ws, "f32", True)
+    check_backward(m, n, ws, "silu", 0.1)
+    assert bool((buf[size:] == 0x5A).all())
 
 
 @pytest.mark.parametrize("act,bias,res,keep_z,p,yt", [
@@ -291,7 +332,7 @@ def check_grad_input(m, n, k, space, wt="bf16", off=0, pad=0, seed=2):
     B.fsdp_linear_grad_input(dx.ptr, dz.ptr, w.ptr, m, n, k, w_dtype=wt, w_scale=scale, workspace=space,
                              lddx=dx.ld, lddz=dz.ld, ldw=w.ld)
     torch.cuda.synchronize()
-    v, s = OL.product(dz.np(), wv.T)
+    v, s = product(dz.np(), wv.T)
     close(dx.np(), v, product_err(n, s) + 4 * U * s, "bf16", "dx")
     dx.check_surroundings()
 
@@ -308,7 +349,7 @@ def check_grad_weight(m, n, k, space, dt="bf16", add=False, off=0, pad=0, seed=3
     B.fsdp_linear_grad_weight(dw.ptr, dz.ptr, x.ptr, m, n, k, dw_dtype=dt, accumulate=add, workspace=space,
                               lddw=dw.ld, lddz=dz.ld, ldx=x.ld)
     torch.cuda.synchronize()
-    v, s = OL.product(dz.np().T, x.np().T)
+    v, s = product(dz.np().T, x.np().T)
     close(dw.np(), v + old, product_err(m, s) + 2 * U * np.abs(v + old), dt, "dw")
     dw.check_surroundings()
 
