@@ -1190,11 +1190,17 @@ __device__ __forceinline__ void put_db(void* db, int f32, int accumulate, int64_
     }
 }
 
-__global__ __launch_bounds__(kElemBlock) void epilogue_backward_kernel(BackwardArgs a) {
-    __shared__ float sums[kElemBlock][9];
-    const int tid = threadIdx.x, per = kElemBlock >> a.g.tx, width = 1 << a.g.tx;
+// BLOCK 256: a row block's sums of its columns.  BLOCK 1024 is the form for
+// few rows, 4 lanes a row and every row in one block, so that the sums need no
+// second launch.
+constexpr int kTallBlock = 1024;
+template <int BLOCK>
+__global__ __launch_bounds__(BLOCK) void epilogue_backward_kernel(BackwardArgs a) {
+    __shared__ float sums[BLOCK == kElemBlock ? BLOCK : 64][9];
+    const int tid = threadIdx.x, per = BLOCK >> a.g.tx, width = 1 << a.g.tx;
     const int64_t rb = blockIdx.x / a.g.cblocks;
-    const int64_t j = ((static_cast<int64_t>(blockIdx.x % a.g.cblocks) << a.g.tx) + (tid & (width - 1))) * 8;
+    const int64_t j0 = (static_cast<int64_t>(blockIdx.x % a.g.cblocks) << a.g.tx) * 8;
+    const int64_t j = j0 + (tid & (width - 1)) * 8;
     const int cnt = static_cast<int>(min(a.n - j, static_cast<int64_t>(8)));  // <= 0 outside
     const int64_t chunks = (a.n + 7) >> 3, end = cnt > 0 ? min(a.m, (rb + 1) * a.g.rows) : 0;
     const uint64_t off = mask_offset(a.mask);
@@ -1210,15 +1216,28 @@ __global__ __launch_bounds__(kElemBlock) void epilogue_backward_kernel(BackwardA
         if (a.dz) stream_store8(a.dz + i * a.lddz + j, cnt, a.wt, v);
     }
     if (!a.sums) return;
+    int places = per;  // of sums a column in LDS
+    if constexpr (BLOCK == kElemBlock) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sums[tid][q] = sum[q];
+        for (int q = 0; q < 8; ++q) sums[tid][q] = sum[q];
+    } else {
+        // first over the wave's rows: lanes of one column chunk are 4 apart
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+            for (int d = 4; d < 64; d <<= 1) sum[q] += __shfl_xor(sum[q], d);
+        places = BLOCK / 64;
+        if ((tid & 63) < 4)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) sums[(tid >> 6) * 4 + (tid & 3)][q] = sum[q];
+    }
     __syncthreads();
-    // thread t of the block's first ones: column t of the block, over its rows in order
-    for (int t = tid; t < width * 8; t += kElemBlock) {
-        const int64_t col = (static_cast<int64_t>(blockIdx.x % a.g.cblocks) << a.g.tx) * 8 + t;
+    // thread t of the block's first ones: column t of the block, over its places in order
+    for (int t = tid; t < width * 8; t += BLOCK) {
+        const int64_t col = j0 + t;
         if (col >= a.n) break;
         float s = 0;
-        for (int r = 0; r < per; ++r) s += sums[r * width + (t >> 3)][t & 7];
+        for (int r = 0; r < places; ++r) s += sums[r * width + (t >> 3)][t & 7];
         if (a.part) a.part[rb * a.n + col] = s;
         else put_db(a.db, a.db_f32, a.accumulate, col, s);
     }
@@ -1631,15 +1650,18 @@ int32_t run_product(Product& g, bool fp8, void* workspace, int64_t bytes, hipStr
     if (g.m == 0 || g.n == 0) return FSDP_OK;
     g.pitch = (g.n + 7) / 8 * 8;
     g.e.n = g.n;
+    const Space space(workspace, bytes);
+    const bool a_ok = direct_ok(g.a, g.lda, AL ? g.m : g.k, AL ? g.k : g.m, 8);
+    const bool b_ok = direct_ok(g.b, g.ldb, BL ? g.n : g.k, BL ? g.k : g.n, fp8 ? 16 : 8);
     if constexpr (AL && BL) {
-        if (g.m <= 32) {
+        // Up to 16 tokens, and up to 32 where the tiles would need operands laid
+        // out anew.  32 tokens by 64-tiles: [4096, 11008] 23 us, this way 35;
+        // [11008, 4096] 23 and 24.  16 tokens of [4096, 4096]: 13 and 10.
+        if (g.m <= 16 || (g.m <= 32 && !(a_ok && b_ok))) {
             g.splits = 1;
             return g.m <= 16 ? run_few<1>(g, fp8, stream, who) : run_few<2>(g, fp8, stream, who);
         }
     }
-    const Space space(workspace, bytes);
-    const bool a_ok = direct_ok(g.a, g.lda, AL ? g.m : g.k, AL ? g.k : g.m, 8);
-    const bool b_ok = direct_ok(g.b, g.ldb, BL ? g.n : g.k, BL ? g.k : g.n, fp8 ? 16 : 8);
     if (a_ok && b_ok) {
         if constexpr (AL) {
             if (fp8) return run_direct<AL, BL, true>(g, space, stream, who);
@@ -1805,6 +1827,10 @@ Grid elementwise_grid(int64_t m, int64_t n, int64_t rows_max, int64_t* blocks) {
     return g;
 }
 
+// Rows up to which one workgroup takes a column block's whole height.  333 x
+// 1024: 6.5 us, by row blocks and a second launch 9.0; 600 x 4096: 11.7 and 10.7.
+constexpr int64_t kTallRows = 512;
+
 int32_t epilogue_backward_impl(uint16_t* dz, int64_t lddz, void* db, int32_t db_dtype, int32_t accumulate,
                                const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int32_t act,
                                const fsdp_dropout_mask* dropout, int64_t m, int64_t n, void* workspace,
@@ -1844,16 +1870,21 @@ int32_t epilogue_backward_impl(uint16_t* dz, int64_t lddz, void* db, int32_t db_
     a.accumulate = accumulate;
     a.act = act;
     a.sums = db != nullptr;
-    const int64_t cblocks = ceil_div(ceil_div(n, 8), 64);
     a.wt = stream_ok(dz, lddz, 2);
+    if (db && m <= kTallRows) {
+        a.g = Grid{2, static_cast<int32_t>(ceil_div(n, 32)), kTallRows};
+        epilogue_backward_kernel<kTallBlock><<<dim3(static_cast<uint32_t>(a.g.cblocks)), dim3(kTallBlock), 0, stream>>>(a);
+        return launched(who);
+    }
+    const int64_t cblocks = ceil_div(ceil_div(n, 8), 64);
+    // 24 workgroups a CU: 59 us for 4096 x 11008; 16 take 62, 8 66, 32 64
     int64_t want = 24 * kCus / cblocks;
     if (db) want = std::min(want, std::min(workspace_bytes, FSDP_LINEAR_WORKSPACE_BYTES) / (4 * n));
     int64_t blocks;
     a.g = elementwise_grid(m, n, std::max<int64_t>(1, want), &blocks);
-    if (m == 0) blocks = 1;  // db = 0
     a.part = db && blocks > 1 ? static_cast<float*>(workspace) : nullptr;
     if (blocks * a.g.cblocks > 0x7fffff) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
-    epilogue_backward_kernel<<<dim3(static_cast<uint32_t>(blocks * a.g.cblocks)), dim3(kElemBlock), 0, stream>>>(a);
+    epilogue_backward_kernel<kElemBlock><<<dim3(static_cast<uint32_t>(blocks * a.g.cblocks)), dim3(kElemBlock), 0, stream>>>(a);
     TRY(launched(who));
     if (!a.part) return FSDP_OK;
     column_sum_kernel<<<dim3(static_cast<uint32_t>(ceil_div(n, 64))), dim3(kSumBlock), 0, stream>>>(
