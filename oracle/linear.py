@@ -40,11 +40,11 @@ def philox(counter, key):
     return c
 
 
-def keep_factor(rows, cols, p, seed, offset):
-    """The mask's factors, [rows, cols]: 0 where dropped."""
+def keep_factor(rows, cols, p, seed, offset, first=0):
+    """The mask's factors of `rows` rows from `first` on, [rows, cols]: 0 where dropped."""
     t = int(np.rint(p * 65536.0))
     per_row = (cols + 7) // 8
-    block = np.arange(rows * per_row, dtype=np.uint64)
+    block = np.arange(rows * per_row, dtype=np.uint64) + np.uint64(first * per_row)
     seed, offset = int(seed) & ((1 << 64) - 1), int(offset) & ((1 << 64) - 1)
     words = philox((block & np.uint64(M32), block >> np.uint64(32),
                     np.full_like(block, offset & M32), np.full_like(block, offset >> 32)),

@@ -1376,6 +1376,9 @@ int32_t launched(const char* who) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Workgroups of one launch: its threads are counted in 32 bits.
+constexpr int64_t kMaxBlocks = 0x3fffff;
+
 // Rows on 16-byte boundaries and lengths in whole 16-byte chunks of e elements;
 // a tile's rows within the 31 bits of a buffer offset.
 bool direct_ok(const void* p, int64_t ld, int64_t rows, int64_t cols, int e) {
@@ -1388,7 +1391,7 @@ int32_t launch_product(Product& g, hipStream_t stream, const char* who) {
     g.tn = static_cast<int32_t>(ceil_div(g.n, BN));
     const int64_t blocks = static_cast<int64_t>(g.tm) * g.tn * g.splits;
     const int64_t joins = ceil_div(static_cast<int64_t>(g.m) * (g.pitch / 8), kJoinBlock);
-    if (blocks > 0x7fffff || (g.splits > 1 && joins > 0x7fffff))
+    if (blocks > kMaxBlocks || (g.splits > 1 && joins > kMaxBlocks))
         return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
     product_kernel<BM, BN, WI, WJ, KW, AL, BL, DIRECT, FP8>
         <<<dim3(static_cast<uint32_t>(blocks)), dim3(WI * WJ * KW * 64), 0, stream>>>(g);
@@ -1422,6 +1425,7 @@ struct Way {
     int64_t splits;
     double us;
 };
+constexpr double kNoWay = 1e30;
 
 // What a product takes in microseconds, from times measured over products of
 // one 64 x 64 tile to 8192 x 8192 x 8192 on MI355X; within a fifth of most of
@@ -1447,7 +1451,7 @@ Way way_of(int tile, int64_t splits, const Product& g) {
     else if (tiles <= kCus) us += 3 + 0.57 * steps;
     else us += std::ceil(tiles / (2 * kCus)) * (4 + 0.9 * steps);
     if (splits > 1) us += 3 + 8.0 * splits * g.m * g.pitch / 6e6;
-    return Way{tile, splits, us};
+    return Way{tile, splits, tiles > kMaxBlocks ? kNoWay : us};
 }
 
 // The splits that fill `fill` workgroups, at least two steps each, partial sums
@@ -1521,6 +1525,7 @@ int64_t round_cut(int64_t along, int64_t across) {
 template <bool AL, bool BL, bool FP8>
 int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const char* who) {
     const Way best = best_way<BL>(g, space);
+    if (best.us == kNoWay) return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
     const int64_t cj = round_cut(g.n, g.m), ci = round_cut(g.m, g.n);
     double us = best.us;
     int cut = 0;
@@ -1570,6 +1575,8 @@ int32_t run_few(const Product& g, bool fp8, hipStream_t stream, const char* who)
             cost = c;
         }
     }
+    if (ceil_div(g.n, 16 * best) > kMaxBlocks)
+        return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
     switch (best) {
         case 1: return launch_few<MB, 1>(g, fp8, stream, who);
         case 2: return launch_few<MB, 2>(g, fp8, stream, who);
@@ -1650,6 +1657,9 @@ int32_t run_product(Product& g, bool fp8, void* workspace, int64_t bytes, hipStr
     if (g.m == 0 || g.n == 0) return FSDP_OK;
     g.pitch = (g.n + 7) / 8 * 8;
     g.e.n = g.n;
+    // The stride of a single row says nothing; its length stands for it.
+    if ((AL ? g.m : g.k) <= 1) g.lda = ((AL ? g.k : g.m) + 15) / 16 * 16;
+    if ((BL ? g.n : g.k) <= 1) g.ldb = ((BL ? g.k : g.n) + 15) / 16 * 16;
     const Space space(workspace, bytes);
     const bool a_ok = direct_ok(g.a, g.lda, AL ? g.m : g.k, AL ? g.k : g.m, 8);
     const bool b_ok = direct_ok(g.b, g.ldb, BL ? g.n : g.k, BL ? g.k : g.n, fp8 ? 16 : 8);
@@ -1871,7 +1881,7 @@ int32_t epilogue_backward_impl(uint16_t* dz, int64_t lddz, void* db, int32_t db_
     a.act = act;
     a.sums = db != nullptr;
     a.wt = stream_ok(dz, lddz, 2);
-    if (db && m <= kTallRows) {
+    if (db && m <= kTallRows && n <= 32 * (kMaxBlocks / 2)) {
         a.g = Grid{2, static_cast<int32_t>(ceil_div(n, 32)), kTallRows};
         epilogue_backward_kernel<kTallBlock><<<dim3(static_cast<uint32_t>(a.g.cblocks)), dim3(kTallBlock), 0, stream>>>(a);
         return launched(who);
@@ -1883,7 +1893,7 @@ int32_t epilogue_backward_impl(uint16_t* dz, int64_t lddz, void* db, int32_t db_
     int64_t blocks;
     a.g = elementwise_grid(m, n, std::max<int64_t>(1, want), &blocks);
     a.part = db && blocks > 1 ? static_cast<float*>(workspace) : nullptr;
-    if (blocks * a.g.cblocks > 0x7fffff) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
+    if (blocks * a.g.cblocks > kMaxBlocks) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
     epilogue_backward_kernel<kElemBlock><<<dim3(static_cast<uint32_t>(blocks * a.g.cblocks)), dim3(kElemBlock), 0, stream>>>(a);
     TRY(launched(who));
     if (!a.part) return FSDP_OK;
@@ -1920,7 +1930,7 @@ int32_t dropout_impl(void* y, int64_t ldy, const void* x, int64_t ldx, const voi
     a.wt = stream_ok(y, ldy, e);
     int64_t blocks;
     a.g = elementwise_grid(rows, cols, 16 * kCus / ceil_div(ceil_div(cols, 8), 64), &blocks);
-    if (blocks * a.g.cblocks > 0x7fffff) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
+    if (blocks * a.g.cblocks > kMaxBlocks) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
     const dim3 grid(static_cast<uint32_t>(blocks * a.g.cblocks));
     if (e == 2) dropout_kernel<uint16_t><<<grid, dim3(kElemBlock), 0, stream>>>(a);
     else dropout_kernel<float><<<grid, dim3(kElemBlock), 0, stream>>>(a);

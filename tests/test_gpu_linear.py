@@ -696,3 +696,69 @@ def test_layer_between_two_steps(gpu, space, copy):
                     d, s = OL.product(v[da].T, v[xa].T)
                     close(slices[i][rank].double().cpu().numpy().reshape(shapes[i]), d, product_err(m, s), "bf16",
                           f"slice {i}")
+
+
+# ---------------------------------------------------------------- strides of one row, offsets past 32 bits
+
+@pytest.mark.parametrize("ld", [0, 1, 5, 1 << 40])
+def test_the_stride_of_a_single_row_says_nothing(gpu, space, ld):
+    g = gen(31)
+    n, k = 72, 136
+    x, w = randn(g, 1, k).bfloat16(), randn(g, n, k).bfloat16()
+    dz, one = randn(g, 1, n).bfloat16(), randn(g, 1, k).bfloat16()
+    pairs = []
+    for s in (None, ld):
+        y, dx = torch.empty(1, n, device=gpu), torch.empty(1, k, dtype=torch.bfloat16, device=gpu)
+        dw, out = torch.empty(n, k, device=gpu), torch.empty(300, 1, device=gpu)
+        dxw = torch.empty(300, k, dtype=torch.bfloat16, device=gpu)
+        B.fsdp_linear_forward(y, x, w, 1, n, k, y_dtype="f32", workspace=space, ldx=s, ldy=s)
+        B.fsdp_linear_grad_input(dx, dz, w, 1, n, k, workspace=space, lddz=s, lddx=s)
+        B.fsdp_linear_grad_weight(dw, dz, x, 1, n, k, dw_dtype="f32", workspace=space, lddz=s, ldx=s)
+        many = torch.ones(300, k, dtype=torch.bfloat16, device=gpu)
+        B.fsdp_linear_forward(out, many, one, 300, 1, k, y_dtype="f32", workspace=space, ldw=s)
+        B.fsdp_linear_grad_input(dxw, torch.ones(300, 1, dtype=torch.bfloat16, device=gpu), one, 300, 1, k,
+                                 workspace=space, ldw=s)
+        pairs.append([y, dx, dw, out, dxw])
+    for a, b in zip(*pairs):
+        assert torch.equal(a, b)
+    assert torch.equal(pairs[0][2], dz.float().t() * x.float())
+    assert torch.equal(pairs[0][4], one.expand(300, k))
+
+
+def test_offsets_past_32_bits(gpu, space):
+    """2.2 G elements a matrix: products, gradients and dropout, on rows from all
+    over it."""
+    m, n, k = (1 << 21) + 5, 1032, 16
+    g = gen(41)
+    x, w = randn(g, m, k).bfloat16(), randn(g, n, k).bfloat16()
+    d = dict(p=0.25, seed=6, offset=7)
+    y = torch.empty(m, n, dtype=torch.bfloat16, device=gpu)
+    rows = [0, 1, 65, m // 2, (1 << 32) // (2 * n), (1 << 31) // n, (1 << 32) // (2 * n) + 1, m - 70, m - 1]
+    B.fsdp_linear_forward(y, x, w, m, n, k, dropout=d, workspace=space)
+    keep = np.concatenate([OL.keep_factor(1, n, **d, first=r) for r in rows])
+    xv, wv = x[rows].double().cpu().numpy(), w.double().cpu().numpy()
+    v, s = OL.product(xv, wv)
+    close(y[rows].double().cpu().numpy(), v * keep, product_err(k, s) * keep + 4 * U * np.abs(v * keep), "bf16", "y")
+    # the gradients, with y as dz: every row counts in dW
+    dx = torch.empty(m, k, dtype=torch.bfloat16, device=gpu)
+    B.fsdp_linear_grad_input(dx, y, w, m, n, k, workspace=space)
+    dv = y[rows].double().cpu().numpy()
+    v, s = OL.product(dv, wv.T)
+    close(dx[rows].double().cpu().numpy(), v, product_err(n, s), "bf16", "dx")
+    dw = torch.empty(n, k, device=gpu)
+    B.fsdp_linear_grad_weight(dw, y, x, m, n, k, dw_dtype="f32", workspace=space)
+    ref, mag = (torch.zeros(n, k, dtype=torch.float64, device=gpu) for _ in range(2))
+    for a in range(0, m, 1 << 18):
+        t, u = y[a:a + (1 << 18)].double(), x[a:a + (1 << 18)].double()
+        ref += t.t().contiguous() @ u
+        mag += t.abs().t().contiguous() @ u.abs()
+    close(dw.double().cpu().numpy(), ref.cpu().numpy(), product_err(m, mag.cpu().numpy()), "f32", "dw")
+    # the elementwise passes, in place
+    before = y[rows].double().cpu().numpy()
+    B.fsdp_dropout(y, y, m, n, "bf16", d)
+    once = y[rows].double().cpu().numpy()
+    close(once, before * keep, 4 * U * np.abs(before * keep), "bf16", "dropout")
+    db = torch.empty(n, device=gpu)
+    B.fsdp_linear_epilogue_backward(y, y, m, n, dropout=d, db=db, workspace=space)
+    again = y[rows].double().cpu().numpy()
+    close(again, once * keep, 4 * U * np.abs(once) * keep, "bf16", "dz")

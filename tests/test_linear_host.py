@@ -163,6 +163,17 @@ def test_refusals(call, kw, code):
     assert e.value.name == code, str(e.value)
 
 
+def test_more_tiles_than_a_launch():
+    """Refused before any device work, on every way's path."""
+    far = dict(x=1 << 40, w=1 << 42, y=1 << 50)
+    big = 1 << 30
+    for kw in (dict(m=big, n=big, k=8), dict(m=big, n=big, k=7), dict(m=16, n=big, k=8, w=1 << 44),
+               dict(m=big, n=big, k=16, w_dtype="e4m3", w_scale=64)):
+        with pytest.raises(B.FsdpError) as e:
+            forward(**{**far, **kw})
+        assert e.value.name == "FSDP_E_CAPACITY", (kw, str(e.value))
+
+
 def test_reserved_and_null_record():
     L = B.lib()
     assert L.fsdp_linear_forward(None, None) == -1

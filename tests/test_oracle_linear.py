@@ -36,6 +36,11 @@ def test_mask_element_by_element():
             assert f[i, j] == (65536 / (65536 - t) if bits >= t else 0.0)
 
 
+def test_mask_of_later_rows():
+    whole = OL.keep_factor(20, 33, 0.4, 8, 9)
+    assert np.array_equal(whole[7:], OL.keep_factor(13, 33, 0.4, 8, 9, first=7))
+
+
 @pytest.mark.parametrize("p", [0.0, 2.0 ** -17, 2.0 ** -16, 0.1, 0.5, 1.0 - 2.0 ** -16, 1.0])
 def test_mask_rate(p):
     f = OL.keep_factor(256, 256, p, 1, 2)
