@@ -621,6 +621,56 @@ def test_parts_of_a_packed_projection(gpu, space):
         at += n
 
 
+def test_captured_training_step(gpu, space):
+    """Forward, backward and the optimizer's step in one graph, with dropout's
+    offset read from the count that the step advances: replays equal the eager
+    calls at t = 1, 2, 3, with eager work between them."""
+    from rank_step_amd.workloads import HPARAMS
+    m, n, k = 48, 136, 264
+    g = gen(51)
+    x, dy = randn(g, m, k).bfloat16(), randn(g, m, n).bfloat16()
+    p0 = randn(g, n, k, 0.05)
+
+    class Run:
+        def __init__(self):
+            self.p, self.m, self.v = p0.clone(), torch.zeros_like(p0), torch.zeros_like(p0)
+            self.w, self.dw = p0.bfloat16(), torch.zeros(n, k, dtype=torch.bfloat16, device=gpu)
+            self.y, self.z, self.dz = (torch.zeros(m, n, dtype=torch.bfloat16, device=gpu) for _ in range(3))
+            self.db = torch.zeros(n, device=gpu)
+            self.plan = B.MtPlan([{"param_fp32": self.p, "exp_avg": self.m, "exp_avg_sq": self.v,
+                                   "grad_slices": self.dw, "slice_stride": n * k, "unshard_bf16_out": self.w,
+                                   "shard_numel": n * k, "valid": n * k}], 1, "bf16")
+
+        def layer(self, mask):
+            B.fsdp_linear_forward(self.y, x, self.w, m, n, k, act="silu", z=self.z, dropout=mask, workspace=space)
+            B.fsdp_linear_epilogue_backward(self.dz, dy, m, n, z=self.z, act="silu", dropout=mask, db=self.db,
+                                            workspace=space)
+            B.fsdp_linear_grad_weight(self.dw, self.dz, x, m, n, k, workspace=space)
+
+        def out(self):
+            return [t.clone() for t in (self.p, self.m, self.v, self.w, self.dw, self.y, self.dz, self.db)]
+
+    eager, graphed = Run(), Run()
+    count = torch.zeros(1, dtype=torch.int64, device=gpu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        graphed.layer(dict(p=0.3, seed=8, offset=1 << 40, offset_dev=count))
+        graphed.plan.step_capturable(HPARAMS, count)
+    for t in (1, 2, 3):
+        eager.layer(dict(p=0.3, seed=8, offset=(1 << 40) + t - 1))
+        eager.plan.step(HPARAMS, t)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(count) == t
+        for i, (a, b) in enumerate(zip(eager.out(), graphed.out())):
+            assert torch.equal(a, b), (t, i)
+    del graph
+    eager.plan.close()
+    graphed.plan.close()
+
+
 @pytest.mark.parametrize("copy", ["bf16", "e4m3"])
 def test_layer_between_two_steps(gpu, space, copy):
     """A two-layer MLP as a rank runs it: the step writes the weight copies,

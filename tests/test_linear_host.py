@@ -208,3 +208,22 @@ def test_exports_and_constants():
     for name, value in B.ACTIVATIONS.items():
         assert re.search(r"FSDP_ACT_%s = %d\b" % (name.upper(), value), text), name
     assert B.WEIGHT_DTYPES["e4m3"] == int(re.search(r"FSDP_DT_E4M3 = (\d+)", text).group(1))
+
+
+def test_from_plain_c(tmp_path):
+    import json
+    import os
+    import shutil
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("needs a C compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = tmp_path / "linear_from_c"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"),
+                    os.path.join(root, "tests", "c", "linear_from_c.c"), "-o", str(exe), B.lib_path(),
+                    "-Wl,-rpath," + os.path.dirname(B.lib_path())], check=True, timeout=120)
+    got = json.loads(subprocess.run([str(exe)], capture_output=True, text=True, timeout=60, check=True).stdout)
+    assert got["linear"] == ctypes.sizeof(B.Linear) and got["mask"] == ctypes.sizeof(B.DropoutMask)
+    assert got["act_at"] == B.Linear.act.offset
+    assert got["empty"] == 0 and got["bad"] == -1
+    assert got["message"] == "fsdp_linear_forward: unknown activation"
