@@ -44,6 +44,7 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 // alignment, so these are still single instructions.
 struct __attribute__((packed, aligned(2))) Bytes16 { u32x4 v; };
 struct __attribute__((packed, aligned(1))) Bytes8 { uint32_t v[2]; };
+typedef u32x4 u32x4_any __attribute__((aligned(2)));  // for non-temporal accesses
 
 constexpr int kXcds = 8;
 constexpr int kCus = 256;
@@ -253,6 +254,23 @@ __device__ __forceinline__ u32x4 widen_e4m3(uint32_t c0, uint32_t c1) {
 
 // ---------------------------------------------------------------- epilogue
 
+// A product's outputs are not read again by its launch: stored non-temporally
+// they leave L2 to the operands (8192 x 4096 x 11008 581 -> 553 us, 8192 x 8192 x
+// 8192 770 -> 750; written through, 572 and 765).
+__device__ __forceinline__ void output8(uint16_t* p, int cnt, const float (&v)[8]) {
+    if (cnt >= 8) __builtin_nontemporal_store(pack8(v), reinterpret_cast<u32x4_any*>(p));
+    else store8(p, cnt, v);
+}
+
+__device__ __forceinline__ void output8(float* p, int cnt, const float (&v)[8]) {
+    if (cnt >= 8) {
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), reinterpret_cast<u32x4_any*>(p));
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}), reinterpret_cast<u32x4_any*>(p + 4));
+    } else {
+        store8(p, cnt, v);
+    }
+}
+
 struct Epilogue {
     void* out;
     const void* res;  // of out's type: the residual, or out itself to accumulate
@@ -301,7 +319,7 @@ __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int st
     if (e.z) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-            if (row + b * step < m) store8(e.z + (row + b * step) * e.ldz + j, cnt, v[b]);
+            if (row + b * step < m) output8(e.z + (row + b * step) * e.ldz + j, cnt, v[b]);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) activate8(v[b], e.act);
@@ -320,8 +338,8 @@ __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int st
     for (int b = 0; b < NB; ++b) {
         const int64_t i = row + b * step;
         if (i < m) {
-            if (e.out_f32) store8(static_cast<float*>(e.out) + i * e.ldo + j, cnt, v[b]);
-            else store8(static_cast<uint16_t*>(e.out) + i * e.ldo + j, cnt, v[b]);
+            if (e.out_f32) output8(static_cast<float*>(e.out) + i * e.ldo + j, cnt, v[b]);
+            else output8(static_cast<uint16_t*>(e.out) + i * e.ldo + j, cnt, v[b]);
         }
     }
 }
@@ -615,7 +633,7 @@ __device__ __forceinline__ void arrive() {
 // that the registers hold (256 a lane), which needs the fewest LDS and L2 bytes
 // a product; with eight waves of 128 x 64, which read half as much again, an
 // 8192 x 4096 x 4096 weight gradient took 322 us, this way 206 when both were
-// new, 194 now.  8192 x 8192 x 8192: 780 us, 1.41 PFLOP/s (the library's
+// new, 194 now.  8192 x 8192 x 8192: 750 us, 1.47 PFLOP/s (the library's
 // plain product: 1.42).  What bounds it is power: without any memory traffic it
 // takes 5 % fewer cycles, at 2.3 GHz, where with it the clock falls to 1.9; the
 // matrix units are busy in 71 % of the cycles of that weight gradient.  Four
@@ -1092,8 +1110,6 @@ __global__ __launch_bounds__(kPackBlock) void pack_kernel(Pack a, Pack b, int bl
 // eight L2s for its release to write back.  8192 x 4096 bf16 with a residual:
 // 32.1 us (6.3 TB/s), with ordinary accesses 38.8, with non-temporal ones both
 // ways 35.4.
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-
 __device__ __forceinline__ void stream_load8(const uint16_t* p, int cnt, float (&v)[8]) {
     if (cnt >= 8) {
         const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
