@@ -1065,15 +1065,17 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
 
 // ---------------------------------------------------------------- operands laid out anew
 
-// A matrix as the direct loads want it: bf16 rows whose length is rounded up to
-// 8 with zeros, on 128-byte boundaries, so that the 128 bytes of a row which a
-// stage takes are one cache line (rows 8208 bytes apart took a 4096 x 2048 x
-// 4097 product from 60 to 101 us).
+// A matrix as the direct loads want it: rows whose length is rounded up to 16
+// bytes with zeros, on 128-byte boundaries, so that the 128 bytes of a row which
+// a stage takes are one cache line (rows 8208 bytes apart took a 4096 x 2048 x
+// 4097 product from 60 to 101 us).  5 us for a few megabytes, which is a
+// launch's latency, then 4 TB/s; the loads through registers, which need no
+// copy, took 25 us instead of 17 for the 1000 x 1024 x 1365 forward product.
 struct Pack {
     const void* src;
-    uint16_t* dst;
+    uint8_t* dst;
     int64_t ld;
-    int32_t rows, cols, chunks, pitch, fp8;  // chunks: 16-byte pieces of a row; pitch: elements between packed rows
+    int32_t rows, cols, chunks, pitch, fp8;  // chunks: 16-byte pieces of a row; pitch: bytes between packed rows
 };
 constexpr int kPackBlock = 256;
 __global__ __launch_bounds__(kPackBlock) void pack_kernel(Pack a, Pack b, int blocks_a) {
@@ -1083,24 +1085,9 @@ __global__ __launch_bounds__(kPackBlock) void pack_kernel(Pack a, Pack b, int bl
     const int row = id / p.chunks, c = id - row * p.chunks;
     if (row >= p.rows) return;
     u32x4 v;
-    if (p.fp8) {
-        const uint8_t* q = static_cast<const uint8_t*>(p.src) + row * p.ld + c * 8;
-        uint32_t w0 = 0, w1 = 0;
-        if (c * 8 + 8 <= p.cols) {
-            const Bytes8 x = *reinterpret_cast<const Bytes8*>(q);
-            w0 = x.v[0];
-            w1 = x.v[1];
-        } else {
-            for (int s = 0; s < p.cols - c * 8; ++s) {
-                if (s < 4) w0 |= static_cast<uint32_t>(q[s]) << (8 * s);
-                else w1 |= static_cast<uint32_t>(q[s]) << (8 * (s - 4));
-            }
-        }
-        v = widen_e4m3(w0, w1);
-    } else {
-        v = row8(static_cast<const uint16_t*>(p.src) + row * p.ld, c * 8, p.cols);
-    }
-    *reinterpret_cast<u32x4*>(p.dst + static_cast<int64_t>(row) * p.pitch + c * 8) = v;
+    if (p.fp8) v = row16(static_cast<const uint8_t*>(p.src) + row * p.ld, c * 16, p.cols);
+    else v = row8(static_cast<const uint16_t*>(p.src) + row * p.ld, c * 8, p.cols);
+    *reinterpret_cast<u32x4*>(p.dst + static_cast<int64_t>(row) * p.pitch + c * 16) = v;
 }
 
 // ---------------------------------------------------------------- elementwise passes
@@ -1626,11 +1613,12 @@ int32_t run_few(const Product& g, bool fp8, hipStream_t stream, const char* who)
     }
 }
 
-int64_t packed_pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
+// Bytes of a packed row.
+int64_t packed_row(int64_t cols, bool fp8) { return ceil_div(cols * (fp8 ? 1 : 2), 128) * 128; }
 
 Pack pack_of(const void* src, int64_t ld, int64_t rows, int64_t cols, bool fp8, void* dst) {
-    return Pack{src, static_cast<uint16_t*>(dst), ld, static_cast<int32_t>(rows), static_cast<int32_t>(cols),
-                static_cast<int32_t>(ceil_div(cols, 8)), static_cast<int32_t>(packed_pitch(cols)), fp8};
+    return Pack{src, static_cast<uint8_t*>(dst), ld, static_cast<int32_t>(rows), static_cast<int32_t>(cols),
+                static_cast<int32_t>(ceil_div(cols, fp8 ? 16 : 8)), static_cast<int32_t>(packed_row(cols, fp8)), fp8};
 }
 
 // The product with operands that are not as the direct loads want them: laid
@@ -1641,13 +1629,16 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
                    const char* who) {
     const int64_t ar = AL ? g.m : g.k, ac = AL ? g.k : g.m;
     Space space = whole;
-    void* pa = a_ok ? nullptr : space.take(ar * packed_pitch(ac) * 2);
+    void* pa = a_ok ? nullptr : space.take(ar * packed_row(ac, false));
     int64_t cols = g.n;  // output columns at a time
     if (!b_ok) {
-        const int64_t one = BL ? packed_pitch(g.k) * 2 : static_cast<int64_t>(g.k) * 2;  // bytes of a column's part
+        // bytes that a column takes, and that the last one's row is rounded up to
+        const int64_t one = BL ? packed_row(g.k, fp8) : static_cast<int64_t>(g.k) * (fp8 ? 1 : 2);
         const int64_t most = (space.left - 256) / std::max<int64_t>(1, one);
-        // equal pieces, in whole tiles
-        if (most < packed_pitch(cols)) cols = std::min<int64_t>(most, ceil_div(cols, ceil_div(cols, std::max<int64_t>(1, most))) + 255) / 256 * 256;
+        if (most < (cols + 127) / 128 * 128) {  // equal pieces, in whole tiles
+            const int64_t pieces = ceil_div(cols, std::max<int64_t>(1, most));
+            cols = std::min(most, ceil_div(cols, pieces) + 255) / 256 * 256;
+        }
     }
     if ((!a_ok && !pa) || cols < std::min<int64_t>(g.n, 256)) {
         Product s = g;
@@ -1669,14 +1660,14 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
                 blocks_a = ceil_div(ar * a.chunks, kPackBlock);
             }
             s.a = pa;
-            s.lda = packed_pitch(ac);
+            s.lda = packed_row(ac, false) / 2;
         }
         if (!b_ok) {
             const int64_t br = BL ? n : g.k, bc = BL ? g.k : n;
-            b = pack_of(s.b, g.ldb, br, bc, fp8, rest.take(br * packed_pitch(bc) * 2));
+            b = pack_of(s.b, g.ldb, br, bc, fp8, rest.take(br * packed_row(bc, fp8)));
             blocks_b = ceil_div(br * b.chunks, kPackBlock);
             s.b = b.dst;
-            s.ldb = b.pitch;
+            s.ldb = b.pitch / (fp8 ? 1 : 2);
         }
         if (blocks_a + blocks_b > 0) {
             pack_kernel<<<dim3(static_cast<uint32_t>(blocks_a + blocks_b)), dim3(kPackBlock), 0, stream>>>(
@@ -1684,9 +1675,8 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
             const int32_t st = launched(who);
             if (st != FSDP_OK) return st;
         }
-        const bool codes = fp8 && b_ok;
         int32_t st;
-        if constexpr (AL) st = codes ? run_direct<AL, BL, true>(s, rest, stream, who) : run_direct<AL, BL, false>(s, rest, stream, who);
+        if constexpr (AL) st = fp8 ? run_direct<AL, BL, true>(s, rest, stream, who) : run_direct<AL, BL, false>(s, rest, stream, who);
         else st = run_direct<AL, BL, false>(s, rest, stream, who);
         if (st != FSDP_OK) return st;
     }
