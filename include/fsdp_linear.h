@@ -138,9 +138,9 @@ int32_t fsdp_linear_forward(const fsdp_linear* a, hipStream_t stream);
  *   db = column sums of D(dy) * act'(z), taken before dz is rounded, of
  *        db_dtype [n]; added to what db holds if accumulate is 1 (NULL: none)
  * dy: bf16 [m, n].  z: bf16 [m, n] as the forward call stored it; may be NULL
- * when act is FSDP_ACT_NONE.  At z = 0 relu's slope is 0; where a slope or the
- * mask is 0 by selection (dropped elements, relu at z <= 0) dz is 0 whatever
- * dy holds.  The residual's gradient is dy. */
+ * when act is FSDP_ACT_NONE.  At z = 0 relu's slope is 0.  Both select: where
+ * an element is dropped dz is 0 whatever dy and z hold, and where relu has
+ * z <= 0 whatever dy holds.  The residual's gradient is dy. */
 int32_t fsdp_linear_epilogue_backward(uint16_t* dz, int64_t lddz, void* db, int32_t db_dtype,
                                       int32_t accumulate, const uint16_t* dy, int64_t lddy,
                                       const uint16_t* z, int64_t ldz, int32_t act,

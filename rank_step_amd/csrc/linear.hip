@@ -87,9 +87,9 @@ __device__ __forceinline__ u32x4 philox(uint64_t block, uint64_t offset, uint64_
     return u32x4{c0, c1, c2, c3};
 }
 
-// A dropped element is +0 whatever it held, so this selects.
-__device__ __forceinline__ void drop8(float (&v)[8], const Mask& m, uint64_t off, uint64_t block) {
-    const u32x4 w = philox(block, off, m.seed);
+// D with the block's bits.  A dropped element is +0 whatever it held, so this
+// selects.
+__device__ __forceinline__ void select8(float (&v)[8], const Mask& m, const u32x4& w) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         // bits >= t, with the 16 bits in the high half: what is below them cannot
@@ -97,6 +97,10 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Mask& m, uint64_t off
         const uint32_t bits = (i & 1) ? w[i / 2] : w[i / 2] << 16;
         v[i] = bits > m.above ? v[i] * m.scale : 0.0f;
     }
+}
+
+__device__ __forceinline__ void drop8(float (&v)[8], const Mask& m, uint64_t off, uint64_t block) {
+    select8(v, m, philox(block, off, m.seed));
 }
 
 // ---------------------------------------------------------------- activations
@@ -633,10 +637,10 @@ __device__ __forceinline__ void arrive() {
 // that the registers hold (256 a lane), which needs the fewest LDS and L2 bytes
 // a product; with eight waves of 128 x 64, which read half as much again, an
 // 8192 x 4096 x 4096 weight gradient took 322 us, this way 206 when both were
-// new, 194 now.  8192 x 8192 x 8192: 750 us, 1.47 PFLOP/s (the library's
+// new, 193 now.  8192 x 8192 x 8192: 750 us, 1.47 PFLOP/s (the library's
 // plain product: 1.42).  What bounds it is power: without any memory traffic it
 // takes 5 % fewer cycles, at 2.3 GHz, where with it the clock falls to 1.9; the
-// matrix units are busy in 71 % of the cycles of that weight gradient.  Four
+// matrix units are busy in 74 % of the cycles of that weight gradient.  Four
 // stages of 32 (a longer look ahead) were 6 % slower: twice the barriers, and
 // half a cache line a row and load.  A workgroup that stays and fetches its
 // next tile during the epilogue was 2 % slower to 3 % faster.
@@ -1236,8 +1240,13 @@ __global__ __launch_bounds__(BLOCK) void epilogue_backward_kernel(BackwardArgs a
         float v[8], z[8];
         stream_load8(a.dy + i * a.lddy + j, cnt, v);
         if (a.act != FSDP_ACT_NONE) stream_load8(a.z + i * a.ldz + j, cnt, z);
-        if (a.mask.t) drop8(v, a.mask, off, static_cast<uint64_t>(i * chunks + (j >> 3)));
+        // The bits are drawn while the loads are on their way, and select last, so
+        // that a dropped element is 0 whatever dy and z hold (1 % slower than
+        // selecting dy).
+        u32x4 bits = {0, 0, 0, 0};
+        if (a.mask.t) bits = philox(static_cast<uint64_t>(i * chunks + (j >> 3)), off, a.mask.seed);
         activation_grad8(v, z, a.act);
+        if (a.mask.t) select8(v, a.mask, bits);
 #pragma unroll
         for (int q = 0; q < 8; ++q) sum[q] += v[q];
         if (a.dz) stream_store8(a.dz + i * a.lddz + j, cnt, a.wt, v);

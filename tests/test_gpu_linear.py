@@ -433,6 +433,26 @@ def test_epilogue_backward_selects(gpu, space):
     assert torch.equal(db, 2 * keep.sum(0).float())
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("rows", [40, 600])
+def test_epilogue_backward_drops_whatever_z_holds(gpu, space, act, rows):
+    """The forward call drops an element whose z is not finite to +0; so does its gradient."""
+    n = 100
+    d = dict(p=0.5, seed=8, offset=9)
+    keep = torch.from_numpy(OL.keep_factor(rows, n, **d) > 0).to(gpu)
+    for bad in ("nan", "inf", "-inf"):
+        z = torch.where(keep, torch.zeros(rows, n, device=gpu), torch.full((rows, n), float(bad), device=gpu))
+        z = z.to(torch.bfloat16)
+        dy = torch.where(keep, torch.ones_like(z), torch.full_like(z, float("-inf")))
+        dz, db = torch.empty_like(z), torch.empty(n, device=gpu)
+        B.fsdp_linear_epilogue_backward(dz, dy, rows, n, z=z, act=act, dropout=d, db=db, workspace=space)
+        slope = {"none": 1.0, "relu": 0.0}.get(act, 0.5)  # at 0; times the scale 2
+        assert torch.equal(dz, torch.where(keep, torch.full_like(z, 2 * slope), torch.zeros_like(z)))
+        # a slope is off by less than 2^-20 (far below dz's rounding), each of `rows` sums by 2^-24
+        want = 2 * slope * keep.sum(0).double()
+        assert bool(((db.double() - want).abs() <= want * (2.0 ** -20 + rows * 2.0 ** -24)).all())
+
+
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_activation_range(gpu, space, act):
     """The whole range of z: bf16 values from the smallest to the largest."""
