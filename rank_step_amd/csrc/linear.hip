@@ -1630,26 +1630,76 @@ Pack pack_of(const void* src, int64_t ld, int64_t rows, int64_t cols, bool fp8, 
                 static_cast<int32_t>(ceil_div(cols, fp8 ? 16 : 8)), static_cast<int32_t>(packed_row(cols, fp8)), fp8};
 }
 
-// The product with operands that are not as the direct loads want them: laid
-// out anew in the workspace, B by columns of the output if it does not fit at
-// once, or staged through registers where there is no workspace for that.
+int64_t round_up(int64_t x, int64_t a) { return ceil_div(x, a) * a; }
+
+// How a product with unaligned operands is computed: its output in pieces of
+// rows x cols, whose operands are laid out anew one after the other; rows = 0:
+// whole, with the operands staged through registers.
+struct Pieces {
+    int64_t rows, cols;
+    bool by_rows;  // a piece of A serves all pieces of B, not the other way round
+};
+
+// Whole operands where they fit in the workspace; else the pieces of least
+// estimated time, or none.  Small pieces fill the chip badly, and many lay
+// operands out again and again (at 4.5 TB/s and 4 us a launch).  Staged, a
+// 128-tile's step takes 1.5 to 1.8 us where both operands are l-major, 1.7 to
+// 2.4 with an o-major B (5.5 where only one round of workgroups hides its
+// loads), 2.6 to 4.3 with both, against 0.9.  Pieces and staged, with 64 MiB:
+// weight gradient of [4095, 11007] over 8192 tokens 1126 and 3300 us, the input
+// gradient 670 and 1220; forward of 8191 tokens through [11007, 4095] 670 and
+// 1160, but through [4095, 11007], of whose operands only 1500 rows each fit,
+// 1180 staged.  Pieces of B alone are taken for 6 % more, and others for 6 %
+// less: the estimates are no nearer.
+template <bool AL, bool BL, typename FA, typename FB>
+Pieces pieces_of(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space& space, FA bytes_a, FB bytes_b) {
+    if (bytes_a(g.m) + bytes_b(g.n) <= space.left) return {g.m, g.n, true};
+    if (bytes_a(std::min(g.m, 256)) + bytes_b(std::min(g.n, 256)) > space.left) return {0, 0, true};
+    Product s = g;
+    split(s, splits_for(128, 2 * kCus, g, space), space);
+    const double tiles = static_cast<double>(ceil_div(g.m, 128)) * ceil_div(g.n, 128) * s.splits;
+    const double rounds = std::ceil(tiles / (2 * kCus));
+    const double step = AL && BL ? (fp8 ? 1.5 : 1.8) : !AL ? 3.4 : rounds > 1 ? 2.4 : 5.5;
+    double least = 3 + rounds * (4 + step * s.kper / kBK);
+    Pieces best{0, 0, true};
+    for (int64_t na = 1; na <= (a_ok ? 1 : 32); ++na) {
+        const int64_t r = na == 1 ? g.m : std::min<int64_t>(g.m, round_up(ceil_div(g.m, na), 256));
+        const int64_t left = space.left - bytes_a(r);
+        for (int64_t nb = 1; left >= 0 && nb <= (b_ok ? 1 : 32); ++nb) {
+            const int64_t c = nb == 1 ? g.n : std::min<int64_t>(g.n, round_up(ceil_div(g.n, nb), 256));
+            if (bytes_b(c) > left) continue;
+            Space rest = space;
+            rest.take(bytes_a(r) + bytes_b(c));
+            Product p = g;
+            p.m = static_cast<int32_t>(r);
+            p.n = static_cast<int32_t>(c);
+            p.pitch = static_cast<int32_t>(round_up(c, 8));
+            const int64_t ra = ceil_div(g.m, r), cb = ceil_div(g.n, c);
+            const double once = static_cast<double>(bytes_a(r)) * ra, other = static_cast<double>(bytes_b(c)) * cb;
+            const double by_rows = once + other * (cb > 1 ? ra : 1), by_cols = other + once * (ra > 1 ? cb : 1);
+            const double us = ra * cb * (4 + best_way<BL>(p, rest).us) + std::min(by_rows, by_cols) * 2 / 4.5e6;
+            if (us < (na == 1 ? 1.06 : 0.94) * least) {
+                least = us;
+                best = {r, c, by_rows <= by_cols};
+            }
+            break;  // fewer columns a piece only cost more
+        }
+    }
+    return best;
+}
+
+// The product with operands that are not as the direct loads want them.
 template <bool AL, bool BL>
 int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space& whole, hipStream_t stream,
                    const char* who) {
-    const int64_t ar = AL ? g.m : g.k, ac = AL ? g.k : g.m;
-    Space space = whole;
-    void* pa = a_ok ? nullptr : space.take(ar * packed_row(ac, false));
-    int64_t cols = g.n;  // output columns at a time
-    if (!b_ok) {
-        // bytes that a column takes, and that the last one's row is rounded up to
-        const int64_t one = BL ? packed_row(g.k, fp8) : static_cast<int64_t>(g.k) * (fp8 ? 1 : 2);
-        const int64_t most = (space.left - 256) / std::max<int64_t>(1, one);
-        if (most < (cols + 127) / 128 * 128) {  // equal pieces, in whole tiles
-            const int64_t pieces = ceil_div(cols, std::max<int64_t>(1, most));
-            cols = std::min(most, ceil_div(cols, pieces) + 255) / 256 * 256;
-        }
-    }
-    if ((!a_ok && !pa) || cols < std::min<int64_t>(g.n, 256)) {
+    const auto bytes_a = [&](int64_t r) {
+        return a_ok ? 0 : round_up(AL ? r * packed_row(g.k, false) : g.k * packed_row(r, false), 256);
+    };
+    const auto bytes_b = [&](int64_t c) {
+        return b_ok ? 0 : round_up(BL ? c * packed_row(g.k, fp8) : g.k * packed_row(c, fp8), 256);
+    };
+    const Pieces p = pieces_of<AL, BL>(g, fp8, a_ok, b_ok, whole, bytes_a, bytes_b);
+    if (p.rows == 0) {
         Product s = g;
         split(s, splits_for(128, 2 * kCus, s, whole), whole);
         if constexpr (AL) {
@@ -1657,25 +1707,30 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
         }
         return launch_product<128, 128, 2, 2, 1, AL, BL, false, false>(s, stream, who);
     }
-    for (int64_t j0 = 0; j0 < g.n; j0 += cols) {
-        const int64_t n = std::min<int64_t>(cols, g.n - j0);
-        Product s = columns<BL>(g, fp8, j0, n);
-        Space rest = space;
+    Space space = whole;
+    void* const pa = space.take(bytes_a(p.rows));
+    void* const pb = space.take(bytes_b(p.cols));
+    const int64_t na = ceil_div(g.m, p.rows), nb = ceil_div(g.n, p.cols);
+    int64_t has_a = -1, has_b = -1;  // the pieces that lie there
+    for (int64_t t = 0; t < na * nb; ++t) {
+        const int64_t ia = p.by_rows ? t / nb : t % na, ib = p.by_rows ? t % nb : t / na;
+        const int64_t i0 = ia * p.rows, j0 = ib * p.cols;
+        const int64_t m = std::min(p.rows, g.m - i0), n = std::min(p.cols, g.n - j0);
+        Product s = columns<BL>(rows<AL>(g, i0, m), fp8, j0, n);
         Pack a{}, b{};
         int64_t blocks_a = 0, blocks_b = 0;
         if (!a_ok) {
-            if (j0 == 0) {
-                a = pack_of(g.a, g.lda, ar, ac, false, pa);
-                blocks_a = ceil_div(ar * a.chunks, kPackBlock);
-            }
+            a = pack_of(s.a, g.lda, AL ? m : g.k, AL ? g.k : m, false, pa);
+            if (ia != has_a) blocks_a = ceil_div(static_cast<int64_t>(a.rows) * a.chunks, kPackBlock);
+            has_a = ia;
             s.a = pa;
-            s.lda = packed_row(ac, false) / 2;
+            s.lda = a.pitch / 2;
         }
         if (!b_ok) {
-            const int64_t br = BL ? n : g.k, bc = BL ? g.k : n;
-            b = pack_of(s.b, g.ldb, br, bc, fp8, rest.take(br * packed_row(bc, fp8)));
-            blocks_b = ceil_div(br * b.chunks, kPackBlock);
-            s.b = b.dst;
+            b = pack_of(s.b, g.ldb, BL ? n : g.k, BL ? g.k : n, fp8, pb);
+            if (ib != has_b) blocks_b = ceil_div(static_cast<int64_t>(b.rows) * b.chunks, kPackBlock);
+            has_b = ib;
+            s.b = pb;
             s.ldb = b.pitch / (fp8 ? 1 : 2);
         }
         if (blocks_a + blocks_b > 0) {
@@ -1685,8 +1740,8 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
             if (st != FSDP_OK) return st;
         }
         int32_t st;
-        if constexpr (AL) st = fp8 ? run_direct<AL, BL, true>(s, rest, stream, who) : run_direct<AL, BL, false>(s, rest, stream, who);
-        else st = run_direct<AL, BL, false>(s, rest, stream, who);
+        if constexpr (AL) st = fp8 ? run_direct<AL, BL, true>(s, space, stream, who) : run_direct<AL, BL, false>(s, space, stream, who);
+        else st = run_direct<AL, BL, false>(s, space, stream, who);
         if (st != FSDP_OK) return st;
     }
     return FSDP_OK;

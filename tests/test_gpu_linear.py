@@ -219,6 +219,21 @@ def test_small_workspaces(gpu, m, n, k, size):
     assert bool((buf[size:] == 0x5A).all())
 
 
+@pytest.mark.parametrize("mib", [24, 33, 48])
+def test_unaligned_products_in_pieces(gpu, mib):
+    """Large unaligned operands of which neither fits in the workspace: the output
+    in pieces of rows and columns, each with its part of every epilogue operand."""
+    size = mib << 20
+    buf = torch.full((size + 64,), 0x5A, dtype=torch.uint8, device=gpu)
+    ws = buf[:size]
+    check_forward(2999, 2901, 8191, ws, act="silu", bias=True, res=True, keep_z=True, p=0.3)
+    check_forward(2999, 2901, 8191, ws, "e4m3", yt="f32", bias=True, res=True, same=True, p=0.2, off=1)
+    check_grad_input(2999, 8191, 2901, ws)
+    check_grad_input(2999, 8191, 2901, ws, "e4m3", off=3, pad=1)
+    check_grad_weight(8191, 2999, 2901, ws, "f32", True)
+    assert bool((buf[size:] == 0x5A).all())
+
+
 @pytest.mark.parametrize("act,bias,res,keep_z,p,yt", [
     c for i, c in enumerate(itertools.product(["none", "relu", "gelu", "silu"], [False, True], [False, True],
                                               [False, True], [0.0, 0.5], ["bf16", "f32"])) if i % 5 == 0])
