@@ -22,7 +22,8 @@
  * atomics).  Every call can be captured into a HIP graph.  In addition:
  *   - Matrices are row-major with a row stride (ld*) in elements, at least the
  *     row's length; rows may start at any element.  Elements between a row's
- *     end and the next row's start are neither read nor written.
+ *     end and the next row's start are not written, and nothing depends on
+ *     them; reads stay within the aligned 4-byte words of a row's elements.
  *   - A size of 0 is allowed; a buffer without elements may be NULL.  m, n
  *     and k are at most 2^30 (else FSDP_E_CAPACITY).  A product over no terms
  *     is 0.

@@ -941,40 +941,61 @@ __global__ __launch_bounds__(kJoinBlock) void join_kernel(Product g) {
 
 // ---------------------------------------------------------------- products of few rows
 
-// 8 elements of a row from k on, zeros from `len` on; any alignment.
-__device__ __forceinline__ u32x4 row8(const uint16_t* row, int k, int len) {
-    if (k + 8 <= len) return reinterpret_cast<const Bytes16*>(row + k)->v;
-    u32x4 w = {0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-        const uint32_t c = k + s < len ? row[k + s] : 0u;
-        w[s / 2] |= c << (16 * (s & 1));
-    }
-    return w;
+// The 16 bytes at p.  ODD: where p is off a 4-byte boundary a 16-byte load takes
+// several times as long, so they come as the aligned words that hold them (five,
+// and no byte outside those that hold some of the 16) and are moved down.
+template <bool ODD>
+__device__ __forceinline__ u32x4 bytes16(const uint8_t* p) {
+    if constexpr (!ODD) return reinterpret_cast<const Bytes16*>(p)->v;
+    const uint32_t in = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 3, bits = in * 8;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - in);
+    typedef u32x4 Words __attribute__((aligned(4)));
+    const u32x4 w = *reinterpret_cast<const Words*>(q);
+    const uint32_t last = q[in ? 4 : 3];
+    return u32x4{__builtin_amdgcn_alignbit(w[1], w[0], bits), __builtin_amdgcn_alignbit(w[2], w[1], bits),
+                 __builtin_amdgcn_alignbit(w[3], w[2], bits), __builtin_amdgcn_alignbit(last, w[3], bits)};
 }
 
-__device__ __forceinline__ u32x4 row16(const uint8_t* row, int k, int len) {
-    if (k + 16 <= len) return reinterpret_cast<const Bytes16*>(row + k)->v;
+// The same for bytes [at, at + 16) of a row of `len`, zeros from its end on.
+// Past the end, the row's last 16 bytes are read and moved down, so that this is
+// one load too; of a shorter row, each element.
+template <typename T, bool ODD>
+__device__ __forceinline__ u32x4 row_end16(const uint8_t* row, int64_t at, int64_t len) {
     u32x4 w = {0, 0, 0, 0};
+    if (at >= len) return w;
+    if (len < 16) {
 #pragma unroll
-    for (int s = 0; s < 16; ++s) {
-        const uint32_t c = k + s < len ? row[k + s] : 0u;
-        w[s / 4] |= c << (8 * (s & 3));
+        for (int s = 0; s < static_cast<int>(16 / sizeof(T)); ++s) {
+            const int64_t b = at + s * static_cast<int64_t>(sizeof(T));
+            const uint32_t c = b < len ? *reinterpret_cast<const T*>(row + b) : 0u;
+            w[s * sizeof(T) / 4] |= c << (8 * (s * sizeof(T) % 4));
+        }
+        return w;
     }
-    return w;
+    const int64_t from = min(at, len - 16);
+    w = bytes16<ODD>(row + from);
+    const uint32_t back = static_cast<uint32_t>(at - from);
+    if (back & 8) w = u32x4{w[2], w[3], 0, 0};
+    if (back & 4) w = u32x4{w[1], w[2], w[3], 0};
+    const uint32_t bits = (back & 3) * 8;
+    return u32x4{__builtin_amdgcn_alignbit(w[1], w[0], bits), __builtin_amdgcn_alignbit(w[2], w[1], bits),
+                 __builtin_amdgcn_alignbit(w[3], w[2], bits), __builtin_amdgcn_alignbit(0u, w[3], bits)};
 }
 
 // The forward product for at most 16 * MB tokens: bound by reading W once.  One
-// token: [4096, 4096] 8.5 us with the call, [28672, 8192] 87 us (5.4 TB/s), from
-// E4M3 codes 46; sixteen tokens: 10.3, 106 and 62.  Four waves or sixteen a
+// token: [4096, 4096] 8.2 us with the call, [28672, 8192] 90 us (5.2 TB/s), from
+// E4M3 codes 46; sixteen tokens: 10.7, 100 and 59.  Four waves or sixteen a
 // workgroup: 3-15 % slower at most sizes; non-temporal loads of W 8-25 %.  A
 // workgroup takes 16 * JB output features; its eight waves take every eighth
 // chunk of 64 contraction elements, from memory straight into the fragments
 // of the matrix instructions (W is used once, so LDS would only be a detour;
-// x comes from L2), several chunks on their way at a time.  Their sums are
-// added in LDS, so the call is one launch.
+// x comes from L2), several chunks on their way at a time, all of whose loads
+// are issued before the first is used (left to the compiler's order, sixteen
+// tokens of [11008, 4096] take 23.1 us, this way 20.0).  Their sums are added
+// in LDS, so the call is one launch.  ODD: rows off 4-byte boundaries; 16 tokens
+// of [4096, 4095] 17 us, by unaligned loads 30.
 constexpr int kFewWaves = 8;
-template <int MB, int JB, bool FP8>
+template <int MB, int JB, bool FP8, bool ODD>
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
     constexpr int kPitch = 20;  // floats of 16, padded against bank conflicts
     __shared__ __attribute__((aligned(16))) float sums[kFewWaves][MB][JB][16 * kPitch];
@@ -982,11 +1003,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
     const int lo = lane & 15, q = lane >> 4;
     const int j0 = blockIdx.x * (16 * JB);
     // Rows past the end are read as the last one; what they give is not stored.
-    const uint16_t* x[MB];
+    const uint8_t* x[MB];
     const uint8_t* w[JB];
 #pragma unroll
     for (int i = 0; i < MB; ++i)
-        x[i] = static_cast<const uint16_t*>(g.a) + min(i * 16 + lo, g.m - 1) * g.lda;
+        x[i] = static_cast<const uint8_t*>(g.a) + min(i * 16 + lo, g.m - 1) * g.lda * 2;
 #pragma unroll
     for (int j = 0; j < JB; ++j)
         w[j] = static_cast<const uint8_t*>(g.b) + min(j0 + j * 16 + lo, g.n - 1) * g.ldb * (FP8 ? 1 : 2);
@@ -1002,20 +1023,27 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
     struct Chunk {
         u32x4 x[MB][2], w[JB][FP8 ? 1 : 2];
     };
-    auto load = [&](Chunk& c, int k, int len) {
+    // END: the chunk may end behind the rows' end.
+    auto load = [&](Chunk& c, int k, auto end) {
+        auto row16 = [&](const uint8_t* row, int at, auto type) {
+            using T = decltype(type);
+            constexpr int64_t e = sizeof(T);
+            if constexpr (decltype(end)::value) return row_end16<T, ODD>(row, at * e, g.k * e);
+            else return bytes16<ODD>(row + at * e);
+        };
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
-            if (FP8) {
-                c.w[j][0] = row16(w[j], k + q * 16, len);
+            if constexpr (FP8) {
+                c.w[j][0] = row16(w[j], k + q * 16, uint8_t());
             } else {
-                c.w[j][0] = row8(reinterpret_cast<const uint16_t*>(w[j]), k + q * 8, len);
-                c.w[j][FP8 ? 0 : 1] = row8(reinterpret_cast<const uint16_t*>(w[j]), k + 32 + q * 8, len);
+                c.w[j][0] = row16(w[j], k + q * 8, uint16_t());
+                c.w[j][1] = row16(w[j], k + 32 + q * 8, uint16_t());
             }
         }
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-            c.x[i][0] = row8(x[i], k + q * (FP8 ? 16 : 8), len);
-            c.x[i][1] = row8(x[i], k + (FP8 ? q * 16 + 8 : 32 + q * 8), len);
+            c.x[i][0] = row16(x[i], k + q * (FP8 ? 16 : 8), uint16_t());
+            c.x[i][1] = row16(x[i], k + (FP8 ? q * 16 + 8 : 32 + q * 8), uint16_t());
         }
     };
     auto multiply = [&](const Chunk& c) {
@@ -1034,19 +1062,22 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
                         b[j], __builtin_bit_cast(bf16x8, c.x[i][h]), acc[i][j], 0, 0, 0);
         }
     };
-    constexpr int kAhead = MB * JB == 1 ? 8 : 4;
+    // eight chunks on their way where they take no more than 160 registers
+    constexpr int kAhead = ((FP8 ? JB : 2 * JB) + 2 * MB) * 32 <= 160 ? 8 : 4;
     const int full = g.k / 64;
     int c = wave;
     for (; c + (kAhead - 1) * kFewWaves < full; c += kAhead * kFewWaves) {
         Chunk r[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) load(r[u], (c + u * kFewWaves) * 64, 0x7fffffff);
+        for (int u = 0; u < kAhead; ++u) load(r[u], (c + u * kFewWaves) * 64, std::false_type{});
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) multiply(r[u]);
     }
     for (; c * 64 < g.k; c += kFewWaves) {
         Chunk r;
-        load(r, c * 64, g.k);
+        if (c < full) load(r, c * 64, std::false_type{});
+        else load(r, c * 64, std::true_type{});
         multiply(r);
     }
     // Lane: token lo, features 4 q + 0..3.
@@ -1076,6 +1107,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
 // 4097 product from 60 to 101 us).  5 us for a few megabytes, which is a
 // launch's latency, then 4 TB/s; the loads through registers, which need no
 // copy, took 25 us instead of 17 for the 1000 x 1024 x 1365 forward product.
+// Rows may lie off 4-byte boundaries, which bytes16 takes into account.
 struct Pack {
     const void* src;
     uint8_t* dst;
@@ -1090,8 +1122,10 @@ __global__ __launch_bounds__(kPackBlock) void pack_kernel(Pack a, Pack b, int bl
     const int row = id / p.chunks, c = id - row * p.chunks;
     if (row >= p.rows) return;
     u32x4 v;
-    if (p.fp8) v = row16(static_cast<const uint8_t*>(p.src) + row * p.ld, c * 16, p.cols);
-    else v = row8(static_cast<const uint16_t*>(p.src) + row * p.ld, c * 8, p.cols);
+    const int64_t e = p.fp8 ? 1 : 2;
+    const uint8_t* from = static_cast<const uint8_t*>(p.src) + row * p.ld * e;
+    if (p.fp8) v = row_end16<uint8_t, true>(from, c * 16, p.cols);
+    else v = row_end16<uint16_t, true>(from, c * 16, p.cols * e);
     *reinterpret_cast<u32x4*>(p.dst + static_cast<int64_t>(row) * p.pitch + c * 16) = v;
 }
 
@@ -1635,15 +1669,18 @@ int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const cha
 template <int MB, int JB>
 int32_t launch_few(const Product& g, bool fp8, hipStream_t stream, const char* who) {
     const dim3 grid(static_cast<uint32_t>(ceil_div(g.n, 16 * JB))), block(kFewWaves * 64);
-    if (fp8) few_rows_kernel<MB, JB, true><<<grid, block, 0, stream>>>(g);
-    else few_rows_kernel<MB, JB, false><<<grid, block, 0, stream>>>(g);
+    const bool odd = !aligned(g.a, 4) || !aligned(g.b, 4) || g.lda % 2 != 0 || g.ldb % (fp8 ? 4 : 2) != 0;
+    if (fp8 && odd) few_rows_kernel<MB, JB, true, true><<<grid, block, 0, stream>>>(g);
+    else if (fp8) few_rows_kernel<MB, JB, true, false><<<grid, block, 0, stream>>>(g);
+    else if (odd) few_rows_kernel<MB, JB, false, true><<<grid, block, 0, stream>>>(g);
+    else few_rows_kernel<MB, JB, false, false><<<grid, block, 0, stream>>>(g);
     return launched(who);
 }
 
 // The features of a workgroup: x is read again by each, W's rows once, and the
 // CU with the most workgroups ends last; so the least rounds * (bytes of x and
 // W of one).  11008 features of 4096 E4M3 codes, 16 tokens: 48 a workgroup (230
-// workgroups) take 12.4 us, 32 (344) 17.
+// workgroups) take 12.2 us, 32 (344) 17.
 template <int MB>
 int32_t run_few(const Product& g, bool fp8, hipStream_t stream, const char* who) {
     int best = 0;
