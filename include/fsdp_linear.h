@@ -141,7 +141,9 @@ int32_t fsdp_linear_forward(const fsdp_linear* a, hipStream_t stream);
  * dy: bf16 [m, n].  z: bf16 [m, n] as the forward call stored it; may be NULL
  * when act is FSDP_ACT_NONE.  At z = 0 relu's slope is 0.  Both select: where
  * an element is dropped dz is 0 whatever dy and z hold, and where relu has
- * z <= 0 whatever dy holds.  The residual's gradient is dy. */
+ * z <= 0 whatever dy holds.  Where z is NaN and the element is kept dz is NaN,
+ * relu's too (but with FSDP_ACT_NONE z is not read).  The residual's gradient
+ * is dy. */
 int32_t fsdp_linear_epilogue_backward(uint16_t* dz, int64_t lddz, void* db, int32_t db_dtype,
                                       int32_t accumulate, const uint16_t* dy, int64_t lddy,
                                       const uint16_t* z, int64_t ldz, int32_t act,

@@ -73,9 +73,9 @@ def act(z, name):
 
 
 def act_grad(z, name):
-    """act'(z); relu's is 0 at 0."""
+    """act'(z); relu's is 0 at 0, and NaN at NaN as every other."""
     if name == "relu":
-        return np.where(z <= 0, 0.0, 1.0)
+        return np.where(np.isnan(z), z, np.where(z <= 0, 0.0, 1.0))
     if name == "gelu":
         return special.ndtr(z) + z * np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
     if name == "silu":

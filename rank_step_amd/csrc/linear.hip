@@ -163,7 +163,7 @@ __device__ __forceinline__ void activate8(float (&v)[8], int act) {
 __device__ __forceinline__ void activation_grad8(float (&d)[8], const float (&z)[8], int act) {
     if (act == FSDP_ACT_RELU) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) d[q] = z[q] <= 0.0f ? 0.0f : d[q];
+        for (int q = 0; q < 8; ++q) d[q] = z[q] <= 0.0f ? 0.0f : z[q] != z[q] ? z[q] : d[q];  // NaN stays
     } else if (act == FSDP_ACT_GELU) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {

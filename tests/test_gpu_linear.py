@@ -468,6 +468,24 @@ def test_epilogue_backward_drops_whatever_z_holds(gpu, space, act, rows):
         assert bool(((db.double() - want).abs() <= want * (2.0 ** -20 + rows * 2.0 ** -24)).all())
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+@pytest.mark.parametrize("rows", [40, 600])
+def test_epilogue_backward_nan_of_z_stays(gpu, space, act, rows):
+    """A kept element whose z is NaN has a NaN gradient, and its column a NaN sum; no other."""
+    n = 100
+    z = randn(gen(11), rows, n).to(torch.bfloat16)
+    hit = torch.zeros(rows, n, dtype=torch.bool, device=gpu)
+    hit[3, 5] = hit[rows - 1, 99] = hit[rows // 2, 64:70] = True
+    z[hit] = float("nan")
+    dy = torch.ones_like(z)
+    for d in (None, dict(p=0.5, seed=12, offset=13)):
+        keep = torch.ones_like(hit) if d is None else torch.from_numpy(OL.keep_factor(rows, n, **d) > 0).to(gpu)
+        dz, db = torch.empty_like(z), torch.empty(n, device=gpu)
+        B.fsdp_linear_epilogue_backward(dz, dy, rows, n, z=z, act=act, dropout=d, db=db, workspace=space)
+        assert torch.equal(dz.isnan(), hit & keep)
+        assert torch.equal(db.isnan(), (hit & keep).any(0))
+
+
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_activation_range(gpu, space, act):
     """The whole range of z: bf16 values from the smallest to the largest."""

@@ -74,6 +74,13 @@ def test_activation_against_torch_and_differences(name):
     assert np.all(OL.act_grad_slack(z, name) >= np.abs(OL.act_grad(z, name)) - 1e-15)
 
 
+@pytest.mark.parametrize("name", ["relu", "gelu", "silu"])
+def test_slope_at_nan_is_nan(name):
+    z = np.array([np.nan, -1.0, 1.0])
+    assert np.array_equal(np.isnan(OL.act_grad(z, name)), [True, False, False])
+    assert np.array_equal(np.isnan(OL.act(z, name)), [True, False, False])
+
+
 @pytest.mark.parametrize("name", ["none", "relu", "gelu", "silu"])
 def test_layer_gradients_against_differences(name):
     rng = np.random.default_rng(3)
