@@ -1790,6 +1790,13 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
     Space space = whole;
     void* const pa = space.take(bytes_a(p.rows));
     void* const pb = space.take(bytes_b(p.cols));
+    // That a piece's launch is possible is known before the first operand is laid out.
+    Product whole_piece = g;
+    whole_piece.m = static_cast<int32_t>(p.rows);
+    whole_piece.n = static_cast<int32_t>(p.cols);
+    whole_piece.pitch = static_cast<int32_t>(round_up(p.cols, 8));
+    if (best_way<BL>(whole_piece, space).us == kNoWay)
+        return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
     const int64_t na = ceil_div(g.m, p.rows), nb = ceil_div(g.n, p.cols);
     int64_t has_a = -1, has_b = -1;  // the pieces that lie there
     for (int64_t t = 0; t < na * nb; ++t) {

@@ -174,6 +174,20 @@ def test_more_tiles_than_a_launch():
         assert e.value.name == "FSDP_E_CAPACITY", (kw, str(e.value))
 
 
+@pytest.mark.parametrize("kw", [dict(w=(1 << 42) + 2), dict(w=(1 << 42) + 1, w_dtype="e4m3", w_scale=64)])
+def test_more_tiles_than_a_launch_with_an_operand_to_lay_out(kw):
+    """A tall product whose weight is off 16-byte boundaries and fits in the
+    workspace: refused before the weight is laid out there."""
+    kw = dict(x=1 << 40, m=1 << 30, n=8, k=8, workspace=Space(1 << 52, 1 << 20), **kw)
+    with pytest.raises(B.FsdpError) as e:
+        forward(y=1 << 50, **kw)
+    assert e.value.name == "FSDP_E_CAPACITY", str(e.value)
+    kw["dz"] = kw.pop("x")
+    with pytest.raises(B.FsdpError) as e:
+        grad_input(dx=1 << 50, **kw)
+    assert e.value.name == "FSDP_E_CAPACITY", str(e.value)
+
+
 def test_reserved_and_null_record():
     L = B.lib()
     assert L.fsdp_linear_forward(None, None) == -1
