@@ -1,0 +1,48 @@
+"""The linear layer's host logic under AddressSanitizer and UBSan (CPU only).
+
+tests/c/linear_plan.cpp includes the library's own csrc/linear_plan.h (checks
+of matrices and overlaps, and by which launches a product is computed) and is
+compiled with g++ and -fsanitize=address,undefined -fno-sanitize-recover=all,
+so that any signed overflow or access out of bounds ends it.
+"""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "rank_step_amd", "csrc")
+
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+
+
+@pytest.fixture(scope="module")
+def exe(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("plan") / "linear_plan")
+    # host-only build with g++ (no device code involved)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-Wall", "-Werror", "-fno-omit-frame-pointer",
+                    "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                    "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+                    os.path.join(ROOT, "tests", "c", "linear_plan.cpp"), os.path.join(CSRC, "common.cpp"),
+                    "-o", out], check=True, timeout=300)
+    return out
+
+
+def run(exe, *args, text=None):
+    p = subprocess.run([exe, *args], input=text, capture_output=True, text=True, timeout=600)
+    assert p.returncode == 0, p.stderr[-4000:]
+    return p.stdout
+
+
+def test_overlap_matches_brute_force(exe):
+    """No overlap is missed; matrices of one row stride, and single rows, are refused only for one."""
+    assert run(exe, "overlap", "12345", "200000").split() == ["200000", "0", "0"]
+
+
+def test_random_plans_hold_their_bounds(exe):
+    """Sizes up to 2^30 and workspaces up to twice what a call uses: partial sums
+    and operands laid out anew fit, the parts cover the contraction, cuts and
+    pieces lie on multiples of 256, and every launch is a possible one."""
+    assert run(exe, "plan", "777", "200000").split() == ["200000", "0"]
