@@ -166,7 +166,11 @@ constexpr double kNoWay = 1e30;
 //     more where B is read by its columns.  1024 x 1024 x 4096: 17 us, by
 //     128-tiles 42, by those split in four 22.
 //   A split's sums go to memory and back at 6 TB/s, and the join is a launch.
-//     64 x 1024 x 4096 by 64-tiles: 15.5 us, split in 16 9.8.
+//     64 x 1024 x 4096 by 64-tiles: 15.5 us, split in 16 9.8.  The join's
+//     threads add the parts one after the other, which over small outputs takes
+//     0.1 us for each beyond 24: 33 x 64 x 11008 by 128-tiles in 86 parts 15.1
+//     us, by 64-tiles in 20 10.7; but 7 x 16 x 1888 by 128-tiles in 15 7.9, by
+//     64-tiles in 3 8.8.
 template <bool BL>
 inline Way way_of(int tile, int64_t splits, const Extent& g) {
     const double tiles = static_cast<double>(ceil_div(g.m, tile)) * ceil_div(g.n, tile) * splits;
@@ -176,7 +180,7 @@ inline Way way_of(int tile, int64_t splits, const Extent& g) {
     else if (tile == 64) us += std::ceil(tiles / kCus) * (3 + (BL ? 0.165 : 0.2) * steps);
     else if (tiles <= kCus) us += 3 + 0.57 * steps;
     else us += std::ceil(tiles / (2 * kCus)) * (4 + 0.9 * steps);
-    if (splits > 1) us += 3 + 8.0 * splits * g.m * g.pitch / 6e6;
+    if (splits > 1) us += 3 + std::max(8.0 * splits * g.m * g.pitch / 6e6, 0.1 * (splits - 24));
     return Way{tile, splits, tiles > kMaxBlocks ? kNoWay : us};
 }
 

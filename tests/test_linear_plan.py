@@ -46,3 +46,22 @@ def test_random_plans_hold_their_bounds(exe):
     and operands laid out anew fit, the parts cover the contraction, cuts and
     pieces lie on multiples of 256, and every launch is a possible one."""
     assert run(exe, "plan", "777", "200000").split() == ["200000", "0"]
+
+
+def routes(exe, products, workspace=64 << 20):
+    """The launches of aligned products (call, output rows, columns, contraction)."""
+    lines = "".join(f"{c} 0 {m} {n} {k} 1 1 {workspace}\n" for c, m, n, k in products)
+    return run(exe, "route", text=lines).splitlines()
+
+
+def test_small_outputs_over_long_contractions_are_not_split_too_far(exe):
+    """One thread adds an output's parts one after the other, so many parts of a
+    small output cost more than they save: (33, 64, 11008) in 86 parts of
+    128-tiles took 15.1 us, in 20 of 64-tiles 10.7."""
+    small = [("forward", 33, 64, 11008), ("grad_input", 1, 64, 11008), ("grad_input", 16, 64, 11008),
+             ("grad_weight", 64, 64, 8192), ("grad_weight", 16, 96, 19917), ("forward", 144, 32, 9456)]
+    for p, r in zip(small, routes(exe, small)):
+        tile, parts = r.removeprefix("direct ").split("/")
+        assert tile == "64" and int(parts) <= 40, (p, r)
+    # where a few parts are enough, or where each part is long, the split stays
+    assert routes(exe, [("grad_input", 7, 16, 1888), ("grad_weight", 64, 64, 1 << 20)]) == ["direct 128/15", "direct 64/256"]
