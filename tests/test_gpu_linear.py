@@ -33,6 +33,7 @@ import torch
 from oracle import fp8 as F8
 from oracle import linear as OL
 from rank_step_amd import binding as B
+from tests.linear_routes import ROUTES
 
 pytestmark = pytest.mark.gpu
 
@@ -570,6 +571,23 @@ def test_one_mask_everywhere(gpu, space):
         B.fsdp_linear_forward(y, x, w, m, n, k, dropout=d, workspace=space)
         B.fsdp_linear_epilogue_backward(dz, one, m, n, dropout=d)
         assert torch.equal(y, alone) and torch.equal(dz, alone), (m, n, k)
+
+
+@pytest.mark.parametrize("call,wt,m,n,k,size,off,pad,way", ROUTES)
+def test_every_way(gpu, call, wt, m, n, k, size, off, pad, way):
+    """Every way to compute a product, in every call and weight type; what lies
+    behind the workspace stays."""
+    buf = torch.full((size + 64,), 0x5A, dtype=torch.uint8, device=gpu)
+    ws = buf[:size] if size else None
+    if call == "forward":
+        check_forward(m, n, k, ws, wt, act="silu", bias=True, res=True, keep_z=True, p=0.2, off=off, pad=pad)
+        check_forward(m, n, k, ws, wt, yt="f32", off=off, pad=pad, seed=6)
+    elif call == "grad_input":
+        check_grad_input(m, k, n, ws, wt, off, pad)
+    else:
+        check_grad_weight(k, m, n, ws, "f32", True, off, pad)
+        check_grad_weight(k, m, n, ws, "bf16", False, off, pad)
+    assert bool((buf[size:] == 0x5A).all())
 
 
 # ---------------------------------------------------------------- streams, graphs, runs

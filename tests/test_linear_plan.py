@@ -12,6 +12,8 @@ import subprocess
 
 import pytest
 
+from tests.linear_routes import KINDS, ROUTES, program_case
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "rank_step_amd", "csrc")
 
@@ -65,3 +67,21 @@ def test_small_outputs_over_long_contractions_are_not_split_too_far(exe):
         assert tile == "64" and int(parts) <= 40, (p, r)
     # where a few parts are enough, or where each part is long, the split stays
     assert routes(exe, [("grad_input", 7, 16, 1888), ("grad_weight", 64, 64, 1 << 20)]) == ["direct 128/15", "direct 64/256"]
+
+
+def test_every_way_is_in_the_gpu_tests(exe):
+    """tests/linear_routes.py: each product takes the way it stands for, and every
+    kernel form is among them."""
+    got = run(exe, "route", text="".join(program_case(*r[:8]) for r in ROUTES)).splitlines()
+    wrong = [(r, g) for r, g in zip(ROUTES, got) if r[8] != g]
+    assert not wrong, wrong
+    seen = {(r[0], r[1], w.split("/")[0], "split" if w.split("/")[1] != "1" else "whole", r[8].split()[0])
+            for r in ROUTES if not r[8].startswith("few") for w in r[8].split() if "/" in w}
+    for call, wt in KINDS:
+        for tile, parts, how in (("256", "whole", "direct"), ("128", "whole", "direct"), ("128", "split", "direct"),
+                                 ("64", "whole", "direct"), ("64", "split", "direct"),
+                                 ("128", "whole", "staged"), ("128", "split", "staged")):
+            assert (call, wt, tile, parts, how) in seen, (call, wt, tile, parts, how)
+    few = {(r[1], r[6], r[8]) for r in ROUTES if r[8].startswith("few")}
+    assert few >= {(wt, 1, f"few {t}x{f}") for wt in ("bf16", "e4m3") for t in (1, 2) for f in (1, 2, 3, 4)}
+    assert few >= {(wt, 0, f"few 1x{f}") for wt in ("bf16", "e4m3") for f in (1, 2, 3, 4)}
