@@ -883,3 +883,27 @@ def test_offsets_past_32_bits(gpu, space):
     B.fsdp_linear_epilogue_backward(y, y, m, n, dropout=d, db=db, workspace=space)
     again = y[rows].double().cpu().numpy()
     close(again, once * keep, 4 * U * np.abs(once) * keep, "bf16", "dz")
+
+
+@pytest.mark.parametrize("n", [1032, 1033])
+def test_every_row_counts_past_32_bits(gpu, space, n):
+    """The weight gradient of 2.2 G elements of dz, exactly: dz is +-1 and x an
+    integer of at most 2, so every partial sum is an integer of at most 2^22 and
+    exact in fp32, and one row left out or taken twice would show."""
+    m, k = (1 << 21) + 5, 16
+    g = gen(43)
+    dz = torch.empty(m, n, dtype=torch.bfloat16, device=gpu)
+    x = (torch.randint(0, 2, (m, k), generator=g, device=gpu) * 3 - 1).bfloat16()  # -1 or 2: no row adds nothing
+    old = torch.randint(-9, 10, (n, k), generator=g, device=gpu).float()
+    ref = old.double()
+    for a in range(0, m, 1 << 18):
+        b = min(m, a + (1 << 18))
+        dz[a:b] = (torch.randint(0, 2, (b - a, n), generator=g, device=gpu, dtype=torch.int8) * 2 - 1).bfloat16()
+        ref += dz[a:b].double().t().contiguous() @ x[a:b].double()
+    dw = old.clone()
+    B.fsdp_linear_grad_weight(dw, dz, x, m, n, k, dw_dtype="f32", accumulate=True, workspace=space)
+    assert torch.equal(dw.double(), ref)
+    # column sums of the same rows: every one counts in db too
+    db = torch.empty(n, device=gpu)
+    B.fsdp_linear_epilogue_backward(None, dz, m, n, db=db, workspace=space)
+    assert torch.equal(db.double(), sum(dz[a:a + (1 << 18)].double().sum(0) for a in range(0, m, 1 << 18)))
