@@ -117,11 +117,12 @@ __device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + exp_f
 // The normal distribution function and exp(-z^2/2).  With u = |z| / sqrt(2),
 // erfc(u) = exp(-u^2) g(u) and g(u) = t P(t), t = 1 / (1 + 0.4 u): g is smooth
 // and falls like 1/u, so a polynomial of degree 8 in t holds its relative
-// error under 1.3e-7 for every u >= 0 (coefficients fitted to erfc by weighted
-// least squares); evaluated in fp32 it is 4.4e-7.  erfc itself, and not
-// 1 + erf, so that the lower tail keeps its relative precision.  It shares its
-// exponential with the density that the gradient needs, and costs about a
-// third of separate erf and exp calls.
+// error under 2.1e-7 for every u >= 0 (coefficients fitted to erfc by weighted
+// least squares); evaluated in fp32 it is 4.6e-7, and 6.3e-7 with a reciprocal
+// a whole unit off.  erfc itself, and not 1 + erf, so that the lower tail keeps
+// a relative precision: g's, and up to z^2 2^-24 by the rounding of the exponent
+// (1.4e-6 at z = -5).  It shares its exponential with the density that the
+// gradient needs, and costs about a third of separate erf and exp calls.
 __device__ __forceinline__ void normal(float z, float* phi, float* gauss) {
     const float t = rcp_fast(fmaf(0.28284271f, fabsf(z), 1.0f));  // 0.4 / sqrt(2)
     float p = 0.0251327585f;  // the coefficients halved
