@@ -25,8 +25,9 @@
  *     end and the next row's start are not written, and nothing depends on
  *     them; reads stay within the aligned 4-byte words of a row's elements.
  *   - A size of 0 is allowed; a buffer without elements may be NULL.  m, n
- *     and k are at most 2^30 (else FSDP_E_CAPACITY).  A product over no terms
- *     is 0.
+ *     and k are at most 2^30, and a launch holds at most 2^22 - 1 workgroups,
+ *     each of which takes up to 256 x 256 outputs (else FSDP_E_CAPACITY).  A
+ *     product over no terms is 0.
  *   - A written matrix must not overlap another buffer of the call
  *     (FSDP_E_ALIAS), except where a call says that it may be the same matrix
  *     (same address and stride).  Matrices of one row stride that take
@@ -34,7 +35,10 @@
  *     overlap.
  *   - Products accumulate in fp32 over bf16 operands (E4M3 codes widen to
  *     bf16 exactly); everything after the product is fp32, and each output is
- *     rounded once, to nearest even.  NaN gives NaN.
+ *     rounded once, to nearest even.  NaN gives NaN.  The division by an E4M3
+ *     weight's scale is a product with the scale's reciprocal rounded to fp32,
+ *     which has to be a normal number: it is for every scale 448 / max(amax,
+ *     1e-12) of a finite amax.
  *   - workspace, workspace_bytes: device memory the call may use, 16-byte
  *     aligned, or NULL and 0.  A long product over few output tiles is split
  *     over its length when the partial sums fit there, and column sums over
@@ -143,7 +147,7 @@ int32_t fsdp_linear_forward(const fsdp_linear* a, hipStream_t stream);
  * an element is dropped dz is 0 whatever dy and z hold, and where relu has
  * z <= 0 whatever dy holds.  Where z is NaN and the element is kept dz is NaN,
  * relu's too (but with FSDP_ACT_NONE z is not read).  The residual's gradient
- * is dy. */
+ * is dy.  dy is bf16 also where y was fp32 (rounded by the caller). */
 int32_t fsdp_linear_epilogue_backward(uint16_t* dz, int64_t lddz, void* db, int32_t db_dtype,
                                       int32_t accumulate, const uint16_t* dy, int64_t lddy,
                                       const uint16_t* z, int64_t ldz, int32_t act,

@@ -338,6 +338,41 @@ def test_every_e4m3_code(gpu, space):
     assert np.array_equal(dx.double().cpu().numpy()[0], np.where(np.isnan(want), 0, want))
 
 
+@pytest.mark.parametrize("scale", [3.0, 448.0 / 1e-12, 448.0 / 3.38e38, 0.7])
+def test_e4m3_scale_is_a_product_with_its_reciprocal(gpu, space, scale):
+    """One code a sum, so the only roundings are the reciprocal's and the product's."""
+    codes = torch.arange(0, 0x7F, dtype=torch.uint8, device=gpu).reshape(1, -1).repeat(16, 1).contiguous()
+    k = codes.shape[1]
+    s = torch.full((1,), scale, device=gpu)
+    recip = np.float32(1) / np.float32(s.item())
+    want = F8.e4m3_value(np.arange(k)).astype(np.float32) * recip
+    for m in (16, k):  # few tokens, and tiles
+        x = torch.eye(m, k, device=gpu).bfloat16()
+        y = torch.empty(m, 16, device=gpu)
+        B.fsdp_linear_forward(y, x, codes, m, 16, k, w_dtype="e4m3", w_scale=s, y_dtype="f32", workspace=space)
+        assert np.array_equal(y.cpu().numpy(), np.repeat(want[:m, None], 16, 1))
+    dx = torch.empty(16, k, dtype=torch.bfloat16, device=gpu)
+    B.fsdp_linear_grad_input(dx, torch.eye(16, device=gpu).bfloat16(), codes, 16, 16, k, w_dtype="e4m3", w_scale=s,
+                             workspace=space)
+    assert torch.equal(dx, torch.from_numpy(want).to(gpu).bfloat16().expand(16, k))
+
+
+def test_subnormal_values(gpu, space):
+    """bf16 operands under 2^-126 count as what they are, and an fp32 output under it is kept."""
+    x = torch.zeros(40, 64, dtype=torch.bfloat16, device=gpu)
+    w = torch.zeros(64, 64, dtype=torch.bfloat16, device=gpu)
+    for i in range(40):
+        x[i, i] = 2.0 ** -(94 + i)  # 2^-133 is bf16's least
+    w[torch.arange(64), torch.arange(64)] = 2.0 ** 100
+    for m in (3, 40):
+        y = torch.empty(m, 64, device=gpu)
+        B.fsdp_linear_forward(y, x[40 - m:], w, m, 64, 64, y_dtype="f32", workspace=space)
+        want = torch.zeros_like(y)
+        for i in range(m):
+            want[i, 40 - m + i] = 2.0 ** (6 - (40 - m + i))
+        assert torch.equal(y, want), (m, (y != want).nonzero()[:4].tolist())
+
+
 # ---------------------------------------------------------------- gradients
 
 def check_grad_input(m, n, k, space, wt="bf16", off=0, pad=0, seed=2):
