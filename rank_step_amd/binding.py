@@ -194,20 +194,21 @@ def _ptr(x):
 
 
 _raw_stream = None  # the current stream's handle, once torch's device is in use
+_raw_stream_of = None  # that of a device
 
 
 def _current_stream():
     """torch's current stream on the current device.  Its raw accessor takes a
     tenth of the 3 us that building a Stream object takes, which for a small
     call is most of the host's time."""
-    global _raw_stream
+    global _raw_stream, _raw_stream_of
     if _raw_stream is None:
         import torch
         handle = torch.cuda.current_stream().cuda_stream
         raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
         if raw is None or device is None:
             return handle
-        _raw_stream = lambda: raw(device())  # noqa: E731
+        _raw_stream, _raw_stream_of = (lambda: raw(device())), raw  # noqa: E731
     return _raw_stream()
 
 
@@ -394,6 +395,15 @@ def fsdp_reduce_sqnorm_noalloc(grad_shard_out, sqnorm_out, grad_slices, slice_dt
 # with p, seed and offset, and optionally offset_dev (a device int64 [1]).
 # ``workspace``: None or a device tensor, all of which the call may use.
 #
+# These calls take matrices of many types and layouts, so torch tensors are
+# checked against the sizes and types that the call gives them (addresses given
+# as ints are passed on): the element type, a layout that the row stride
+# describes (without one, contiguous), room for the matrix, and the current
+# device.  One expression a tensor, since a small call's time is the host's:
+# 0.15 us a tensor, which taking the device's number once for them and the
+# stream makes up for (forward with seven tensors 5.4 -> 6.0 us, the others
+# within 0.1).
+#
 # The records go to the library as packed bytes: a small call's time is mostly
 # the host's, and a packed record takes a fifth of a ctypes structure's.
 
@@ -402,69 +412,152 @@ _MASK = struct.Struct("=dQQQ")
 _LINEAR = struct.Struct("=3q" + "Qq" + "QqQ" + "Q" + "Qq" + "Qq" + "Qq" + "Q" + "Qq" + "4i")
 assert _MASK.size == ctypes.sizeof(DropoutMask) and _LINEAR.size == ctypes.sizeof(Linear)
 
+_tensor = None  # torch.Tensor, once torch is in use
+_element = {}   # by an element type's name and its code: torch's dtype
+_raw_bits = {}  # by torch's dtype: others that hold the same bits
+_device = None  # the current device's number; without a GPU one that no tensor has
+_bf16 = _f32 = _i64 = None
 
-def _mask(d):
+
+def _load_torch():
+    global _tensor, _device, _bf16, _f32, _i64
+    import torch
+    _bf16, _f32, _i64 = torch.bfloat16, torch.float32, torch.int64
+    _element.update({"f32": _f32, 0: _f32, "bf16": _bf16, 1: _bf16, "e4m3": torch.uint8, 2: torch.uint8})
+    _raw_bits.update({_bf16: (torch.int16, torch.uint16), torch.uint8: (torch.float8_e4m3fn, torch.int8)})
+    if not torch.cuda.is_available():
+        _device = lambda: -2  # noqa: E731
+    else:
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _tensor = torch.Tensor
+
+
+def _at(x, what, dtype, device, rows, cols, ld=None):
+    """The address of rows x cols elements of torch's dtype; ld None: packed."""
+    if (ld is None and type(x) is _tensor and x.dtype is dtype and x.is_contiguous() and x.numel() >= rows * cols
+            and x.get_device() == device):
+        return x.data_ptr()
+    if x is None or not isinstance(x, _tensor):
+        return _ptr(x)
+    # refused, unless it is a subclass, the same bits under another type's name, or has a row stride
+    if dtype is not None and x.dtype is not dtype and x.dtype not in _raw_bits.get(dtype, ()):
+        raise FsdpError(-2, f"{what} is {x.dtype}, the call takes {dtype}")
+    if ld is None:
+        if not x.is_contiguous():
+            raise FsdpError(-1, f"{what} is not contiguous (a matrix's row stride can be given)")
+        ld, room = cols, x.numel()
+    else:
+        if cols > 1 and x.dim() > 0 and x.size(-1) > 1 and x.stride(-1) != 1:
+            raise FsdpError(-1, f"{what}'s columns are not next to each other")
+        room = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+    if rows > 0 and cols > 0 and room < (rows - 1) * ld + cols:
+        raise FsdpError(-1, f"{what} has room for {room} elements, the call needs {rows} rows of {cols}, {ld} apart")
+    if x.get_device() != device:
+        raise FsdpError(-1, f"{what} is on {x.device}, not on the current GPU")
+    return x.data_ptr()
+
+
+def _mask(d, device):
     if d is None:
         return None
-    return _MASK.pack(d["p"], d["seed"] & _M64, d["offset"] & _M64, _ptr(d.get("offset_dev")) or 0)
+    return _MASK.pack(d["p"], d["seed"] & _M64, d["offset"] & _M64,
+                      _at(d.get("offset_dev"), "offset_dev", _i64, device, 1, 1) or 0)
 
 
-def _workspace(w):
-    return (None, 0) if w is None else (w.data_ptr(), w.numel() * w.element_size())
+def _workspace(w, device):
+    if w is None:
+        return None, 0
+    if type(w) is _tensor and w.is_contiguous() and w.get_device() == device:
+        return w.data_ptr(), w.nbytes
+    return _at(w, "workspace", None, device, 0, 0), w.numel() * w.element_size()
 
 
-def _ld(ld, cols):
-    return cols if ld is None else ld
+def _stream_on(stream, device):
+    """_stream(stream), when the current device's number is known."""
+    if stream is None and _raw_stream_of is not None:
+        return _raw_stream_of(device)
+    return _stream(stream)
 
 
 def fsdp_linear_forward(y, x, w, m, n, k, w_dtype="bf16", w_scale=None, y_dtype="bf16", bias=None,
                         residual=None, act="none", z=None, dropout=None, workspace=None, ldy=None,
                         ldx=None, ldw=None, ldr=None, ldz=None, stream=None):
     """z = x W^T + bias; y = dropout(act(z)) + residual."""
-    ws, ws_bytes = _workspace(workspace)
-    mask = None if dropout is None else ctypes.create_string_buffer(_mask(dropout), _MASK.size)
-    a = _LINEAR.pack(m, n, k, _ptr(x) or 0, k if ldx is None else ldx, _ptr(w) or 0, k if ldw is None else ldw,
-                     _ptr(w_scale) or 0, _ptr(bias) or 0, _ptr(residual) or 0, n if ldr is None else ldr,
-                     _ptr(y) or 0, n if ldy is None else ldy, _ptr(z) or 0, n if ldz is None else ldz,
+    if _tensor is None:
+        _load_torch()
+    dev, out = _device(), _element.get(y_dtype)
+    ws, ws_bytes = _workspace(workspace, dev)
+    mask = None if dropout is None else ctypes.create_string_buffer(_mask(dropout, dev), _MASK.size)
+    a = _LINEAR.pack(m, n, k, _at(x, "x", _bf16, dev, m, k, ldx) or 0, k if ldx is None else ldx,
+                     _at(w, "w", _element.get(w_dtype), dev, n, k, ldw) or 0, k if ldw is None else ldw,
+                     0 if w_scale is None else _at(w_scale, "w_scale", _f32, dev, 1, 1),
+                     0 if bias is None else _at(bias, "bias", _bf16, dev, 1, n),
+                     0 if residual is None else _at(residual, "residual", out, dev, m, n, ldr), n if ldr is None else ldr,
+                     _at(y, "y", out, dev, m, n, ldy) or 0, n if ldy is None else ldy,
+                     0 if z is None else _at(z, "z", _bf16, dev, m, n, ldz), n if ldz is None else ldz,
                      0 if mask is None else ctypes.addressof(mask), ws or 0, ws_bytes,
                      WEIGHT_DTYPES.get(w_dtype, w_dtype), DTYPES.get(y_dtype, y_dtype),
                      ACTIVATIONS.get(act, act), 0)
-    _check(lib().fsdp_linear_forward(a, _stream(stream)))
+    _check(lib().fsdp_linear_forward(a, _stream_on(stream, dev)))
 
 
 def fsdp_linear_epilogue_backward(dz, dy, m, n, z=None, act="none", dropout=None, db=None, db_dtype="f32",
                                   accumulate=False, workspace=None, lddz=None, lddy=None, ldz=None,
                                   stream=None):
     """dz = dropout(dy) act'(z), and db = its column sums."""
-    ws, ws_bytes = _workspace(workspace)
+    if _tensor is None:
+        _load_torch()
+    dev = _device()
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(lib().fsdp_linear_epilogue_backward(
-        _ptr(dz), _ld(lddz, n), _ptr(db), DTYPES.get(db_dtype, db_dtype), int(accumulate), _ptr(dy),
-        _ld(lddy, n), _ptr(z), _ld(ldz, n), ACTIVATIONS.get(act, act), _mask(dropout), m, n, ws, ws_bytes,
-        _stream(stream)))
+        _at(dz, "dz", _bf16, dev, m, n, lddz), n if lddz is None else lddz,
+        None if db is None else _at(db, "db", _element.get(db_dtype), dev, 1, n), DTYPES.get(db_dtype, db_dtype),
+        int(accumulate), _at(dy, "dy", _bf16, dev, m, n, lddy), n if lddy is None else lddy,
+        None if z is None else _at(z, "z", _bf16, dev, m, n, ldz), n if ldz is None else ldz,
+        ACTIVATIONS.get(act, act), None if dropout is None else _mask(dropout, dev), m, n, ws, ws_bytes,
+        _stream_on(stream, dev)))
 
 
 def fsdp_linear_grad_input(dx, dz, w, m, n, k, w_dtype="bf16", w_scale=None, workspace=None, lddx=None,
                            lddz=None, ldw=None, stream=None):
     """dx = dz W."""
-    ws, ws_bytes = _workspace(workspace)
-    _check(lib().fsdp_linear_grad_input(_ptr(dx), _ld(lddx, k), _ptr(dz), _ld(lddz, n), _ptr(w), _ld(ldw, k),
-                                        WEIGHT_DTYPES.get(w_dtype, w_dtype), _ptr(w_scale), m, n, k, ws,
-                                        ws_bytes, _stream(stream)))
+    if _tensor is None:
+        _load_torch()
+    dev = _device()
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(lib().fsdp_linear_grad_input(
+        _at(dx, "dx", _bf16, dev, m, k, lddx), k if lddx is None else lddx,
+        _at(dz, "dz", _bf16, dev, m, n, lddz), n if lddz is None else lddz,
+        _at(w, "w", _element.get(w_dtype), dev, n, k, ldw), k if ldw is None else ldw,
+        WEIGHT_DTYPES.get(w_dtype, w_dtype), None if w_scale is None else _at(w_scale, "w_scale", _f32, dev, 1, 1),
+        m, n, k, ws, ws_bytes, _stream_on(stream, dev)))
 
 
 def fsdp_linear_grad_weight(dw, dz, x, m, n, k, dw_dtype="bf16", accumulate=False, workspace=None, lddw=None,
                             lddz=None, ldx=None, stream=None):
     """dW = dz^T x, stored or added to what dw holds."""
-    ws, ws_bytes = _workspace(workspace)
-    _check(lib().fsdp_linear_grad_weight(_ptr(dw), _ld(lddw, k), DTYPES.get(dw_dtype, dw_dtype), int(accumulate),
-                                         _ptr(dz), _ld(lddz, n), _ptr(x), _ld(ldx, k), m, n, k, ws, ws_bytes,
-                                         _stream(stream)))
+    if _tensor is None:
+        _load_torch()
+    dev = _device()
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(lib().fsdp_linear_grad_weight(
+        _at(dw, "dw", _element.get(dw_dtype), dev, n, k, lddw), k if lddw is None else lddw,
+        DTYPES.get(dw_dtype, dw_dtype), int(accumulate), _at(dz, "dz", _bf16, dev, m, n, lddz),
+        n if lddz is None else lddz, _at(x, "x", _bf16, dev, m, k, ldx), k if ldx is None else ldx, m, n, k, ws,
+        ws_bytes, _stream_on(stream, dev)))
 
 
 def fsdp_dropout(y, x, rows, cols, dtype, dropout, residual=None, ldy=None, ldx=None, ldr=None, stream=None):
     """y = dropout(x) + residual; with dy for x and no residual, its gradient."""
-    _check(lib().fsdp_dropout(_ptr(y), _ld(ldy, cols), _ptr(x), _ld(ldx, cols), _ptr(residual), _ld(ldr, cols),
-                              DTYPES.get(dtype, dtype), rows, cols, _mask(dropout), _stream(stream)))
+    if _tensor is None:
+        _load_torch()
+    dev, each = _device(), _element.get(dtype)
+    _check(lib().fsdp_dropout(
+        _at(y, "y", each, dev, rows, cols, ldy), cols if ldy is None else ldy,
+        _at(x, "x", each, dev, rows, cols, ldx), cols if ldx is None else ldx,
+        None if residual is None else _at(residual, "residual", each, dev, rows, cols, ldr),
+        cols if ldr is None else ldr, DTYPES.get(dtype, dtype), rows, cols, _mask(dropout, dev),
+        _stream_on(stream, dev)))
 
 
 class MtPlan:

@@ -625,6 +625,27 @@ def test_every_way(gpu, call, wt, m, n, k, size, off, pad, way):
     assert bool((buf[size:] == 0x5A).all())
 
 
+def test_tensors_as_they_come(gpu, space):
+    """Parameters, E4M3 tensors, raw bits and views with their row stride give what packed tensors give."""
+    m, n, k = 40, 48, 64
+    g = gen(61)
+    x, w = randn(g, m, k).bfloat16(), randn(g, n, k, 0.1).bfloat16()
+    y, got = (torch.empty(m, n, dtype=torch.bfloat16, device=gpu) for _ in range(2))
+    B.fsdp_linear_forward(y, x, w, m, n, k, workspace=space)
+    wide = torch.full((n, 2 * k), float("nan"), dtype=torch.bfloat16, device=gpu)
+    wide[:, k:] = w
+    for wt, kw in ((torch.nn.Parameter(w), {}), (w.view(torch.int16), {}), (wide[:, k:], dict(ldw=2 * k))):
+        B.fsdp_linear_forward(got.zero_(), x, wt, m, n, k, workspace=space, **kw)
+        assert torch.equal(got, y)
+    f8, one = w.to(torch.float8_e4m3fn), torch.ones(1, device=gpu)
+    B.fsdp_linear_forward(y, x, f8.view(torch.uint8), m, n, k, w_dtype="e4m3", w_scale=one, workspace=space)
+    B.fsdp_linear_forward(got, x, f8, m, n, k, w_dtype="e4m3", w_scale=one, workspace=space)
+    assert torch.equal(got, y)
+    for bad, kw in ((x.t(), {}), (x[:, :32], {}), (x[:20], {}), (x.float(), {}), (x.cpu(), {}), (x.t(), dict(ldx=k))):
+        with pytest.raises(B.FsdpError):
+            B.fsdp_linear_forward(got, bad, w, m, n, k, workspace=space, **kw)
+
+
 # ---------------------------------------------------------------- streams, graphs, runs
 
 def layer(gpu, m, n, k, seed):

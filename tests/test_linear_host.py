@@ -163,6 +163,69 @@ def test_refusals(call, kw, code):
     assert e.value.name == code, str(e.value)
 
 
+def _tensors():
+    import torch
+    b, f = torch.bfloat16, torch.float32
+    return torch, b, f, lambda r, c, dt=b: torch.zeros(r, c, dtype=dt)
+
+
+def _wrong_tensors():
+    """(call, arguments, code, words of the message) of tensors that do not hold
+    what the call would read or write there."""
+    torch, b, f, t = _tensors()
+    from_stride = t(8, 32)
+    return [
+        (forward, dict(x=t(4, 16, f)), "FSDP_E_DTYPE", "x is torch.float32"),
+        (forward, dict(x=t(4, 16, torch.float16)), "FSDP_E_DTYPE", "x is torch.float16"),
+        (forward, dict(w=t(8, 16, torch.uint8)), "FSDP_E_DTYPE", "w is"),
+        (forward, dict(w=t(8, 16), w_dtype="e4m3", w_scale=R), "FSDP_E_DTYPE", "w is"),
+        (forward, dict(w_dtype=2, w_scale=t(1, 1)), "FSDP_E_DTYPE", "w_scale"),
+        (forward, dict(y=t(4, 8), y_dtype="f32"), "FSDP_E_DTYPE", "y is"),
+        (forward, dict(residual=t(4, 8, f)), "FSDP_E_DTYPE", "residual is"),
+        (forward, dict(z=t(4, 8, f)), "FSDP_E_DTYPE", "z is"),
+        (forward, dict(bias=t(1, 8, f)), "FSDP_E_DTYPE", "bias is"),
+        (backward, dict(db=t(1, 8)), "FSDP_E_DTYPE", "db is"),  # db_dtype is f32 unless given
+        (grad_weight, dict(dw=t(8, 16, f)), "FSDP_E_DTYPE", "dw is"),
+        (dropout, dict(x=t(4, 8), dtype="f32"), "FSDP_E_DTYPE", "x is"),
+        (dropout, dict(dropout={**P, "offset_dev": torch.zeros(1, dtype=torch.int32)}), "FSDP_E_DTYPE", "offset_dev"),
+        (forward, dict(x=t(16, 4).t()), "FSDP_E_ARG", "not contiguous"),
+        (forward, dict(w=from_stride[:, :16]), "FSDP_E_ARG", "not contiguous"),
+        (forward, dict(bias=t(1, 1).expand(1, 8)), "FSDP_E_ARG", "not contiguous"),
+        (forward, dict(workspace=torch.zeros(64, 4, dtype=torch.uint8)[:, :2]), "FSDP_E_ARG", "not contiguous"),
+        (grad_input, dict(dz=t(4, 16)[:, 8:]), "FSDP_E_ARG", "not contiguous"),
+        (dropout, dict(y=t(8, 4).t()), "FSDP_E_ARG", "not contiguous"),
+        (forward, dict(x=t(16, 4).t(), ldx=4), "FSDP_E_ARG", "next to each other"),
+        (forward, dict(w=from_stride[:, :16], ldw=36), "FSDP_E_ARG", "room"),
+        (forward, dict(w=from_stride[1:, :16], ldw=32), "FSDP_E_ARG", "room"),
+        (forward, dict(y=t(4, 8)[:, 4:], ldy=8), "FSDP_E_ARG", "room"),
+        (forward, dict(x=t(4, 15)), "FSDP_E_ARG", "room"),
+        (forward, dict(y=t(3, 8)), "FSDP_E_ARG", "room"),
+        (backward, dict(db=t(1, 7, f)), "FSDP_E_ARG", "room"),
+        (grad_weight, dict(dw=t(8, 15)), "FSDP_E_ARG", "room"),
+        (dropout, dict(residual=t(4, 7)), "FSDP_E_ARG", "room"),
+        (forward, dict(x=t(4, 16)), "FSDP_E_ARG", "on cpu"),
+        (forward, dict(w=from_stride[:, :16], ldw=32), "FSDP_E_ARG", "on cpu"),
+        (forward, dict(workspace=torch.zeros(64, dtype=torch.uint8)), "FSDP_E_ARG", "on cpu"),
+        (backward, dict(z=t(4, 8)), "FSDP_E_ARG", "on cpu"),
+        (grad_input, dict(w=t(8, 16).view(torch.int16)), "FSDP_E_ARG", "on cpu"),  # the same bits
+        (grad_input, dict(w=torch.zeros(8, 16).to(torch.float8_e4m3fn), w_dtype="e4m3", w_scale=R), "FSDP_E_ARG", "on cpu"),
+        (dropout, dict(x=torch.nn.Parameter(t(4, 8))), "FSDP_E_ARG", "on cpu"),
+        (dropout, dict(dropout={**P, "offset_dev": torch.zeros(1, dtype=torch.int64)}), "FSDP_E_ARG", "on cpu"),
+    ]
+
+
+@pytest.mark.parametrize("i", range(36))
+def test_tensors_that_do_not_hold_the_operand(i):
+    """A tensor of another type, layout, size or device than the call takes is
+    refused, not read as if it were."""
+    cases = _wrong_tensors()
+    assert len(cases) == 36
+    call, kw, code, words = cases[i]
+    with pytest.raises(B.FsdpError) as e:
+        call(**kw)
+    assert e.value.name == code and words in str(e.value), str(e.value)
+
+
 def test_more_tiles_than_a_launch():
     """Refused before any device work, on every way's path."""
     far = dict(x=1 << 40, w=1 << 42, y=1 << 50)
