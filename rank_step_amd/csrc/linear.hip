@@ -350,14 +350,20 @@ __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int st
 
 // ---------------------------------------------------------------- tiled product
 
-struct Product : Extent {
+// In this order: with the sizes before the pointers 16 tokens of [11008, 4096]
+// codes took 12.45 us for 12.2, the odd gradients 1 % more.
+struct Product {
     const void* a;
     const void* b;
     int64_t lda, ldb;
+    int32_t m, n, k;        // output rows and columns, contraction length
     int32_t splits, kper;   // the contraction in `splits` parts of kper (a multiple of kBK)
     int32_t tm, tn;         // output tiles
     float* part;            // splits > 1: [splits][m][pitch] partial sums
+    int32_t pitch;          // n rounded up to 8
     Epilogue e;
+
+    Extent extent() const { return {m, n, k, pitch}; }
 };
 
 // Workgroup b runs on XCD b mod 8, and each XCD has its own L2: consecutive
@@ -1425,7 +1431,8 @@ void split(Product& g, int64_t splits, const Space& space) {
 template <bool BL>
 Product columns(const Product& g, bool fp8, int64_t j0, int64_t n) {
     Product s = g;
-    static_cast<Extent&>(s) = columns_of(g, n);
+    s.n = static_cast<int32_t>(n);
+    s.pitch = columns_of(g.extent(), n).pitch;
     const int64_t e = fp8 ? 1 : 2, oe = g.e.out_f32 ? 4 : 2;
     s.b = static_cast<const uint8_t*>(g.b) + (BL ? j0 * g.ldb : j0) * e;
     s.e.out = static_cast<uint8_t*>(g.e.out) + j0 * oe;
@@ -1440,7 +1447,7 @@ Product columns(const Product& g, bool fp8, int64_t j0, int64_t n) {
 template <bool AL>
 Product rows(const Product& g, int64_t i0, int64_t m) {
     Product s = g;
-    static_cast<Extent&>(s) = rows_of(g, m);
+    s.m = static_cast<int32_t>(m);
     const int64_t oe = g.e.out_f32 ? 4 : 2;
     s.a = static_cast<const uint8_t*>(g.a) + (AL ? i0 * g.lda : i0) * 2;
     s.e.out = static_cast<uint8_t*>(g.e.out) + i0 * g.e.ldo * oe;
@@ -1453,9 +1460,9 @@ Product rows(const Product& g, int64_t i0, int64_t m) {
 // The product whole, or its two parts after a cut.
 template <bool AL, bool BL, bool FP8>
 int32_t run_direct(Product& g, const Space& space, hipStream_t stream, const char* who) {
-    const Way best = best_way<BL>(g, space);
+    const Way best = best_way<BL>(g.extent(), space);
     if (best.us == kNoWay) return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
-    const Cut cut = cut_of<BL>(g, best, space);
+    const Cut cut = cut_of<BL>(g.extent(), best, space);
     if (cut.columns + cut.rows > 0) {
         const int64_t cj = cut.columns, ci = cut.rows;
         Product p = cj > 0 ? columns<BL>(g, FP8, 0, cj) : rows<AL>(g, 0, ci);
@@ -1502,10 +1509,10 @@ Pack pack_of(const void* src, int64_t ld, int64_t rows, int64_t cols, bool fp8, 
 template <bool AL, bool BL>
 int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space& whole, hipStream_t stream,
                    const char* who) {
-    const Pieces p = pieces_of<AL, BL>(g, fp8, a_ok, b_ok, whole);
+    const Pieces p = pieces_of<AL, BL>(g.extent(), fp8, a_ok, b_ok, whole);
     if (p.rows == 0) {
         Product s = g;
-        split(s, splits_for(128, 2 * kCus, s, whole), whole);
+        split(s, splits_for(128, 2 * kCus, s.extent(), whole), whole);
         if constexpr (AL) {
             if (fp8) return launch_product<128, 128, 2, 2, 1, AL, BL, false, true>(s, stream, who);
         }
@@ -1515,7 +1522,7 @@ int32_t run_packed(const Product& g, bool fp8, bool a_ok, bool b_ok, const Space
     void* const pa = space.take(packed_bytes(a_ok, AL, p.rows, g.k, false));
     void* const pb = space.take(packed_bytes(b_ok, BL, p.cols, g.k, fp8));
     // That a piece's launch is possible is known before the first operand is laid out.
-    if (best_way<BL>(columns_of(rows_of(g, p.rows), p.cols), space).us == kNoWay)
+    if (best_way<BL>(columns_of(rows_of(g.extent(), p.rows), p.cols), space).us == kNoWay)
         return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
     const int64_t na = ceil_div(g.m, p.rows), nb = ceil_div(g.n, p.cols);
     int64_t has_a = -1, has_b = -1;  // the pieces that lie there
