@@ -1065,18 +1065,32 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
                         b[j], __builtin_bit_cast(bf16x8, c.x[i][h]), acc[i][j], 0, 0, 0);
         }
     };
-    // eight chunks on their way where they take no more than 160 registers
+    // Eight chunks on their way where they take no more than 160 registers, else
+    // four; what is left of a wave's chunks in batches of four and two.  Eight
+    // against four: one token of [4096, 4096] 8.1 and 8.4 us, from codes 6.3 and
+    // 6.9; [28672, 8192] 89.3 and 86.4, from codes 45.7 and 47.5.  Up to 224
+    // registers: codes of [32000, 4096] 3-7 % faster, 16 tokens of bf16
+    // [8192, 8192] and [8192, 28672] 4 % slower.  One token of [4096, 11008],
+    // whose waves have 21 chunks: 23.7 (codes 16.2), the rest one by one 23.7
+    // (16.9), by fours alone 22.2 (14.4); [4096, 14336] 23.9 (14.6), one by one
+    // 25.7 (15.7).
     constexpr int kAhead = ((FP8 ? JB : 2 * JB) + 2 * MB) * 32 <= 160 ? 8 : 4;
     const int full = g.k / 64;
     int c = wave;
-    for (; c + (kAhead - 1) * kFewWaves < full; c += kAhead * kFewWaves) {
-        Chunk r[kAhead];
+    auto batches = [&](auto ahead) {
+        constexpr int kN = decltype(ahead)::value;
+        for (; c + (kN - 1) * kFewWaves < full; c += kN * kFewWaves) {
+            Chunk r[kN];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) load(r[u], (c + u * kFewWaves) * 64, std::false_type{});
-        __builtin_amdgcn_sched_barrier(0);
+            for (int u = 0; u < kN; ++u) load(r[u], (c + u * kFewWaves) * 64, std::false_type{});
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) multiply(r[u]);
-    }
+            for (int u = 0; u < kN; ++u) multiply(r[u]);
+        }
+    };
+    batches(std::integral_constant<int, kAhead>{});
+    if constexpr (kAhead > 4) batches(std::integral_constant<int, 4>{});
+    batches(std::integral_constant<int, 2>{});
     for (; c * 64 < g.k; c += kFewWaves) {
         Chunk r;
         if (c < full) load(r, c * 64, std::false_type{});

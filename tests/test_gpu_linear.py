@@ -181,6 +181,15 @@ def test_forward_shapes(gpu, space, m, n, k, wt):
     check_forward(m, n, k, None, wt, act="gelu", bias=True, off=3, pad=5, keep_z=True)
 
 
+@pytest.mark.parametrize("m", [1, 16, 30])
+@pytest.mark.parametrize("wt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("k", [64 * 8 * 15 + 64 * 5 + 40, 64 * 8 * 7 + 8, 64 * 8 * 3, 64 * 9])
+def test_few_tokens_by_batches_of_chunks(gpu, space, m, wt, k):
+    """Contractions that leave each wave chunks for every size of batch, and a part of one."""
+    check_forward(m, 40, k, space, wt, bias=True)
+    check_forward(m, 70, k - 3, space, wt, off=1, pad=1, yt="f32")
+
+
 @pytest.mark.parametrize("m,n,k", BIG)
 def test_forward_many_tiles(gpu, space, m, n, k):
     check_forward(m, n, k, space, act="gelu", bias=True, res=True, keep_z=True, p=0.1)
