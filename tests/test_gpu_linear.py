@@ -739,6 +739,50 @@ def test_graph_replays_with_a_device_offset(gpu, m, n, k):
     assert not torch.equal(seen[0], seen[1])
 
 
+WAYS_CAPTURED = [r for r in ROUTES if r[8] in ("direct 256/1", "direct 128/10", "direct 64/15", "staged 128/6",
+                                               "pieces 3x3 64/1", "pieces 1x1 64/15", "few 2x2")
+                 or r[8].startswith("direct columns")]
+
+
+@pytest.mark.parametrize("call,wt,m,n,k,size,off,pad,way", WAYS_CAPTURED)
+def test_every_way_captured(gpu, call, wt, m, n, k, size, off, pad, way):
+    """The call in a graph, replayed over changed inputs with eager work between: each
+    replay gives the eager call's bits."""
+    g = gen(71)
+    rows, cols = (k, m) if call == "grad_weight" else (m, k)
+    a = Mat(rows, cols, "bf16", randn(g, rows, cols), off, pad)
+    b = Mat(k, n, "bf16", randn(g, k, n), off, pad) if call == "grad_weight" else \
+        weight(g, *((n, k) if call == "forward" else (k, n)), wt, off, pad)
+    out = Mat(m, n, "bf16", None, off, pad)
+    ws = torch.empty(size, dtype=torch.uint8, device=gpu) if size else None
+
+    def run():
+        if call == "forward":
+            B.fsdp_linear_forward(out.ptr, a.ptr, b[0].ptr, m, n, k, w_dtype=wt, w_scale=b[1], act="gelu", workspace=ws,
+                                  ldy=out.ld, ldx=a.ld, ldw=b[0].ld, dropout=dict(p=0.1, seed=1, offset=2))
+        elif call == "grad_input":
+            B.fsdp_linear_grad_input(out.ptr, a.ptr, b[0].ptr, m, k, n, w_dtype=wt, w_scale=b[1], workspace=ws,
+                                     lddx=out.ld, lddz=a.ld, ldw=b[0].ld)
+        else:
+            B.fsdp_linear_grad_weight(out.ptr, a.ptr, b.ptr, k, m, n, workspace=ws, lddw=out.ld, lddz=a.ld, ldx=b.ld)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        a.t.copy_(randn(g, rows, cols))
+        run()
+        want = out.t.clone()
+        out.t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.t, want)
+    out.check_surroundings()
+
+
 def test_parts_of_a_packed_projection(gpu, space):
     """Three products into the columns of one buffer, whose rows they share."""
     m, k, parts = 50, 256, (128, 64, 72)
@@ -972,3 +1016,37 @@ def test_every_row_counts_past_32_bits(gpu, space, n):
     db = torch.empty(n, device=gpu)
     B.fsdp_linear_epilogue_backward(None, dz, m, n, db=db, workspace=space)
     assert torch.equal(db.double(), sum(dz[a:a + (1 << 18)].double().sum(0) for a in range(0, m, 1 << 18)))
+
+
+@pytest.mark.parametrize("wt", ["bf16", "e4m3"])
+def test_weights_past_32_bits(gpu, space, wt):
+    """A weight of 2.2 G elements, exactly: its elements are -1 or 2 and the other
+    operand's +-1, so every sum is an integer under 2^24."""
+    n, k = (1 << 22) + 24, 528
+    g = gen(81)
+    w = torch.empty(n, k, dtype=TT[wt], device=gpu)
+    for a in range(0, n, 1 << 18):
+        b = min(n, a + (1 << 18))
+        two = torch.randint(0, 2, (b - a, k), generator=g, device=gpu, dtype=torch.uint8)
+        w[a:b] = 0xB8 - two * 0x78 if wt == "e4m3" else (two.char() * 3 - 1).bfloat16()  # codes of -1 and 2
+    one = torch.ones(1, device=gpu) if wt == "e4m3" else None
+
+    def values(a, b):
+        return w[a:b].view(torch.float8_e4m3fn).double() if wt == "e4m3" else w[a:b].double()
+
+    def signs(*shape):
+        return (torch.randint(0, 2, shape, generator=g, device=gpu, dtype=torch.int8) * 2 - 1).bfloat16()
+
+    for m in (3, 40):
+        x, dz = signs(m, k), signs(m, n)
+        y = torch.empty(m, n, device=gpu)
+        B.fsdp_linear_forward(y, x, w, m, n, k, w_dtype=wt, w_scale=one, y_dtype="f32", workspace=space)
+        dx = torch.empty(m, k, dtype=torch.bfloat16, device=gpu)
+        B.fsdp_linear_grad_input(dx, dz, w, m, n, k, w_dtype=wt, w_scale=one, workspace=space)
+        ref = torch.zeros(m, k, dtype=torch.float64, device=gpu)
+        for a in range(0, n, 1 << 18):
+            b = min(n, a + (1 << 18))
+            v = values(a, b)
+            assert torch.equal(y[:, a:b].double(), x.double() @ v.t().contiguous()), (m, a)
+            ref += dz[:, a:b].double().contiguous() @ v
+        assert torch.equal(dx, ref.bfloat16()), m
