@@ -986,17 +986,19 @@ __device__ __forceinline__ u32x4 row_end16(const uint8_t* row, int64_t at, int64
 }
 
 // The forward product for at most 16 * MB tokens: bound by reading W once.  One
-// token: [4096, 4096] 8.2 us with the call, [28672, 8192] 90 us (5.2 TB/s), from
-// E4M3 codes 46; sixteen tokens: 10.7, 100 and 59.  Four waves or sixteen a
+// token: [4096, 4096] 8.2 us with the call, [28672, 8192] 89 us (5.3 TB/s), from
+// E4M3 codes 46; sixteen tokens: 10.4, 101 and 61.  Four waves or sixteen a
 // workgroup: 3-15 % slower at most sizes; non-temporal loads of W 8-25 %.  A
 // workgroup takes 16 * JB output features; its eight waves take every eighth
 // chunk of 64 contraction elements, from memory straight into the fragments
 // of the matrix instructions (W is used once, so LDS would only be a detour;
 // x comes from L2), several chunks on their way at a time, all of whose loads
 // are issued before the first is used (left to the compiler's order, sixteen
-// tokens of [11008, 4096] take 23.1 us, this way 20.0).  Their sums are added
-// in LDS, so the call is one launch.  ODD: rows off 4-byte boundaries; 16 tokens
-// of [4096, 4095] 17 us, by unaligned loads 30.
+// tokens of [11008, 4096] take 24.4 us, this way 21.0; of [8192, 28672] 116 and
+// 89; one token of [28672, 8192] 89 both ways).  Nothing is on its way while a
+// batch is multiplied.  Their sums are added in LDS, so the call is one launch.
+// ODD: rows off 4-byte boundaries; 16 tokens of [4096, 4095] 14 us, by unaligned
+// loads 30.
 constexpr int kFewWaves = 8;
 template <int MB, int JB, bool FP8, bool ODD>
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Product g) {
