@@ -11,6 +11,13 @@
 #include "fsdp_linear.h"
 #include "internal.h"
 
+// Returns what x gives unless that is FSDP_OK.
+#define TRY(x)                                     \
+    do {                                           \
+        const int32_t st_ = (x);                   \
+        if (st_ != FSDP_OK) return st_;            \
+    } while (0)
+
 namespace fsdp {
 namespace linear {
 
@@ -96,6 +103,16 @@ inline int32_t check_sizes(int64_t m, int64_t n, int64_t k, const char* who) {
 inline int32_t check_workspace(const void* p, int64_t bytes, const char* who) {
     if (bytes < 0 || (!p && bytes > 0)) return fail(FSDP_E_ARG, "%s: bad workspace", who);
     if (!aligned(p, 16)) return fail(FSDP_E_ALIGN, "%s: workspace misaligned", who);
+    return FSDP_OK;
+}
+
+inline int32_t check_flag(int32_t v, const char* what, const char* who) {
+    if (v != 0 && v != 1) return fail(FSDP_E_ARG, "%s: %s must be 0 or 1", who, what);
+    return FSDP_OK;
+}
+
+inline int32_t check_float_dtype(int32_t d, const char* what, const char* who) {
+    if (d != FSDP_DT_F32 && d != FSDP_DT_BF16) return fail(FSDP_E_DTYPE, "%s: %s must be fp32 or bf16", who, what);
     return FSDP_OK;
 }
 
