@@ -1,5 +1,5 @@
-"""ctypes binding of librank_step.so (C ABI in include/fsdp_step.h and
-include/fsdp_linear.h).
+"""ctypes binding of librank_step.so (C ABI in include/fsdp_step.h,
+include/fsdp_linear.h and include/fsdp_norm.h).
 
 Argument marshalling only: every function here converts its Python arguments
 (torch tensors, ints, dicts) to the C types of the entry point of the same
@@ -28,6 +28,7 @@ ERRORS = {-1: "FSDP_E_ARG", -2: "FSDP_E_DTYPE", -3: "FSDP_E_ALIGN", -4: "FSDP_E_
 DTYPES = {"f32": 0, "bf16": 1}
 WEIGHT_DTYPES = {"bf16": 1, "e4m3": 2}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+NORMS = {"layer": 0, "rms": 1}
 LAYOUTS = {"flat": 0, "shard0": 1, "owner": 2}
 
 # Every function the header declares; the CPU tests check each is exported.
@@ -40,13 +41,16 @@ EXPORTS = ("fsdp_last_error", "fsdp_shard_layout", "fsdp_rank_buffer_layout", "f
            "fsdp_mt_step_amax", "fsdp_mt_cast_fp8", "fsdp_mt_step_fp8",
            "fsdp_mt_reduce_accumulate", "fsdp_grad_accumulate", "fsdp_reduce_sqnorm_noalloc",
            "fsdp_linear_forward", "fsdp_linear_epilogue_backward", "fsdp_linear_grad_input",
-           "fsdp_linear_grad_weight", "fsdp_dropout")
+           "fsdp_linear_grad_weight", "fsdp_dropout", "fsdp_norm_forward", "fsdp_norm_backward")
 
 # fsdp_reduce_sqnorm_noalloc's limit (FSDP_NOALLOC_MAX_NUMEL in the header)
 NOALLOC_MAX_NUMEL = 33_292_288
 
 # The most workspace that a linear call uses (FSDP_LINEAR_WORKSPACE_BYTES in the header)
 LINEAR_WORKSPACE_BYTES = 64 << 20
+
+# The most that a norm's backward call uses (FSDP_NORM_WORKSPACE_BYTES in the header)
+NORM_WORKSPACE_BYTES = 64 << 20
 
 
 class FsdpError(RuntimeError):
@@ -170,6 +174,9 @@ def lib():
             "fsdp_linear_grad_input": [vp, i64, vp, i64, vp, i64, i32, vp, i64, i64, i64, vp, i64, vp],
             "fsdp_linear_grad_weight": [vp, i64, i32, i32, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp],
             "fsdp_dropout": [vp, i64, vp, i64, vp, i64, i32, i64, i64, vp, vp],
+            "fsdp_norm_forward": [vp, i64, vp, vp, vp, i64, i32, i32, vp, vp, i32, ctypes.c_double, i64, i64, vp],
+            "fsdp_norm_backward": [vp, i64, vp, vp, i32, i32, vp, i64, vp, i64, i32, i32, vp, i32, vp, vp, vp, i64,
+                                   i64, i64, vp, i64, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -558,6 +565,47 @@ def fsdp_dropout(y, x, rows, cols, dtype, dropout, residual=None, ldy=None, ldx=
         None if residual is None else _at(residual, "residual", each, dev, rows, cols, ldr),
         cols if ldr is None else ldr, DTYPES.get(dtype, dtype), rows, cols, _mask(dropout, dev),
         _stream_on(stream, dev)))
+
+
+# ---------------------------------------------------------------- norms
+#
+# Row strides, workspaces and the checks of tensors are the linear layer's.
+
+def fsdp_norm_forward(y, x, m, n, dtype="bf16", kind="layer", weight=None, bias=None, w_dtype="bf16", eps=1e-5,
+                      mean=None, rstd=None, ldy=None, ldx=None, stream=None):
+    """y = (x - mean) rstd weight + bias, row by row; mean and rstd are kept where given."""
+    if _tensor is None:
+        _load_torch()
+    dev, each, param = _device(), _element.get(dtype), _element.get(w_dtype)
+    _check(lib().fsdp_norm_forward(
+        _at(y, "y", each, dev, m, n, ldy), n if ldy is None else ldy,
+        None if mean is None else _at(mean, "mean", _f32, dev, 1, m),
+        None if rstd is None else _at(rstd, "rstd", _f32, dev, 1, m),
+        _at(x, "x", each, dev, m, n, ldx), n if ldx is None else ldx, DTYPES.get(dtype, dtype), NORMS.get(kind, kind),
+        None if weight is None else _at(weight, "weight", param, dev, 1, n),
+        None if bias is None else _at(bias, "bias", param, dev, 1, n), DTYPES.get(w_dtype, w_dtype), eps, m, n,
+        _stream_on(stream, dev)))
+
+
+def fsdp_norm_backward(dx, dy, x, m, n, dtype="bf16", kind="layer", weight=None, w_dtype="bf16", mean=None, rstd=None,
+                       residual=None, dw=None, db=None, dw_dtype="f32", accumulate=False, workspace=None, lddx=None,
+                       lddy=None, ldx=None, ldr=None, stream=None):
+    """The gradients: dx (plus residual), and dw and db where given, stored or added to what they hold."""
+    if _tensor is None:
+        _load_torch()
+    dev, each, grad = _device(), _element.get(dtype), _element.get(dw_dtype)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(lib().fsdp_norm_backward(
+        None if dx is None else _at(dx, "dx", each, dev, m, n, lddx), n if lddx is None else lddx,
+        None if dw is None else _at(dw, "dw", grad, dev, 1, n), None if db is None else _at(db, "db", grad, dev, 1, n),
+        DTYPES.get(dw_dtype, dw_dtype), int(accumulate), _at(dy, "dy", each, dev, m, n, lddy),
+        n if lddy is None else lddy, _at(x, "x", each, dev, m, n, ldx), n if ldx is None else ldx,
+        DTYPES.get(dtype, dtype), NORMS.get(kind, kind),
+        None if weight is None else _at(weight, "weight", _element.get(w_dtype), dev, 1, n),
+        DTYPES.get(w_dtype, w_dtype), None if mean is None else _at(mean, "mean", _f32, dev, 1, m),
+        None if rstd is None else _at(rstd, "rstd", _f32, dev, 1, m),
+        None if residual is None else _at(residual, "residual", each, dev, m, n, ldr), n if ldr is None else ldr, m, n,
+        ws, ws_bytes, _stream_on(stream, dev)))
 
 
 class MtPlan:
