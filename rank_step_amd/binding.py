@@ -1,5 +1,5 @@
 """ctypes binding of librank_step.so (C ABI in include/fsdp_step.h,
-include/fsdp_linear.h and include/fsdp_norm.h).
+include/fsdp_linear.h, include/fsdp_norm.h and include/fsdp_mx4.h).
 
 Argument marshalling only: every function here converts its Python arguments
 (torch tensors, ints, dicts) to the C types of the entry point of the same
@@ -41,7 +41,8 @@ EXPORTS = ("fsdp_last_error", "fsdp_shard_layout", "fsdp_rank_buffer_layout", "f
            "fsdp_mt_step_amax", "fsdp_mt_cast_fp8", "fsdp_mt_step_fp8",
            "fsdp_mt_reduce_accumulate", "fsdp_grad_accumulate", "fsdp_reduce_sqnorm_noalloc",
            "fsdp_linear_forward", "fsdp_linear_epilogue_backward", "fsdp_linear_grad_input",
-           "fsdp_linear_grad_weight", "fsdp_dropout", "fsdp_norm_forward", "fsdp_norm_backward")
+           "fsdp_linear_grad_weight", "fsdp_dropout", "fsdp_norm_forward", "fsdp_norm_backward",
+           "fsdp_mx4_quantize", "fsdp_mx4_dequantize", "fsdp_mx4_product")
 
 # fsdp_reduce_sqnorm_noalloc's limit (FSDP_NOALLOC_MAX_NUMEL in the header)
 NOALLOC_MAX_NUMEL = 33_292_288
@@ -51,6 +52,19 @@ LINEAR_WORKSPACE_BYTES = 64 << 20
 
 # The most that a norm's backward call uses (FSDP_NORM_WORKSPACE_BYTES in the header)
 NORM_WORKSPACE_BYTES = 64 << 20
+
+# The most that a 4-bit product uses (FSDP_MX4_WORKSPACE_BYTES in the header)
+MX4_WORKSPACE_BYTES = 64 << 20
+
+
+def mx4_code_bytes(cols):
+    """Bytes of a row's 4-bit codes (FSDP_MX4_CODE_BYTES in the header)."""
+    return (cols + 31) // 32 * 16
+
+
+def mx4_scale_bytes(cols):
+    """Bytes of a row's scales (FSDP_MX4_SCALE_BYTES in the header)."""
+    return (cols + 511) // 512 * 16
 
 
 class FsdpError(RuntimeError):
@@ -125,6 +139,20 @@ class Linear(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class Mx4Operands(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("a_scales", ctypes.c_void_p), ("ldas", ctypes.c_int64),
+                ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64),
+                ("b_scales", ctypes.c_void_p), ("ldbs", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("dropout", ctypes.POINTER(DropoutMask)),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                ("y_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
 def lib_path():
     return _LIB_PATH
 
@@ -177,6 +205,9 @@ def lib():
             "fsdp_norm_forward": [vp, i64, vp, vp, vp, i64, i32, i32, vp, vp, i32, ctypes.c_double, i64, i64, vp],
             "fsdp_norm_backward": [vp, i64, vp, vp, i32, i32, vp, i64, vp, i64, i32, i32, vp, i32, vp, vp, vp, i64,
                                    i64, i64, vp, i64, vp],
+            "fsdp_mx4_quantize": [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i64, i64, vp],
+            "fsdp_mx4_dequantize": [vp, i64, i32, vp, i64, vp, i64, i64, i64, vp],
+            "fsdp_mx4_product": [vp, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -606,6 +637,68 @@ def fsdp_norm_backward(dx, dy, x, m, n, dtype="bf16", kind="layer", weight=None,
         None if rstd is None else _at(rstd, "rstd", _f32, dev, 1, m),
         None if residual is None else _at(residual, "residual", each, dev, m, n, ldr), n if ldr is None else ldr, m, n,
         ws, ws_bytes, _stream_on(stream, dev)))
+
+
+# ---------------------------------------------------------------- 4-bit matrices
+#
+# A 4-bit matrix is two byte arrays, codes and scales; their row strides are in
+# bytes and default to mx4_code_bytes and mx4_scale_bytes of the row.  Other
+# strides, workspaces, dropout and the checks of tensors are the linear layer's.
+
+_MX4 = struct.Struct("=3q" + "Qq" * 4 + "Q" + "Qq" * 3 + "Q" + "Qq" + "2i")
+assert _MX4.size == ctypes.sizeof(Mx4Operands)
+
+
+def fsdp_mx4_quantize(x, rows, cols, x_dtype="bf16", codes=None, scales=None, codes_t=None, scales_t=None, ldx=None,
+                      ldc=None, lds=None, ldct=None, ldst=None, stream=None):
+    """The 4-bit copies of x (codes, scales) and of its transpose (codes_t, scales_t), each where given."""
+    if _tensor is None:
+        _load_torch()
+    dev, byte = _device(), _element["e4m3"]
+    cb, sb, ctb, stb = mx4_code_bytes(cols), mx4_scale_bytes(cols), mx4_code_bytes(rows), mx4_scale_bytes(rows)
+    _check(lib().fsdp_mx4_quantize(
+        None if codes is None else _at(codes, "codes", byte, dev, rows, cb, ldc), cb if ldc is None else ldc,
+        None if scales is None else _at(scales, "scales", byte, dev, rows, sb, lds), sb if lds is None else lds,
+        None if codes_t is None else _at(codes_t, "codes_t", byte, dev, cols, ctb, ldct), ctb if ldct is None else ldct,
+        None if scales_t is None else _at(scales_t, "scales_t", byte, dev, cols, stb, ldst),
+        stb if ldst is None else ldst, _at(x, "x", _element.get(x_dtype), dev, rows, cols, ldx),
+        cols if ldx is None else ldx, DTYPES.get(x_dtype, x_dtype), rows, cols, _stream_on(stream, dev)))
+
+
+def fsdp_mx4_dequantize(y, codes, scales, rows, cols, y_dtype="bf16", ldy=None, ldc=None, lds=None, stream=None):
+    """The values of a 4-bit copy."""
+    if _tensor is None:
+        _load_torch()
+    dev, byte = _device(), _element["e4m3"]
+    cb, sb = mx4_code_bytes(cols), mx4_scale_bytes(cols)
+    _check(lib().fsdp_mx4_dequantize(
+        _at(y, "y", _element.get(y_dtype), dev, rows, cols, ldy), cols if ldy is None else ldy,
+        DTYPES.get(y_dtype, y_dtype), _at(codes, "codes", byte, dev, rows, cb, ldc), cb if ldc is None else ldc,
+        _at(scales, "scales", byte, dev, rows, sb, lds), sb if lds is None else lds, rows, cols,
+        _stream_on(stream, dev)))
+
+
+def fsdp_mx4_product(y, a, a_scales, b, b_scales, m, n, k, y_dtype="bf16", bias=None, residual=None, act="none",
+                     z=None, dropout=None, workspace=None, ldy=None, lda=None, ldas=None, ldb=None, ldbs=None,
+                     ldr=None, ldz=None, stream=None):
+    """z = A B^T + bias; y = dropout(act(z)) + residual."""
+    if _tensor is None:
+        _load_torch()
+    dev, out, byte = _device(), _element.get(y_dtype), _element["e4m3"]
+    ws, ws_bytes = _workspace(workspace, dev)
+    mask = None if dropout is None else ctypes.create_string_buffer(_mask(dropout, dev), _MASK.size)
+    cb, sb = mx4_code_bytes(k), mx4_scale_bytes(k)
+    r = _MX4.pack(m, n, k, _at(a, "a", byte, dev, m, cb, lda) or 0, cb if lda is None else lda,
+                  _at(a_scales, "a_scales", byte, dev, m, sb, ldas) or 0, sb if ldas is None else ldas,
+                  _at(b, "b", byte, dev, n, cb, ldb) or 0, cb if ldb is None else ldb,
+                  _at(b_scales, "b_scales", byte, dev, n, sb, ldbs) or 0, sb if ldbs is None else ldbs,
+                  0 if bias is None else _at(bias, "bias", _bf16, dev, 1, n),
+                  0 if residual is None else _at(residual, "residual", out, dev, m, n, ldr), n if ldr is None else ldr,
+                  _at(y, "y", out, dev, m, n, ldy) or 0, n if ldy is None else ldy,
+                  0 if z is None else _at(z, "z", _bf16, dev, m, n, ldz), n if ldz is None else ldz,
+                  0 if mask is None else ctypes.addressof(mask), ws or 0, ws_bytes, DTYPES.get(y_dtype, y_dtype),
+                  ACTIVATIONS.get(act, act))
+    _check(lib().fsdp_mx4_product(r, _stream_on(stream, dev)))
 
 
 class MtPlan:

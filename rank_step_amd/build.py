@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librank_step.so")
 
-SOURCES = ["rank_step.hip", "linear.hip", "norm.hip", "layout.cpp", "common.cpp"]
+SOURCES = ["rank_step.hip", "linear.hip", "norm.hip", "mx4.hip", "layout.cpp", "common.cpp"]
 
 # IEEE-correct fp32 division and square root, denormals kept, FMA only where
 # the source writes it, and no packed-fp32 instructions.

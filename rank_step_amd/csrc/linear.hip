@@ -27,6 +27,7 @@
 #include "fsdp_linear.h"
 #include "internal.h"
 #include "linear_plan.h"
+#include "mx4_plan.h"
 #include "stream_device.h"
 
 using fsdp::fail;
@@ -556,6 +557,112 @@ __device__ __forceinline__ void arrive() {
     }
 }
 
+// What follows a tile's last product: its sums to memory (a split's part) or
+// through the epilogue.  l0, l1: the LDS stages that the wave used, kStage bytes
+// each, `all` the first one of wave 0 (KW > 1: each wave has its own).
+template <int BM, int BN, int WI, int WJ, int KW>
+__device__ __forceinline__ void finish(const Product& g, f32x4 (&acc)[BM / WI / 16][BN / WJ / 16], Lds* l0, Lds* l1, Lds* all,
+                                       int split, int i0, int j0, int lane, int wave) {
+    constexpr int kWM = BM / WI, kWN = BN / WJ, kFI = kWM / 16, kFJ = kWN / 16, kStage = (BM + BN) * kBK * 2;
+    const int wi = KW == 1 ? wave / WJ : 0, wj = KW == 1 ? wave % WJ : 0;
+    // Lane l holds of each 16x16 block output row l mod 16 and columns
+    // 4 (l / 16) + 0..3.
+    const int lo = lane & 15, hi = lane >> 4;
+    using Quad = __attribute__((address_space(3))) f32x4;
+    const float recip = g.e.scale ? 1.0f / *g.e.scale : 1.0f;
+    const uint64_t off = mask_offset(g.e.mask);
+    float* const sums = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
+    // Rows of 16-byte chunks in LDS are permuted by the row, which spreads the
+    // 16 rows that one write touches over the banks.
+    if constexpr (KW > 1) {
+        arrive<false>();  // this wave's stages are being read and filled until here
+#pragma unroll
+        for (int i = 0; i < kFI; ++i)
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j)
+                *(Quad*)(l0 + (i * 16 + lo) * 256 + (((j * 4 + hi) ^ lo) << 4)) = acc[i][j];
+        __syncthreads();
+        // each wave adds the parts of its 64 / KW rows, in order
+        constexpr int kBatch = 64 / KW / 8;
+        const int c = lane & 7, col = j0 + c * 8, r0 = wave * (64 / KW) + (lane >> 3);
+        float v[kBatch][8];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int r = r0 + q * 8;
+            f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll
+            for (int p = 0; p < KW; ++p) {
+                const Lds* row = all + p * kStage + r * 256;
+                x += *(const Quad*)(row + (((c * 2) ^ (r & 15)) << 4));
+                y += *(const Quad*)(row + (((c * 2 + 1) ^ (r & 15)) << 4));
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                v[q][t] = x[t];
+                v[q][4 + t] = y[t];
+            }
+        }
+        if (g.splits > 1) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int row = i0 + r0 + q * 8;
+                if (row < g.m && col < g.pitch) store8(sums + static_cast<int64_t>(row) * g.pitch + col, 8, v[q]);
+            }
+        } else if (col < g.n) {
+            epilogue8<kBatch>(g.e, i0 + r0, 8, g.m, col, g.n - col, recip, off, v);
+        }
+        return;
+    }
+    if (g.splits > 1) {
+#pragma unroll
+        for (int i = 0; i < kFI; ++i) {
+            const int row = i0 + wi * kWM + i * 16 + lo;
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j) {
+                const int col = j0 + wj * kWN + j * 16 + hi * 4;
+                if (row < g.m && col < g.pitch)
+                    *reinterpret_cast<f32x4*>(sums + static_cast<int64_t>(row) * g.pitch + col) = acc[i][j];
+            }
+        }
+        return;
+    }
+    // 64 rows at a time through the wave's own piece of LDS, so that a lane has
+    // 8 consecutive columns: one 16-byte store and one mask block.
+    arrive<true>();  // the last stages are being read and filled until here
+    constexpr int kHalf = (WI * WJ + 1) / 2, kPiece = 64 * kWN * 4, kLanes = kWN / 8;
+    static_assert(KW > 1 || (kWM % 64 == 0 && kWN >= 64 && kHalf * kPiece <= kStage), "a piece of 64 x kWN floats a wave");
+    Lds* const piece = (wave < kHalf ? l0 : l1) + wave % kHalf * kPiece;
+    const int c = lane % kLanes, col = j0 + wj * kWN + c * 8;
+#pragma unroll
+    for (int h = 0; h < kWM / 64; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j)
+                *(Quad*)(piece + (i * 16 + lo) * (kWN * 4) + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
+        __builtin_amdgcn_wave_barrier();
+        constexpr int kBatch = 4, kStep = 64 / kLanes;
+#pragma unroll 1
+        for (int r = lane / kLanes; r < 64; r += kBatch * kStep) {
+            float v[kBatch][8];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int rq = r + q * kStep;
+                const f32x4 x = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2) ^ (rq & 15)) << 4));
+                const f32x4 y = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2 + 1) ^ (rq & 15)) << 4));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    v[q][t] = x[t];
+                    v[q][4 + t] = y[t];
+                }
+            }
+            if (col < g.n)
+                epilogue8<kBatch>(g.e, i0 + wi * kWM + h * 64 + r, kStep, g.m, col, g.n - col, recip, off, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // BM x BN output tile by WI x WJ waves, two LDS stages of kBK contraction
 // elements: while one is multiplied the next arrives.
 //
@@ -745,102 +852,7 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
         }
     }
 
-    // Lane l holds of each 16x16 block output row l mod 16 and columns
-    // 4 (l / 16) + 0..3.
-    const int lo = lane & 15, hi = lane >> 4;
-    using Quad = __attribute__((address_space(3))) f32x4;
-    const float recip = g.e.scale ? 1.0f / *g.e.scale : 1.0f;
-    const uint64_t off = mask_offset(g.e.mask);
-    float* const sums = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
-    // Rows of 16-byte chunks in LDS are permuted by the row, which spreads the
-    // 16 rows that one write touches over the banks.
-    if constexpr (KW > 1) {
-        arrive<false>();  // this wave's stages are being read and filled until here
-#pragma unroll
-        for (int i = 0; i < kFI; ++i)
-#pragma unroll
-            for (int j = 0; j < kFJ; ++j)
-                *(Quad*)(l0 + (i * 16 + lo) * 256 + (((j * 4 + hi) ^ lo) << 4)) = acc[i][j];
-        __syncthreads();
-        // each wave adds the parts of its 64 / KW rows, in order
-        constexpr int kBatch = 64 / KW / 8;
-        const int c = lane & 7, col = j0 + c * 8, r0 = wave * (64 / KW) + (lane >> 3);
-        float v[kBatch][8];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int r = r0 + q * 8;
-            f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-#pragma unroll
-            for (int p = 0; p < KW; ++p) {
-                const Lds* row = (Lds*)s0 + p * kStage + r * 256;
-                x += *(const Quad*)(row + (((c * 2) ^ (r & 15)) << 4));
-                y += *(const Quad*)(row + (((c * 2 + 1) ^ (r & 15)) << 4));
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                v[q][t] = x[t];
-                v[q][4 + t] = y[t];
-            }
-        }
-        if (g.splits > 1) {
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int row = i0 + r0 + q * 8;
-                if (row < g.m && col < g.pitch) store8(sums + static_cast<int64_t>(row) * g.pitch + col, 8, v[q]);
-            }
-        } else if (col < g.n) {
-            epilogue8<kBatch>(g.e, i0 + r0, 8, g.m, col, g.n - col, recip, off, v);
-        }
-        return;
-    }
-    if (g.splits > 1) {
-#pragma unroll
-        for (int i = 0; i < kFI; ++i) {
-            const int row = i0 + wi * kWM + i * 16 + lo;
-#pragma unroll
-            for (int j = 0; j < kFJ; ++j) {
-                const int col = j0 + wj * kWN + j * 16 + hi * 4;
-                if (row < g.m && col < g.pitch)
-                    *reinterpret_cast<f32x4*>(sums + static_cast<int64_t>(row) * g.pitch + col) = acc[i][j];
-            }
-        }
-        return;
-    }
-    // 64 rows at a time through the wave's own piece of LDS, so that a lane has
-    // 8 consecutive columns: one 16-byte store and one mask block.
-    arrive<true>();  // the last stages are being read and filled until here
-    constexpr int kHalf = (WI * WJ + 1) / 2, kPiece = 64 * kWN * 4, kLanes = kWN / 8;
-    static_assert(KW > 1 || (kWM % 64 == 0 && kWN >= 64 && kHalf * kPiece <= kStage), "a piece of 64 x kWN floats a wave");
-    Lds* const piece = (wave < kHalf ? l0 : l1) + wave % kHalf * kPiece;
-    const int c = lane % kLanes, col = j0 + wj * kWN + c * 8;
-#pragma unroll
-    for (int h = 0; h < kWM / 64; ++h) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < kFJ; ++j)
-                *(Quad*)(piece + (i * 16 + lo) * (kWN * 4) + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
-        __builtin_amdgcn_wave_barrier();
-        constexpr int kBatch = 4, kStep = 64 / kLanes;
-#pragma unroll 1
-        for (int r = lane / kLanes; r < 64; r += kBatch * kStep) {
-            float v[kBatch][8];
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int rq = r + q * kStep;
-                const f32x4 x = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2) ^ (rq & 15)) << 4));
-                const f32x4 y = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2 + 1) ^ (rq & 15)) << 4));
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    v[q][t] = x[t];
-                    v[q][4 + t] = y[t];
-                }
-            }
-            if (col < g.n)
-                epilogue8<kBatch>(g.e, i0 + wi * kWM + h * 64 + r, kStep, g.m, col, g.n - col, recip, off, v);
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
+    finish<BM, BN, WI, WJ, KW>(g, acc, l0, l1, (Lds*)s0, split, i0, j0, lane, wave);
 }
 
 // The sum of a split product's parts, in order, and the epilogue.  A pass over
@@ -1071,15 +1083,6 @@ __global__ __launch_bounds__(kPackBlock) void pack_kernel(Pack a, Pack b, int bl
 }
 
 // ---------------------------------------------------------------- elementwise passes
-
-// 2^tx lanes take one row's chunks of 16 bytes (as many as the row has, up
-// to a wave), the block's 256 >> tx other places take rows, one at a time: two
-// at a time, with twice the loads on their way, were 8 % slower.
-constexpr int kElemBlock = 256;
-struct Grid {
-    int32_t tx, cblocks;  // lanes a row (log2), column blocks
-    int64_t rows;         // rows a block takes in all (a multiple of 256 >> tx)
-};
 
 struct DropoutArgs {
     void* y;
@@ -1546,17 +1549,6 @@ int32_t grad_weight_impl(void* dw, int64_t lddw, int32_t dw_dtype, int32_t accum
 
 // ---------------------------------------------------------------- host: elementwise passes
 
-// chunks: 16-byte ones of a row; rows_max: the most row blocks wanted.
-Grid elementwise_grid(int64_t m, int64_t chunks, int64_t rows_max, int64_t* blocks) {
-    Grid g{};
-    while (g.tx < 6 && (int64_t(1) << g.tx) < chunks) ++g.tx;
-    g.cblocks = static_cast<int32_t>(ceil_div(chunks, int64_t(1) << g.tx));
-    const int64_t per = kElemBlock >> g.tx;
-    g.rows = std::max<int64_t>(1, ceil_div(ceil_div(m, per), std::max<int64_t>(1, rows_max))) * per;
-    *blocks = ceil_div(m, g.rows);
-    return g;
-}
-
 // Rows up to which one workgroup takes a column block's whole height.  333 x
 // 1024: 6.5 us, by row blocks and a second launch 9.0; 600 x 4096: 11.7 and 10.7.
 constexpr int64_t kTallRows = 512;
@@ -1660,6 +1652,8 @@ int32_t dropout_impl(void* y, int64_t ldy, const void* x, int64_t ldx, const voi
 
 }  // namespace
 
+#include "mx4_product.h"
+
 // ---------------------------------------------------------------- entry points
 
 extern "C" int32_t fsdp_linear_forward(const fsdp_linear* a, hipStream_t stream) {
@@ -1701,4 +1695,8 @@ extern "C" int32_t fsdp_dropout(void* y, int64_t ldy, const void* x, int64_t ldx
                                 hipStream_t stream) {
     return fsdp::guarded("fsdp_dropout",
                          [&] { return dropout_impl(y, ldy, x, ldx, residual, ldr, dtype, rows, cols, mask, stream); });
+}
+
+extern "C" int32_t fsdp_mx4_product(const fsdp_mx4_operands* a, hipStream_t stream) {
+    return fsdp::guarded("fsdp_mx4_product", [&] { return mx4_product_impl(a, stream); });
 }

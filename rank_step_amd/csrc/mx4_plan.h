@@ -1,0 +1,38 @@
+// Host logic of the 4-bit matrices (include/fsdp_mx4.h): their checks.  Plain
+// C++ without device code.
+#pragma once
+
+#include "fsdp_mx4.h"
+#include "internal.h"
+#include "linear_plan.h"
+
+namespace fsdp {
+namespace linear {
+
+// A product's rows lie no further apart: a tile's 256 of them are within the 31
+// bits of a buffer offset.
+constexpr int64_t kMaxMx4Stride = int64_t(1) << 22;
+
+// The two arrays of a 4-bit matrix, as matrices of bytes.
+struct Mx4Matrix {
+    Matrix codes, scales;
+};
+
+inline Mx4Matrix mx4_matrix(const void* codes, int64_t ldc, const char* what, const void* scales, int64_t lds,
+                            const char* what_scales, int64_t rows, int64_t cols, bool written) {
+    return {{codes, rows, FSDP_MX4_CODE_BYTES(cols), ldc, 1, what, written},
+            {scales, rows, FSDP_MX4_SCALE_BYTES(cols), lds, 1, what_scales, written}};
+}
+
+inline int32_t check_mx4(const Mx4Matrix& x, const char* who) {
+    for (const Matrix* p : {&x.codes, &x.scales}) {
+        const int32_t st = check_matrix(*p, false, who);
+        if (st != FSDP_OK) return st;
+        if (!aligned(p->p, 16) || (p->rows > 1 && p->ld % 16 != 0))
+            return fail(FSDP_E_ALIGN, "%s: rows of %s do not start on 16-byte boundaries", who, p->what);
+    }
+    return FSDP_OK;
+}
+
+}  // namespace linear
+}  // namespace fsdp

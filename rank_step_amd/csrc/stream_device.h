@@ -5,6 +5,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "internal.h"
 #include "linear_plan.h"
 
@@ -190,12 +192,32 @@ __device__ __forceinline__ void put_sum(void* out, int f32, int accumulate, int6
     }
 }
 
+// 2^tx lanes take one row's chunks of 16 bytes (as many as the row has, up
+// to a wave), the block's 256 >> tx other places take rows, one at a time: two
+// at a time, with twice the loads on their way, were 8 % slower.
+constexpr int kElemBlock = 256;
+struct Grid {
+    int32_t tx, cblocks;  // lanes a row (log2), column blocks
+    int64_t rows;         // rows a block takes in all (a multiple of 256 >> tx)
+};
+
 // ---------------------------------------------------------------- host
 
 // Whether rows take written-through stores: 16-byte boundaries, and 64 rows
 // within the 31 bits of a buffer offset.
 inline bool stream_ok(const void* p, int64_t ld, int elem) {
     return aligned(p, 16) && ld * elem % 16 == 0 && ld <= (int64_t(1) << 22);
+}
+
+// chunks: 16-byte ones of a row; rows_max: the most row blocks wanted.
+inline Grid elementwise_grid(int64_t m, int64_t chunks, int64_t rows_max, int64_t* blocks) {
+    Grid g{};
+    while (g.tx < 6 && (int64_t(1) << g.tx) < chunks) ++g.tx;
+    g.cblocks = static_cast<int32_t>(ceil_div(chunks, int64_t(1) << g.tx));
+    const int64_t per = kElemBlock >> g.tx;
+    g.rows = std::max<int64_t>(1, ceil_div(ceil_div(m, per), std::max<int64_t>(1, rows_max))) * per;
+    *blocks = ceil_div(m, g.rows);
+    return g;
 }
 
 inline int32_t launched(const char* who) {
