@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
+#include <utility>
 
 #include "fsdp_linear.h"
 #include "internal.h"

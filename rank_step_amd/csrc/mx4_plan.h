@@ -1,4 +1,5 @@
-// Host logic of the 4-bit matrices (include/fsdp_mx4.h): their checks.  Plain
+// Host logic of the 4-bit matrices (include/fsdp_mx4.h): their checks, and by
+// which launches a product is computed.  Plain
 // C++ without device code.
 #pragma once
 
@@ -33,6 +34,20 @@ inline int32_t check_mx4(const Mx4Matrix& x, const char* who) {
     }
     return FSDP_OK;
 }
+
+// ---------------------------------------------------------------- ways to compute a product
+//
+// The contraction is counted in 16-bit units of codes, eight a block: a step of
+// kBK of them is 256 elements.
+
+// The contraction in at most `splits` parts of whole pairs of steps, none empty:
+// the scales of two steps are read together.
+inline Parts mx4_parts_of(int64_t k, int64_t splits) {
+    const int64_t turns = std::max<int64_t>(1, ceil_div(k, 2 * kBK)), per = ceil_div(turns, splits);
+    return {static_cast<int32_t>(ceil_div(turns, per)), static_cast<int32_t>(per * 2 * kBK)};
+}
+
+inline Way mx4_best_way(const Extent& g, const Space& space) { return best_way<true>(g, space); }
 
 }  // namespace linear
 }  // namespace fsdp

@@ -37,7 +37,7 @@ struct Mx4Scales {
             const bool of_a = row < BM;
             const int first = of_a ? i0 + row : j0 + row - BM, rows = of_a ? g.m : g.n;
             const int64_t ld = of_a ? g.ldsa : g.ldsb;
-            base[q] = (of_a ? g.sa : g.sb) + first * ld + lbeg / 8;
+            base[q] = (of_a ? g.sa : g.sb) + first * ld + lbeg / 8;  // the same in the whole wave
             off[q] = first + lane < rows ? static_cast<uint32_t>(lane * static_cast<int>(ld)) : kOutside;
         }
     }
@@ -55,94 +55,198 @@ struct Mx4Scales {
     }
 };
 
-__device__ __forceinline__ i32x8 mx4_operand(const u32x4& v) {
-    return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]), 0, 0, 0, 0};
+// acc += the 16x16 product of two fragments over 128 elements; KK: which byte of
+// the scale registers.  In assembly for its register classes, as mfma() above.
+template <int KK>
+__device__ __forceinline__ void mx4_mfma(f32x4& acc, const u32x4& b, const u32x4& a, uint32_t sb, uint32_t sa) {
+    if constexpr (KK == 0)
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+    else
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
 }
 
-// A lane's 16 bytes of row o0 + lane mod 16 from a stage: block 2 (lane / 16) + kk.
-__device__ __forceinline__ u32x4 mx4_fragment(const Lds* tile, int row, int g, int kk) {
-    return *(const __attribute__((address_space(3))) u32x4*)(tile + row * 128 + (((2 * g + kk) ^ (row & 7)) << 4));
+// f(0), ..., f(N - 1), each a constant.
+template <typename F, int... I>
+__device__ __forceinline__ void for_each_constant(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void for_constants(F&& f) {
+    for_each_constant(f, std::make_integer_sequence<int, N>());
+}
+// f(q) for those of COUNT accesses that belong to slot T of N.
+template <int COUNT, int T, int N, typename F>
+__device__ __forceinline__ void for_slot(F&& f) {
+    constexpr int kFirst = T * COUNT / N, kEnd = (T + 1) * COUNT / N;
+    for_constants<kEnd - kFirst>([&](auto q) { f(std::integral_constant<int, kFirst + decltype(q)::value>()); });
 }
 
-template <int BM, int BN, int WI, int WJ>
-__global__ __launch_bounds__(WI* WJ * 64) void mx4_product_kernel(Mx4Product g) {
+// One lane's operands from a stage of W rows: of row o0 + lane mod 16 and every
+// 16th behind it, block 2 (lane / 16) + kk, so that the two blocks that a lane
+// takes of a stage are neighbours and their scales one 16-bit read.
+template <int NF>
+struct Mx4Fragments {
+    int at, scale;
+
+    __device__ __forceinline__ void init(int o0, int lane) {
+        const int lo = lane & 15, g = lane >> 4;
+        at = (o0 + lo) * 128 + (((2 * g) ^ (lo & 7)) << 4);
+        scale = (o0 + lo) * 16 + 2 * g;
+    }
+    __device__ __forceinline__ u32x4 get(const Lds* tile, int f, int kk) const {
+        return *(const __attribute__((address_space(3))) u32x4*)(tile + (at ^ (kk << 4)) + f * 2048);
+    }
+    // h: which stage of the two whose scales lie together
+    __device__ __forceinline__ uint32_t get_scale(const Lds* scales, int f, int h) const {
+        return *(const __attribute__((address_space(3))) uint16_t*)(scales + scale + f * 256 + h * 8);
+    }
+};
+
+// Tiles, waves and stages as product_kernel's.  A step is 256 contraction
+// elements; the scales of two steps come together, 16 bytes a row, into a
+// buffer of their own, of which there are two as well.
+template <int BM, int BN, int WI, int WJ, int KW>
+__global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product g) {
+    static_assert(KW == 1 || (WI == 1 && WJ == 1 && BM == 64 && BN == 64), "waves with parts of the contraction");
     constexpr int kThreads = WI * WJ * 64, kWM = BM / WI, kWN = BN / WJ, kFI = kWM / 16, kFJ = kWN / 16;
-    constexpr int kStage = (BM + BN) * 128;
-    __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t s1[kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t c0[(BM + BN) * 16];
+    constexpr int kStage = (BM + BN) * 128, kScale = (BM + BN) * 16;
+    constexpr bool kShared = KW == 1;  // the waves share their stages
+    __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage * KW];
+    __shared__ __attribute__((aligned(1024))) uint8_t s1[kStage * KW];
+    __shared__ __attribute__((aligned(1024))) uint8_t c0[kScale * KW];
+    __shared__ __attribute__((aligned(1024))) uint8_t c1[kScale * KW];
+
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tid = kShared ? threadIdx.x : lane;  // among the threads that fill a stage
+    const int part = kShared ? 0 : wave, filler = kShared ? wave : 0;
+    Lds* const l0 = (Lds*)s0 + part * kStage;
+    Lds* const l1 = (Lds*)s1 + part * kStage;
+    Lds* const e0 = (Lds*)c0 + part * kScale;
+    Lds* const e1 = (Lds*)c1 + part * kScale;
     const int tiles = g.tm * g.tn;
     const int id = tile_id(blockIdx.x, tiles * g.splits);
     const int split = id / tiles;
     int ti, tj;
     tile_at(id - split * tiles, g.tm, g.tn, &ti, &tj);
     const int i0 = ti * BM, j0 = tj * BN;
-    const int lbeg = split * g.kper, lend = min(g.k, lbeg + g.kper);
-    const int wi = wave / WJ, wj = wave % WJ, lo = lane & 15, hi = lane >> 4;
+    int lbeg = split * g.kper, lend = min(g.k, lbeg + g.kper);
+    if (KW > 1) {
+        const int per = (lend - lbeg + 2 * kBK * KW - 1) / (2 * kBK * KW) * (2 * kBK);
+        lbeg += part * per;
+        lend = min(lend, lbeg + per);
+    }
+    int turns = lend > lbeg ? (lend - lbeg + 2 * kBK - 1) / (2 * kBK) : 0;
+    const int wi = kShared ? wave / WJ : 0, wj = kShared ? wave % WJ : 0;
+
     f32x4 acc[kFI][kFJ];
 #pragma unroll
     for (int i = 0; i < kFI; ++i)
 #pragma unroll
         for (int j = 0; j < kFJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    DirectTile<BM, kThreads, true, 8> ta;
-    DirectTile<BN, kThreads, true, 8> tb;
-    Mx4Scales<BM, BN, WI * WJ> ts;
-    ta.init(g.a, g.lda, i0, g.m, lbeg, lend, threadIdx.x);
-    tb.init(g.b, g.ldb, j0, g.n, lbeg, lend, threadIdx.x);
-    ts.init(g, i0, j0, lbeg, lend, wave, lane);
-    Lds* const stages[2] = {(Lds*)s0, (Lds*)s1};
-    for (int l = lbeg; l < lend; l += 2 * kBK) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int q = 0; q < ta.kLoads; ++q) ta.load(stages[h], wave, q);
-#pragma unroll
-            for (int q = 0; q < tb.kLoads; ++q) tb.load(stages[h] + BM * 128, wave, q);
-            ta.advance();
-            tb.advance();
-        }
-#pragma unroll
-        for (int q = 0; q < ts.kLoads; ++q) ts.load((Lds*)c0, wave, q);
-        arrive<true>();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            i32x8 a[2][kFI], b[2][kFJ];
-            int sa[kFI], sb[kFJ];
-            auto scale = [&](int row) {
-                return static_cast<int>(*(const __attribute__((address_space(3))) uint16_t*)((Lds*)c0 + row * 16 + h * 8 + hi * 2));
-            };
-#pragma unroll
-            for (int i = 0; i < kFI; ++i) {
-                const int row = wi * kWM + i * 16 + lo;
-                a[0][i] = mx4_operand(mx4_fragment(stages[h], row, hi, 0));
-                a[1][i] = mx4_operand(mx4_fragment(stages[h], row, hi, 1));
-                sa[i] = scale(row);
+
+    if (turns > 0) {
+        Mx4Fragments<kFI> fa;
+        Mx4Fragments<kFJ> fb;
+        fa.init(wi * kWM, lane);
+        fb.init(wj * kWN, lane);
+        DirectTile<BM, kThreads, true, 8> ta;
+        DirectTile<BN, kThreads, true, 8> tb;
+        Mx4Scales<BM, BN, WI * WJ> ts;
+        ta.init(g.a, g.lda, i0, g.m, lbeg, lend, tid);
+        tb.init(g.b, g.ldb, j0, g.n, lbeg, lend, tid);
+        ts.init(g, i0, j0, lbeg, lend, filler, lane);
+        constexpr int kLoads = ta.kLoads + tb.kLoads, kSlots = kFI * kFJ;
+        auto fetch = [&](Lds* stage, int q) {
+            if (q < ta.kLoads) ta.load(stage, filler, q);
+            else tb.load(stage + BM * 128, filler, q - ta.kLoads);
+            if (q == kLoads - 1) {
+                ta.advance();
+                tb.advance();
             }
+        };
+
+        u32x4 a[2][kFI], b[2][kFJ];
+        uint32_t sa[2][kFI], sb[2][kFJ];  // of this step and the next
+        // What a half needs, in the order in which it needs it: fragments, and of a
+        // step's first half the step's scales.
+        auto read = [&](const Lds* stage, int kk, int f) {
+            if (f < kFJ) b[kk][f] = fb.get(stage + BM * 128, f, kk);
+            else a[kk][f - kFJ] = fa.get(stage, f - kFJ, kk);
+        };
+        auto read_scale = [&](const Lds* scales, int h, int p, int f) {
+            if (f < kFJ) sb[p][f] = fb.get_scale(scales + BM * 16, f, h);
+            else sa[p][f - kFJ] = fa.get_scale(scales, f - kFJ, h);
+        };
+        // Half KK of the step of parity p, product by product, with `between` (slot) in
+        // each product's shadow.
+        auto multiply = [&](auto kk, int p, auto&& between) {
+            constexpr int KK = decltype(kk)::value;
+            for_constants<kSlots>([&](auto slot) {
+                constexpr int t = decltype(slot)::value;
+                mx4_mfma<KK>(acc[t / kFJ][t % kFJ], b[KK][t % kFJ], a[KK][t / kFJ], sb[p][t % kFJ], sa[p][t / kFJ]);
+                __builtin_amdgcn_sched_barrier(0);
+                between(slot);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        // The step of parity p in `cur`; the next one is in `nxt`, with its scales the
+        // half h of `scales`.  FILL: `more` takes the scales of the two steps from the
+        // next but one on.
+        auto step = [&](Lds* cur, Lds* nxt, int p, const Lds* scales, int h, auto fill, Lds* more) {
+            constexpr int kReads = kFI + kFJ, kFills = kLoads + (decltype(fill)::value ? ts.kLoads : 0);
+            multiply(std::integral_constant<int, 0>(), p, [&](auto slot) {
+                for_slot<kReads, decltype(slot)::value, kSlots>([&](auto q) { read(cur, 1, decltype(q)::value); });
+            });
+            arrive<kShared>();
+            multiply(std::integral_constant<int, 1>(), p, [&](auto slot) {
+                constexpr int t = decltype(slot)::value;
+                for_slot<2 * kReads, t, kSlots>([&](auto i) {
+                    constexpr int q = decltype(i)::value;
+                    if constexpr (q & 1) read_scale(scales, h, 1 - p, q / 2);
+                    else read(nxt, 0, q / 2);
+                });
+                for_slot<kFills, t, kSlots>([&](auto i) {
+                    constexpr int q = decltype(i)::value;
+                    if constexpr (q < kLoads) fetch(cur, q);
+                    else ts.load(more, filler, q - kLoads);
+                });
+            });
+        };
+
 #pragma unroll
-            for (int j = 0; j < kFJ; ++j) {
-                const int row = wj * kWN + j * 16 + lo;
-                b[0][j] = mx4_operand(mx4_fragment(stages[h] + BM * 128, row, hi, 0));
-                b[1][j] = mx4_operand(mx4_fragment(stages[h] + BM * 128, row, hi, 1));
-                sb[j] = scale(BM + row);
-            }
+        for (int q = 0; q < kLoads; ++q) fetch(l0, q);
 #pragma unroll
-            for (int i = 0; i < kFI; ++i)
+        for (int q = 0; q < ts.kLoads; ++q) ts.load(e0, filler, q);
 #pragma unroll
-                for (int j = 0; j < kFJ; ++j) {
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[0][j], a[0][i], acc[i][j], 4, 4, 0, sb[j], 0, sa[i]);
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[1][j], a[1][i], acc[i][j], 4, 4, 1, sb[j], 1, sa[i]);
-                }
+        for (int q = 0; q < kLoads; ++q) fetch(l1, q);
+        arrive<kShared>();
+        settle(acc);
+#pragma unroll
+        for (int f = 0; f < kFI + kFJ; ++f) {
+            read(l0, 0, f);
+            read_scale(e0, 0, 0, f);
         }
-        arrive<true>();
+        // Four steps a turn of the loop, so that each LDS access names its buffer.  An
+        // odd count takes one more step, over zeros.
+        for (;;) {
+            step(l0, l1, 0, e0, 1, std::true_type(), e1);
+            step(l1, l0, 1, e1, 0, std::false_type(), e1);
+            if (--turns <= 0) break;
+            step(l0, l1, 0, e1, 1, std::true_type(), e0);
+            step(l1, l0, 1, e0, 0, std::false_type(), e0);
+            if (--turns <= 0) break;
+        }
+        settle(acc);
     }
-    finish<BM, BN, WI, WJ, 1>(g, acc, (Lds*)s0, (Lds*)s1, (Lds*)s0, split, i0, j0, lane, wave);
+    finish<BM, BN, WI, WJ, KW>(g, acc, l0, l1, (Lds*)s0, split, i0, j0, lane, wave);
 }
 
 // ---------------------------------------------------------------- host
 
-template <int BM, int BN, int WI, int WJ>
+template <int BM, int BN, int WI, int WJ, int KW>
 int32_t launch_mx4(Mx4Product& g, hipStream_t stream, const char* who) {
     g.tm = static_cast<int32_t>(ceil_div(g.m, BM));
     g.tn = static_cast<int32_t>(ceil_div(g.n, BN));
@@ -150,11 +254,24 @@ int32_t launch_mx4(Mx4Product& g, hipStream_t stream, const char* who) {
     const int64_t joins = ceil_div(static_cast<int64_t>(g.m) * (g.pitch / 8), kJoinBlock);
     if (blocks > kMaxBlocks || (g.splits > 1 && joins > kMaxBlocks))
         return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
-    mx4_product_kernel<BM, BN, WI, WJ><<<dim3(static_cast<uint32_t>(blocks)), dim3(WI * WJ * 64), 0, stream>>>(g);
+    mx4_product_kernel<BM, BN, WI, WJ, KW><<<dim3(static_cast<uint32_t>(blocks)), dim3(WI * WJ * KW * 64), 0, stream>>>(g);
     const int32_t st = launched(who);
     if (st != FSDP_OK || g.splits == 1) return st;
     join_kernel<<<dim3(static_cast<uint32_t>(joins)), dim3(kJoinBlock), 0, stream>>>(g);
     return launched(who);
+}
+
+// The product whole, or its two parts after a cut.
+int32_t run_mx4(Mx4Product& g, const Space& space, hipStream_t stream, const char* who) {
+    const Way best = mx4_best_way(g.extent(), space);
+    if (best.us == kNoWay) return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
+    const Parts p = mx4_parts_of(g.k, best.splits);
+    g.splits = p.n;
+    g.kper = p.k;
+    g.part = reinterpret_cast<float*>(space.p);
+    if (best.tile == 256) return launch_mx4<256, 256, 2, 2, 1>(g, stream, who);
+    if (best.tile == 128) return launch_mx4<128, 128, 2, 2, 1>(g, stream, who);
+    return launch_mx4<64, 64, 1, 1, 4>(g, stream, who);
 }
 
 int32_t mx4_product_impl(const fsdp_mx4_operands* a, hipStream_t stream) {
@@ -206,9 +323,7 @@ int32_t mx4_product_impl(const fsdp_mx4_operands* a, hipStream_t stream) {
     g.e.ldz = a->ldz;
     g.e.bias = a->bias;
     g.e.act = a->act;
-    g.splits = 1;
-    g.kper = g.k;
-    return launch_mx4<128, 128, 2, 2>(g, stream, who);
+    return run_mx4(g, Space(a->workspace, a->workspace_bytes), stream, who);
 }
 
 }  // namespace
