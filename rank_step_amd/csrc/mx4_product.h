@@ -20,6 +20,43 @@ struct Mx4Product : Product {
     int64_t ldsa, ldsb;
 };
 
+// One operand's tile of W rows of a step, 128 bytes each, from memory to LDS as
+// DirectTile's l-major ones.  Chunk c of a row, block c, goes to the place of
+// bits (c0 c2 c1), then permuted by the row: lane group g of a matrix instruction
+// reads blocks 2g and 2g + 1, one after the other, and with neighbouring groups
+// at neighbouring places its reads meet no bank twice.
+template <int W, int THREADS>
+struct Mx4Tile {
+    static constexpr int kLoads = W * 8 / THREADS;
+    const uint8_t* base;  // the tile's first row at this step
+    int left;             // bytes of a row from here to the end, may be negative
+    int at;               // this thread's chunk in a row (the same in all its loads)
+    uint32_t off[kLoads];
+
+    __device__ __forceinline__ void init(const void* p, int64_t ld, int o0, int no, int l0, int lend, int tid) {
+        const int row = static_cast<int>(ld * 2), place = (tid & 7) ^ (tid >> 3 & 7);
+        left = (lend - l0) * 2;
+        base = static_cast<const uint8_t*>(p) + o0 * (ld * 2) + static_cast<int64_t>(l0) * 2;
+        at = ((place & 3) << 1 | place >> 2) * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = (i * THREADS + tid) / 8;
+            off[i] = o0 + r < no ? static_cast<uint32_t>(r * row + at) : kOutside;
+        }
+    }
+    __device__ __forceinline__ void load(Lds* dst, int wave, int q) {
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, 0x7fffffff, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc, (__attribute__((address_space(3))) void*)(dst + (q * THREADS + wave * 64) * 16), 16,
+            at < left ? off[q] : kOutside, 0, 0, 0);
+    }
+    __device__ __forceinline__ void advance() {
+        base += 128;
+        left -= 128;
+    }
+};
+
 // LDS scales of a tile: 16 bytes a row, A's rows and then B's, for two stages.
 // 64 rows are one load of a wave; PARTS waves share them.
 template <int BM, int BN, int PARTS>
@@ -92,11 +129,11 @@ struct Mx4Fragments {
 
     __device__ __forceinline__ void init(int o0, int lane) {
         const int lo = lane & 15, g = lane >> 4;
-        at = (o0 + lo) * 128 + (((2 * g) ^ (lo & 7)) << 4);
+        at = (o0 + lo) * 128 + ((g ^ (lo & 7)) << 4);
         scale = (o0 + lo) * 16 + 2 * g;
     }
     __device__ __forceinline__ u32x4 get(const Lds* tile, int f, int kk) const {
-        return *(const __attribute__((address_space(3))) u32x4*)(tile + (at ^ (kk << 4)) + f * 2048);
+        return *(const __attribute__((address_space(3))) u32x4*)(tile + (at ^ (kk << 6)) + f * 2048);
     }
     // h: which stage of the two whose scales lie together
     __device__ __forceinline__ uint32_t get_scale(const Lds* scales, int f, int h) const {
@@ -152,8 +189,8 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
         Mx4Fragments<kFJ> fb;
         fa.init(wi * kWM, lane);
         fb.init(wj * kWN, lane);
-        DirectTile<BM, kThreads, true, 8> ta;
-        DirectTile<BN, kThreads, true, 8> tb;
+        Mx4Tile<BM, kThreads> ta;
+        Mx4Tile<BN, kThreads> tb;
         Mx4Scales<BM, BN, WI * WJ> ts;
         ta.init(g.a, g.lda, i0, g.m, lbeg, lend, tid);
         tb.init(g.b, g.ldb, j0, g.n, lbeg, lend, tid);
