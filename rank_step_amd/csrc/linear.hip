@@ -558,112 +558,6 @@ __device__ __forceinline__ void arrive() {
     }
 }
 
-// What follows a tile's last product: its sums to memory (a split's part) or
-// through the epilogue.  l0, l1: the LDS stages that the wave used, kStage bytes
-// each, `all` the first one of wave 0 (KW > 1: each wave has its own).
-template <int BM, int BN, int WI, int WJ, int KW>
-__device__ __forceinline__ void finish(const Product& g, f32x4 (&acc)[BM / WI / 16][BN / WJ / 16], Lds* l0, Lds* l1, Lds* all,
-                                       int split, int i0, int j0, int lane, int wave) {
-    constexpr int kWM = BM / WI, kWN = BN / WJ, kFI = kWM / 16, kFJ = kWN / 16, kStage = (BM + BN) * kBK * 2;
-    const int wi = KW == 1 ? wave / WJ : 0, wj = KW == 1 ? wave % WJ : 0;
-    // Lane l holds of each 16x16 block output row l mod 16 and columns
-    // 4 (l / 16) + 0..3.
-    const int lo = lane & 15, hi = lane >> 4;
-    using Quad = __attribute__((address_space(3))) f32x4;
-    const float recip = g.e.scale ? 1.0f / *g.e.scale : 1.0f;
-    const uint64_t off = mask_offset(g.e.mask);
-    float* const sums = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
-    // Rows of 16-byte chunks in LDS are permuted by the row, which spreads the
-    // 16 rows that one write touches over the banks.
-    if constexpr (KW > 1) {
-        arrive<false>();  // this wave's stages are being read and filled until here
-#pragma unroll
-        for (int i = 0; i < kFI; ++i)
-#pragma unroll
-            for (int j = 0; j < kFJ; ++j)
-                *(Quad*)(l0 + (i * 16 + lo) * 256 + (((j * 4 + hi) ^ lo) << 4)) = acc[i][j];
-        __syncthreads();
-        // each wave adds the parts of its 64 / KW rows, in order
-        constexpr int kBatch = 64 / KW / 8;
-        const int c = lane & 7, col = j0 + c * 8, r0 = wave * (64 / KW) + (lane >> 3);
-        float v[kBatch][8];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int r = r0 + q * 8;
-            f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-#pragma unroll
-            for (int p = 0; p < KW; ++p) {
-                const Lds* row = all + p * kStage + r * 256;
-                x += *(const Quad*)(row + (((c * 2) ^ (r & 15)) << 4));
-                y += *(const Quad*)(row + (((c * 2 + 1) ^ (r & 15)) << 4));
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                v[q][t] = x[t];
-                v[q][4 + t] = y[t];
-            }
-        }
-        if (g.splits > 1) {
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int row = i0 + r0 + q * 8;
-                if (row < g.m && col < g.pitch) store8(sums + static_cast<int64_t>(row) * g.pitch + col, 8, v[q]);
-            }
-        } else if (col < g.n) {
-            epilogue8<kBatch>(g.e, i0 + r0, 8, g.m, col, g.n - col, recip, off, v);
-        }
-        return;
-    }
-    if (g.splits > 1) {
-#pragma unroll
-        for (int i = 0; i < kFI; ++i) {
-            const int row = i0 + wi * kWM + i * 16 + lo;
-#pragma unroll
-            for (int j = 0; j < kFJ; ++j) {
-                const int col = j0 + wj * kWN + j * 16 + hi * 4;
-                if (row < g.m && col < g.pitch)
-                    *reinterpret_cast<f32x4*>(sums + static_cast<int64_t>(row) * g.pitch + col) = acc[i][j];
-            }
-        }
-        return;
-    }
-    // 64 rows at a time through the wave's own piece of LDS, so that a lane has
-    // 8 consecutive columns: one 16-byte store and one mask block.
-    arrive<true>();  // the last stages are being read and filled until here
-    constexpr int kHalf = (WI * WJ + 1) / 2, kPiece = 64 * kWN * 4, kLanes = kWN / 8;
-    static_assert(KW > 1 || (kWM % 64 == 0 && kWN >= 64 && kHalf * kPiece <= kStage), "a piece of 64 x kWN floats a wave");
-    Lds* const piece = (wave < kHalf ? l0 : l1) + wave % kHalf * kPiece;
-    const int c = lane % kLanes, col = j0 + wj * kWN + c * 8;
-#pragma unroll
-    for (int h = 0; h < kWM / 64; ++h) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < kFJ; ++j)
-                *(Quad*)(piece + (i * 16 + lo) * (kWN * 4) + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
-        __builtin_amdgcn_wave_barrier();
-        constexpr int kBatch = 4, kStep = 64 / kLanes;
-#pragma unroll 1
-        for (int r = lane / kLanes; r < 64; r += kBatch * kStep) {
-            float v[kBatch][8];
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int rq = r + q * kStep;
-                const f32x4 x = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2) ^ (rq & 15)) << 4));
-                const f32x4 y = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2 + 1) ^ (rq & 15)) << 4));
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    v[q][t] = x[t];
-                    v[q][4 + t] = y[t];
-                }
-            }
-            if (col < g.n)
-                epilogue8<kBatch>(g.e, i0 + wi * kWM + h * 64 + r, kStep, g.m, col, g.n - col, recip, off, v);
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
-}
-
 // BM x BN output tile by WI x WJ waves, two LDS stages of kBK contraction
 // elements: while one is multiplied the next arrives.
 //
@@ -853,7 +747,102 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void product_kernel(Product g) {
         }
     }
 
-    finish<BM, BN, WI, WJ, KW>(g, acc, l0, l1, (Lds*)s0, split, i0, j0, lane, wave);
+    // Lane l holds of each 16x16 block output row l mod 16 and columns
+    // 4 (l / 16) + 0..3.
+    const int lo = lane & 15, hi = lane >> 4;
+    using Quad = __attribute__((address_space(3))) f32x4;
+    const float recip = g.e.scale ? 1.0f / *g.e.scale : 1.0f;
+    const uint64_t off = mask_offset(g.e.mask);
+    float* const sums = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
+    // Rows of 16-byte chunks in LDS are permuted by the row, which spreads the
+    // 16 rows that one write touches over the banks.
+    if constexpr (KW > 1) {
+        arrive<false>();  // this wave's stages are being read and filled until here
+#pragma unroll
+        for (int i = 0; i < kFI; ++i)
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j)
+                *(Quad*)(l0 + (i * 16 + lo) * 256 + (((j * 4 + hi) ^ lo) << 4)) = acc[i][j];
+        __syncthreads();
+        // each wave adds the parts of its 64 / KW rows, in order
+        constexpr int kBatch = 64 / KW / 8;
+        const int c = lane & 7, col = j0 + c * 8, r0 = wave * (64 / KW) + (lane >> 3);
+        float v[kBatch][8];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int r = r0 + q * 8;
+            f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll
+            for (int p = 0; p < KW; ++p) {
+                const Lds* row = (Lds*)s0 + p * kStage + r * 256;
+                x += *(const Quad*)(row + (((c * 2) ^ (r & 15)) << 4));
+                y += *(const Quad*)(row + (((c * 2 + 1) ^ (r & 15)) << 4));
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                v[q][t] = x[t];
+                v[q][4 + t] = y[t];
+            }
+        }
+        if (g.splits > 1) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int row = i0 + r0 + q * 8;
+                if (row < g.m && col < g.pitch) store8(sums + static_cast<int64_t>(row) * g.pitch + col, 8, v[q]);
+            }
+        } else if (col < g.n) {
+            epilogue8<kBatch>(g.e, i0 + r0, 8, g.m, col, g.n - col, recip, off, v);
+        }
+        return;
+    }
+    if (g.splits > 1) {
+#pragma unroll
+        for (int i = 0; i < kFI; ++i) {
+            const int row = i0 + wi * kWM + i * 16 + lo;
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j) {
+                const int col = j0 + wj * kWN + j * 16 + hi * 4;
+                if (row < g.m && col < g.pitch)
+                    *reinterpret_cast<f32x4*>(sums + static_cast<int64_t>(row) * g.pitch + col) = acc[i][j];
+            }
+        }
+        return;
+    }
+    // 64 rows at a time through the wave's own piece of LDS, so that a lane has
+    // 8 consecutive columns: one 16-byte store and one mask block.
+    arrive<true>();  // the last stages are being read and filled until here
+    constexpr int kHalf = (WI * WJ + 1) / 2, kPiece = 64 * kWN * 4, kLanes = kWN / 8;
+    static_assert(KW > 1 || (kWM % 64 == 0 && kWN >= 64 && kHalf * kPiece <= kStage), "a piece of 64 x kWN floats a wave");
+    Lds* const piece = (wave < kHalf ? l0 : l1) + wave % kHalf * kPiece;
+    const int c = lane % kLanes, col = j0 + wj * kWN + c * 8;
+#pragma unroll
+    for (int h = 0; h < kWM / 64; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j)
+                *(Quad*)(piece + (i * 16 + lo) * (kWN * 4) + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
+        __builtin_amdgcn_wave_barrier();
+        constexpr int kBatch = 4, kStep = 64 / kLanes;
+#pragma unroll 1
+        for (int r = lane / kLanes; r < 64; r += kBatch * kStep) {
+            float v[kBatch][8];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int rq = r + q * kStep;
+                const f32x4 x = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2) ^ (rq & 15)) << 4));
+                const f32x4 y = *(const Quad*)(piece + rq * (kWN * 4) + (((c * 2 + 1) ^ (rq & 15)) << 4));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    v[q][t] = x[t];
+                    v[q][4 + t] = y[t];
+                }
+            }
+            if (col < g.n)
+                epilogue8<kBatch>(g.e, i0 + wi * kWM + h * 64 + r, kStep, g.m, col, g.n - col, recip, off, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // The sum of a split product's parts, in order, and the epilogue.  A pass over

@@ -12,7 +12,7 @@
 
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 
 struct Mx4Product : Product {
     const uint8_t* sa;
@@ -20,11 +20,12 @@ struct Mx4Product : Product {
     int64_t ldsa, ldsb;
 };
 
-// One operand's tile of W rows of a step, 128 bytes each, from memory to LDS as
-// DirectTile's l-major ones.  Chunk c of a row, block c, goes to the place of
-// bits (c0 c2 c1), then permuted by the row: lane group g of a matrix instruction
-// reads blocks 2g and 2g + 1, one after the other, and with neighbouring groups
-// at neighbouring places its reads meet no bank twice.
+// One operand's tile of W rows of a step, 128 bytes each, from memory to LDS.
+// Chunk c of a row, block c, goes to the place of bits (c0 c2 c1), then permuted
+// by the row: lane group g of a matrix instruction reads blocks 2g and 2g + 1, one
+// after the other, and with neighbouring groups at neighbouring places its
+// reads meet no bank twice (with the blocks in their order 8192 x 28672 x 8192 had
+// five times the conflict cycles).
 template <int W, int THREADS>
 struct Mx4Tile {
     static constexpr int kLoads = W * 8 / THREADS;
@@ -43,26 +44,35 @@ struct Mx4Tile {
             const int r = (i * THREADS + tid) / 8;
             off[i] = o0 + r < no ? static_cast<uint32_t>(r * row + at) : kOutside;
         }
+        end();
+    }
+    // Behind the row's end no load touches memory: the chunks that lie there, and
+    // lie there from then on, are sent out of range.
+    __device__ __forceinline__ void end() {
+        if (__builtin_expect(left < 128, 0) && at >= left) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) off[i] = kOutside;
+        }
     }
     __device__ __forceinline__ void load(Lds* dst, int wave, int q) {
         const __amdgpu_buffer_rsrc_t rsrc =
             __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, 0x7fffffff, 0x00020000);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsrc, (__attribute__((address_space(3))) void*)(dst + (q * THREADS + wave * 64) * 16), 16,
-            at < left ? off[q] : kOutside, 0, 0, 0);
-    }
-    __device__ __forceinline__ void advance() {
-        base += 128;
-        left -= 128;
+            rsrc, (__attribute__((address_space(3))) void*)(dst + (q * THREADS + wave * 64) * 16), 16, off[q], 0, 0, 0);
+        if (q == kLoads - 1) {
+            base += 128;
+            left -= 128;
+            end();
+        }
     }
 };
 
-// LDS scales of a tile: 16 bytes a row, A's rows and then B's, for two stages.
+// LDS scales of a tile: 16 bytes a row, A's rows and then B's, for two steps.
 // 64 rows are one load of a wave; PARTS waves share them.
 template <int BM, int BN, int PARTS>
 struct Mx4Scales {
     static constexpr int kLoads = (BM + BN) / 64 / PARTS;
-    const uint8_t* base[kLoads];
+    const uint8_t* base[kLoads];  // each the same in the whole wave
     uint32_t off[kLoads];
     int left;  // bytes from here to the end of this part's scales, may be negative
 
@@ -74,7 +84,7 @@ struct Mx4Scales {
             const bool of_a = row < BM;
             const int first = of_a ? i0 + row : j0 + row - BM, rows = of_a ? g.m : g.n;
             const int64_t ld = of_a ? g.ldsa : g.ldsb;
-            base[q] = (of_a ? g.sa : g.sb) + first * ld + lbeg / 8;  // the same in the whole wave
+            base[q] = (of_a ? g.sa : g.sb) + first * ld + lbeg / 8;
             off[q] = first + lane < rows ? static_cast<uint32_t>(lane * static_cast<int>(ld)) : kOutside;
         }
     }
@@ -95,7 +105,7 @@ struct Mx4Scales {
 // acc += the 16x16 product of two fragments over 128 elements; KK: which byte of
 // the scale registers.  In assembly for its register classes, as mfma() above.
 template <int KK>
-__device__ __forceinline__ void mx4_mfma(f32x4& acc, const u32x4& b, const u32x4& a, uint32_t sb, uint32_t sa) {
+__device__ __forceinline__ void mx4_mfma(f32x4& acc, const u32x4& b, const u32x4& a, s16x2 sb, s16x2 sa) {
     if constexpr (KK == 0)
         asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
                      : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
@@ -120,38 +130,121 @@ __device__ __forceinline__ void for_slot(F&& f) {
     for_constants<kEnd - kFirst>([&](auto q) { f(std::integral_constant<int, kFirst + decltype(q)::value>()); });
 }
 
-// One lane's operands from a stage of W rows: of row o0 + lane mod 16 and every
-// 16th behind it, block 2 (lane / 16) + kk, so that the two blocks that a lane
-// takes of a stage are neighbours and their scales one 16-bit read.
-template <int NF>
+// One lane's operands from a stage: of row o0 + lane mod 16 and every 16th behind
+// it, block 2 (lane / 16) + kk, so that the two blocks that a lane takes of a step
+// are neighbours and their scales one 16-bit read.
 struct Mx4Fragments {
     int at, scale;
 
-    __device__ __forceinline__ void init(int o0, int lane) {
+    // slot: the row's among the scales
+    __device__ __forceinline__ void init(int o0, int slot, int lane) {
         const int lo = lane & 15, g = lane >> 4;
         at = (o0 + lo) * 128 + ((g ^ (lo & 7)) << 4);
-        scale = (o0 + lo) * 16 + 2 * g;
+        scale = (slot + lo) * 16 + 2 * g;
     }
     __device__ __forceinline__ u32x4 get(const Lds* tile, int f, int kk) const {
         return *(const __attribute__((address_space(3))) u32x4*)(tile + (at ^ (kk << 6)) + f * 2048);
     }
-    // h: which stage of the two whose scales lie together
-    __device__ __forceinline__ uint32_t get_scale(const Lds* scales, int f, int h) const {
-        return *(const __attribute__((address_space(3))) uint16_t*)(scales + scale + f * 256 + h * 8);
+    // h: which of the two steps whose scales lie together.  The upper half of the
+    // register is not used, and left to whatever it holds.
+    __device__ __forceinline__ s16x2 get_scale(const Lds* scales, int f, int h) const {
+        s16x2 v;
+        v[0] = *(const __attribute__((address_space(3))) short*)(scales + scale + f * 256 + h * 8);
+        return v;
     }
 };
 
-// Tiles, waves and stages as product_kernel's.  A step is 256 contraction
-// elements; the scales of two steps come together, 16 bytes a row, into a
+// All but the newest LOADS loads of this wave have come, and all but the newest
+// READS of its LDS reads; SHARED: of every wave of the workgroup.
+template <bool SHARED, int LOADS, int READS>
+__device__ __forceinline__ void mx4_arrive() {
+    static_assert(LOADS < 64 && READS < 16, "the counters' ranges");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(%1)" ::"i"(LOADS), "i"(READS) : "memory");
+    if (SHARED) {
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    }
+}
+// All its LDS reads have.
+template <bool SHARED>
+__device__ __forceinline__ void mx4_read() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (SHARED) {
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    }
+}
+
+// A wave's sums, to memory (a split's part) or through the epilogue: 64 rows at a
+// time through a piece of LDS of its own, 64 rows of FJ * 64 bytes, so that a lane
+// has 8 consecutive columns and a store takes whole lines.  (Exchanged between
+// lanes without LDS, which gives 64 bytes a row and store, it took 274 us of
+// 8192 x 28672 x 8192, this way 105.)  A row's 16-byte chunks are permuted by the
+// row, which spreads the 16 rows that one write touches over the banks.
+template <int FI, int FJ>
+__device__ __forceinline__ void mx4_finish(const Product& g, f32x4 (&acc)[FI][FJ], Lds* piece, int split, int i0, int j0, int lane) {
+    using Quad = __attribute__((address_space(3))) f32x4;
+    constexpr int kRow = FJ * 64, kLanes = FJ * 2, kBatch = 4, kStep = 64 / kLanes;
+    // Lane l holds of each 16x16 block output row l mod 16 and columns 4 (l / 16) + 0..3.
+    const int lo = lane & 15, hi = lane >> 4;
+    if (g.splits > 1) {
+        float* const sums = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
+#pragma unroll
+        for (int i = 0; i < FI; ++i) {
+            const int row = i0 + i * 16 + lo;
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) {
+                const int col = j0 + j * 16 + hi * 4;
+                if (row < g.m && col < g.pitch)
+                    *reinterpret_cast<f32x4*>(sums + static_cast<int64_t>(row) * g.pitch + col) = acc[i][j];
+            }
+        }
+        return;
+    }
+    const uint64_t off = mask_offset(g.e.mask);
+    const int c = lane % kLanes, col = j0 + c * 8;
+#pragma unroll
+    for (int h = 0; h < FI / 4; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) *(Quad*)(piece + (i * 16 + lo) * kRow + (((j * 4 + hi) ^ lo) << 4)) = acc[h * 4 + i][j];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int r = lane / kLanes; r < 64; r += kBatch * kStep) {
+            float v[kBatch][8];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int rq = r + q * kStep;
+                const f32x4 x = *(const Quad*)(piece + rq * kRow + (((c * 2) ^ (rq & 15)) << 4));
+                const f32x4 y = *(const Quad*)(piece + rq * kRow + (((c * 2 + 1) ^ (rq & 15)) << 4));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    v[q][t] = x[t];
+                    v[q][4 + t] = y[t];
+                }
+            }
+            if (col < g.n) epilogue8<kBatch>(g.e, i0 + h * 64 + r, kStep, g.m, col, g.n - col, 1.0f, off, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Tiles and waves as product_kernel's.  A step is 256 contraction elements in
+// two LDS stages; the scales of two steps come together, 16 bytes a row, into a
 // buffer of their own, of which there are two as well.
 template <int BM, int BN, int WI, int WJ, int KW>
 __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product g) {
     static_assert(KW == 1 || (WI == 1 && WJ == 1 && BM == 64 && BN == 64), "waves with parts of the contraction");
     constexpr int kThreads = WI * WJ * 64, kWM = BM / WI, kWN = BN / WJ, kFI = kWM / 16, kFJ = kWN / 16;
-    constexpr int kStage = (BM + BN) * 128, kScale = (BM + BN) * 16;
+    constexpr int kStageA = BM * 128, kStageB = BN * 128, kScale = (BM + BN) * 16;
     constexpr bool kShared = KW == 1;  // the waves share their stages
-    __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage * KW];
-    __shared__ __attribute__((aligned(1024))) uint8_t s1[kStage * KW];
+    // Objects of their own, so that the compiler sees that a load into one and a
+    // read of another have nothing to wait for.
+    __shared__ __attribute__((aligned(1024))) uint8_t sa0[kStageA * KW];
+    __shared__ __attribute__((aligned(1024))) uint8_t sa1[kStageA * KW];
+    __shared__ __attribute__((aligned(1024))) uint8_t sb0[kStageB * KW];
+    __shared__ __attribute__((aligned(1024))) uint8_t sb1[kStageB * KW];
     __shared__ __attribute__((aligned(1024))) uint8_t c0[kScale * KW];
     __shared__ __attribute__((aligned(1024))) uint8_t c1[kScale * KW];
 
@@ -159,8 +252,10 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tid = kShared ? threadIdx.x : lane;  // among the threads that fill a stage
     const int part = kShared ? 0 : wave, filler = kShared ? wave : 0;
-    Lds* const l0 = (Lds*)s0 + part * kStage;
-    Lds* const l1 = (Lds*)s1 + part * kStage;
+    Lds* const a0 = (Lds*)sa0 + part * kStageA;
+    Lds* const a1 = (Lds*)sa1 + part * kStageA;
+    Lds* const b0 = (Lds*)sb0 + part * kStageB;
+    Lds* const b1 = (Lds*)sb1 + part * kStageB;
     Lds* const e0 = (Lds*)c0 + part * kScale;
     Lds* const e1 = (Lds*)c1 + part * kScale;
     const int tiles = g.tm * g.tn;
@@ -176,7 +271,7 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
         lend = min(lend, lbeg + per);
     }
     int turns = lend > lbeg ? (lend - lbeg + 2 * kBK - 1) / (2 * kBK) : 0;
-    const int wi = kShared ? wave / WJ : 0, wj = kShared ? wave % WJ : 0;
+    const int wi = kShared ? wave / WJ : 0, wj = kShared ? wave % WJ : 0, lo = lane & 15;
 
     f32x4 acc[kFI][kFJ];
 #pragma unroll
@@ -185,100 +280,156 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
         for (int j = 0; j < kFJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
     if (turns > 0) {
-        Mx4Fragments<kFI> fa;
-        Mx4Fragments<kFJ> fb;
-        fa.init(wi * kWM, lane);
-        fb.init(wj * kWN, lane);
+        Mx4Fragments fa, fb;
+        fa.init(wi * kWM, wi * kWM, lane);
+        fb.init(wj * kWN, BM + wj * kWN, lane);
         Mx4Tile<BM, kThreads> ta;
         Mx4Tile<BN, kThreads> tb;
         Mx4Scales<BM, BN, WI * WJ> ts;
         ta.init(g.a, g.lda, i0, g.m, lbeg, lend, tid);
         tb.init(g.b, g.ldb, j0, g.n, lbeg, lend, tid);
         ts.init(g, i0, j0, lbeg, lend, filler, lane);
-        constexpr int kLoads = ta.kLoads + tb.kLoads, kSlots = kFI * kFJ;
-        auto fetch = [&](Lds* stage, int q) {
-            if (q < ta.kLoads) ta.load(stage, filler, q);
-            else tb.load(stage + BM * 128, filler, q - ta.kLoads);
-            if (q == kLoads - 1) {
-                ta.advance();
-                tb.advance();
-            }
-        };
+        constexpr int kSlots = kFI * kFJ, kLag = kSlots / 8;
 
-        u32x4 a[2][kFI], b[2][kFJ];
-        uint32_t sa[2][kFI], sb[2][kFJ];  // of this step and the next
-        // What a half needs, in the order in which it needs it: fragments, and of a
-        // step's first half the step's scales.
-        auto read = [&](const Lds* stage, int kk, int f) {
-            if (f < kFJ) b[kk][f] = fb.get(stage + BM * 128, f, kk);
-            else a[kk][f - kFJ] = fa.get(stage, f - kFJ, kk);
-        };
-        auto read_scale = [&](const Lds* scales, int h, int p, int f) {
-            if (f < kFJ) sb[p][f] = fb.get_scale(scales + BM * 16, f, h);
-            else sa[p][f - kFJ] = fa.get_scale(scales, f - kFJ, h);
-        };
-        // Half KK of the step of parity p, product by product, with `between` (slot) in
-        // each product's shadow.
+        // A's fragments of a step's first half, and of the second half of this step
+        // and the next; B's of both halves; the scales of this step and the next.
+        u32x4 x[kFI], y[2][kFI], b[2][kFJ];
+        s16x2 sa[2][kFI], sb[2][kFJ];
+        // One half of the step of parity p, product by product, with `between` (slot)
+        // in each product's shadow.
         auto multiply = [&](auto kk, int p, auto&& between) {
             constexpr int KK = decltype(kk)::value;
             for_constants<kSlots>([&](auto slot) {
                 constexpr int t = decltype(slot)::value;
-                mx4_mfma<KK>(acc[t / kFJ][t % kFJ], b[KK][t % kFJ], a[KK][t / kFJ], sb[p][t % kFJ], sa[p][t / kFJ]);
+                mx4_mfma<KK>(acc[t / kFJ][t % kFJ], b[KK][t % kFJ], KK ? y[p][t / kFJ] : x[t / kFJ], sb[p][t % kFJ], sa[p][t / kFJ]);
                 __builtin_amdgcn_sched_barrier(0);
                 between(slot);
                 __builtin_amdgcn_sched_barrier(0);
             });
         };
-        // The step of parity p in `cur`; the next one is in `nxt`, with its scales the
-        // half h of `scales`.  FILL: `more` takes the scales of the two steps from the
-        // next but one on.
-        auto step = [&](Lds* cur, Lds* nxt, int p, const Lds* scales, int h, auto fill, Lds* more) {
-            constexpr int kReads = kFI + kFJ, kFills = kLoads + (decltype(fill)::value ? ts.kLoads : 0);
+        // The step of parity p in a0 and b0 (or whichever are `a` and `bb`); the next one
+        // is in `na` and `nb`, with its scales the half h of `scales`.
+        //   first half   reads B of the second, and the next step's scales; A's stage,
+        //                read whole before, is filled with the step after the next
+        //   second half  reads all of A and the first half of B of the next step; B's
+        //                stage is filled
+        // So the loads, which take half a step's time to pass, are spread over all of
+        // it, each at least half a step before its use.  Before a stage is filled all
+        // waves have read it: a barrier stands between the halves, and one early in the
+        // first, when the reads at the end of the step before have come.
+        auto step = [&](Lds* a, Lds* bb, Lds* na, Lds* nb, int p, const Lds* scales, int h, auto fill, Lds* more) {
+            constexpr int kFills = tb.kLoads + (decltype(fill)::value ? ts.kLoads : 0), kScales = kFI + kFJ;
             multiply(std::integral_constant<int, 0>(), p, [&](auto slot) {
-                for_slot<kReads, decltype(slot)::value, kSlots>([&](auto q) { read(cur, 1, decltype(q)::value); });
+                constexpr int t = decltype(slot)::value;
+                for_slot<kFJ + kScales, t, kSlots>([&](auto i) {
+                    constexpr int q = decltype(i)::value;
+                    if constexpr (q < kFJ) b[1][q] = fb.get(bb, q, 1);
+                    else if constexpr (q < 2 * kFJ) sb[1 - p][q - kFJ] = fb.get_scale(scales, q - kFJ, h);
+                    else sa[1 - p][q - 2 * kFJ] = fa.get_scale(scales, q - 2 * kFJ, h);
+                });
+                if constexpr (t == kLag) mx4_read<kShared>();
+                if constexpr (t >= kLag)
+                    for_slot<ta.kLoads, t - kLag, kSlots - kLag>([&](auto q) { ta.load(a, filler, decltype(q)::value); });
             });
-            arrive<kShared>();
+            // (the scales are the newest reads, B the oldest)
+            mx4_arrive<kShared, ta.kLoads, kScales < 15 ? kScales : 15>();
             multiply(std::integral_constant<int, 1>(), p, [&](auto slot) {
                 constexpr int t = decltype(slot)::value;
-                for_slot<2 * kReads, t, kSlots>([&](auto i) {
+                for_slot<2 * kFI + kFJ, t, kSlots>([&](auto i) {
                     constexpr int q = decltype(i)::value;
-                    if constexpr (q & 1) read_scale(scales, h, 1 - p, q / 2);
-                    else read(nxt, 0, q / 2);
+                    if constexpr (q < kFI) x[q] = fa.get(na, q, 0);
+                    else if constexpr (q < 2 * kFI) y[1 - p][q - kFI] = fa.get(na, q - kFI, 1);
+                    else b[0][q - 2 * kFI] = fb.get(nb, q - 2 * kFI, 0);
                 });
                 for_slot<kFills, t, kSlots>([&](auto i) {
                     constexpr int q = decltype(i)::value;
-                    if constexpr (q < kLoads) fetch(cur, q);
-                    else ts.load(more, filler, q - kLoads);
+                    if constexpr (q < tb.kLoads) tb.load(bb, filler, q);
+                    else ts.load(more, filler, q - tb.kLoads);
                 });
             });
         };
 
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) fetch(l0, q);
+        for (int q = 0; q < ta.kLoads; ++q) ta.load(a0, filler, q);
+#pragma unroll
+        for (int q = 0; q < tb.kLoads; ++q) tb.load(b0, filler, q);
 #pragma unroll
         for (int q = 0; q < ts.kLoads; ++q) ts.load(e0, filler, q);
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) fetch(l1, q);
+        for (int q = 0; q < ts.kLoads; ++q) ts.load(e1, filler, q);
+#pragma unroll
+        for (int q = 0; q < ta.kLoads; ++q) ta.load(a1, filler, q);
+#pragma unroll
+        for (int q = 0; q < tb.kLoads; ++q) tb.load(b1, filler, q);
         arrive<kShared>();
         settle(acc);
 #pragma unroll
-        for (int f = 0; f < kFI + kFJ; ++f) {
-            read(l0, 0, f);
-            read_scale(e0, 0, 0, f);
+        for (int f = 0; f < kFI; ++f) {
+            x[f] = fa.get(a0, f, 0);
+            y[0][f] = fa.get(a0, f, 1);
+            sa[0][f] = fa.get_scale(e0, f, 0);
+        }
+#pragma unroll
+        for (int f = 0; f < kFJ; ++f) {
+            b[0][f] = fb.get(b0, f, 0);
+            sb[0][f] = fb.get_scale(e0, f, 0);
         }
         // Four steps a turn of the loop, so that each LDS access names its buffer.  An
         // odd count takes one more step, over zeros.
         for (;;) {
-            step(l0, l1, 0, e0, 1, std::true_type(), e1);
-            step(l1, l0, 1, e1, 0, std::false_type(), e1);
+            step(a0, b0, a1, b1, 0, e0, 1, std::false_type(), e0);
+            step(a1, b1, a0, b0, 1, e1, 0, std::true_type(), e0);
             if (--turns <= 0) break;
-            step(l0, l1, 0, e1, 1, std::true_type(), e0);
-            step(l1, l0, 1, e0, 0, std::false_type(), e0);
+            step(a0, b0, a1, b1, 0, e1, 1, std::false_type(), e1);
+            step(a1, b1, a0, b0, 1, e0, 0, std::true_type(), e1);
             if (--turns <= 0) break;
         }
         settle(acc);
     }
-    finish<BM, BN, WI, WJ, KW>(g, acc, l0, l1, (Lds*)s0, split, i0, j0, lane, wave);
+    arrive<kShared>();  // the last stages are being read and filled until here
+    if constexpr (KW == 1) {
+        static_assert(WI * WJ == 4 && kStageA >= 64 * kWN * 4 && kStageB >= 64 * kWN * 4, "a piece of LDS for each wave");
+        mx4_finish(g, acc, wave == 0 ? a0 : wave == 1 ? b0 : wave == 2 ? a1 : b1, split, i0 + wi * kWM, j0 + wj * kWN, lane);
+    } else {
+        // The waves' sums of the tile through LDS, in the waves' order: rows of 256
+        // bytes, the first half of them where A's first stage was, the others where B's
+        // was, their chunks of 16 bytes permuted by the row.
+        using Quad = __attribute__((address_space(3))) f32x4;
+        auto at = [&](int w, int r) { return (r < 32 ? (Lds*)sa0 + w * kStageA : (Lds*)sb0 + w * kStageB) + (r & 31) * 256; };
+#pragma unroll
+        for (int i = 0; i < kFI; ++i)
+#pragma unroll
+            for (int j = 0; j < kFJ; ++j) *(Quad*)(at(wave, i * 16 + lo) + (((j * 4 + (lane >> 4)) ^ lo) << 4)) = acc[i][j];
+        __syncthreads();
+        constexpr int kBatch = 64 / KW / 8;
+        const int c = lane & 7, col = j0 + c * 8, r0 = wave * (64 / KW) + (lane >> 3);
+        float v[kBatch][8];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int r = r0 + q * 8;
+            f32x4 s = {0, 0, 0, 0}, u = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                s += *(const Quad*)(at(w, r) + (((c * 2) ^ (r & 15)) << 4));
+                u += *(const Quad*)(at(w, r) + (((c * 2 + 1) ^ (r & 15)) << 4));
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                v[q][t] = s[t];
+                v[q][4 + t] = u[t];
+            }
+        }
+        if (g.splits > 1) {
+            float* const sums = g.part + static_cast<int64_t>(split) * g.m * g.pitch;
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int row = i0 + r0 + q * 8;
+                if (row < g.m && col < g.pitch) store8(sums + static_cast<int64_t>(row) * g.pitch + col, 8, v[q]);
+            }
+        } else if (col < g.n) {
+            epilogue8<kBatch>(g.e, i0 + r0, 8, g.m, col, g.n - col, 1.0f, mask_offset(g.e.mask), v);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- host
