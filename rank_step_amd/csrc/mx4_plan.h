@@ -47,6 +47,25 @@ inline Parts mx4_parts_of(int64_t k, int64_t splits) {
     return {static_cast<int32_t>(ceil_div(turns, per)), static_cast<int32_t>(per * 2 * kBK)};
 }
 
+// Whether the product takes the way for few rows of A.
+inline bool mx4_few(int64_t m) { return m <= 32; }
+
+// The columns of a workgroup of that way: A is read again by each, B's rows
+// once, and the CU with the most workgroups ends last; so the least rounds *
+// bytes of one.
+inline int mx4_few_features(int64_t m, int64_t n) {
+    int best = 0;
+    int64_t cost = 0;
+    for (int jb = 1; jb <= 4; ++jb) {
+        const int64_t c = ceil_div(ceil_div(n, 16 * jb), kCus) * (16 * jb + m);
+        if (best == 0 || c < cost) {
+            best = jb;
+            cost = c;
+        }
+    }
+    return best;
+}
+
 inline Way mx4_best_way(const Extent& g, const Space& space) { return best_way<true>(g, space); }
 
 }  // namespace linear

@@ -301,7 +301,10 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
             constexpr int KK = decltype(kk)::value;
             for_constants<kSlots>([&](auto slot) {
                 constexpr int t = decltype(slot)::value;
-                mx4_mfma<KK>(acc[t / kFJ][t % kFJ], b[KK][t % kFJ], KK ? y[p][t / kFJ] : x[t / kFJ], sb[p][t % kFJ], sa[p][t / kFJ]);
+                // 2 x 2 blocks, each product with one operand of the one before: a percent less
+                // power than row by row, and so time
+                constexpr int i = t / 4 / (kFJ / 2) * 2 + t % 4 / 2, j = t / 4 % (kFJ / 2) * 2 + (t % 4 / 2 ? 1 - t % 2 : t % 2);
+                mx4_mfma<KK>(acc[i][j], b[KK][j], KK ? y[p][i] : x[i], sb[p][j], sa[p][i]);
                 __builtin_amdgcn_sched_barrier(0);
                 between(slot);
                 __builtin_amdgcn_sched_barrier(0);
@@ -432,6 +435,116 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
     }
 }
 
+// The product for at most 16 * MB rows of A: bound by reading B once.  As
+// few_rows_kernel, with the eight waves taking every eighth 512 contraction
+// elements, 256 bytes of a row and 16 scales, from memory straight into the
+// fragments: lane group q takes blocks 4q to 4q + 3, whose scales are one word.
+template <int MB, int JB>
+__global__ __launch_bounds__(kFewWaves * 64) void mx4_few_rows_kernel(Mx4Product g) {
+    typedef int i32x8 __attribute__((ext_vector_type(8)));
+    constexpr int kPitch = 20;  // floats of 16, padded against bank conflicts
+    __shared__ __attribute__((aligned(16))) float sums[kFewWaves][MB][JB][16 * kPitch];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lo = lane & 15, q = lane >> 4;
+    const int j0 = blockIdx.x * (16 * JB);
+    // Rows past the end are read as the last one; what they give is not stored.
+    const uint8_t *a[MB], *as[MB], *b[JB], *bs[JB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int64_t row = min(i * 16 + lo, g.m - 1);
+        a[i] = static_cast<const uint8_t*>(g.a) + row * g.lda * 2 + q * 64;
+        as[i] = g.sa + row * g.ldsa + q * 4;
+    }
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+        const int64_t row = min(j0 + j * 16 + lo, g.n - 1);
+        b[j] = static_cast<const uint8_t*>(g.b) + row * g.ldb * 2 + q * 64;
+        bs[j] = g.sb + row * g.ldsb + q * 4;
+    }
+    f32x4 acc[MB][JB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    struct Chunk {
+        u32x4 a[MB][4], b[JB][4];
+        int as[MB], bs[JB];
+    };
+    const int blocks = g.k / 8, full = blocks / 16, all = (blocks + 15) / 16;
+    // END: the chunk may end behind the rows' end (its scales are there all the same).
+    auto load = [&](Chunk& c, int at, auto end) {
+        auto block = [&](const uint8_t* row, int t) {
+            if (decltype(end)::value && at * 16 + q * 4 + t >= blocks) return u32x4{0, 0, 0, 0};
+            return *reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(at) * 256 + t * 16);
+        };
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            c.bs[j] = *reinterpret_cast<const int*>(bs[j] + at * 16);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) c.b[j][t] = block(b[j], t);
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            c.as[i] = *reinterpret_cast<const int*>(as[i] + at * 16);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) c.a[i][t] = block(a[i], t);
+        }
+    };
+    auto multiply = [&](const Chunk& c) {
+        auto operand = [](const u32x4& v) {
+            return i32x8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]), 0, 0, 0, 0};
+        };
+        for_constants<4>([&](auto which) {
+            constexpr int t = decltype(which)::value;
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int j = 0; j < JB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(c.b[j][t]), operand(c.a[i][t]), acc[i][j],
+                                                                                 4, 4, t, c.bs[j], t, c.as[i]);
+        });
+    };
+    int c = wave;
+    auto batches = [&](auto ahead) {
+        constexpr int kN = decltype(ahead)::value;
+        for (; c + (kN - 1) * kFewWaves < full; c += kN * kFewWaves) {
+            Chunk r[kN];
+#pragma unroll
+            for (int u = 0; u < kN; ++u) load(r[u], c + u * kFewWaves, std::false_type{});
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < kN; ++u) multiply(r[u]);
+        }
+    };
+    if constexpr (MB + JB <= 2) batches(std::integral_constant<int, 4>{});
+    batches(std::integral_constant<int, 2>{});
+    for (; c < all; c += kFewWaves) {
+        Chunk r;
+        if (c < full) load(r, c, std::false_type{});
+        else load(r, c, std::true_type{});
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(r);
+    }
+    // Lane: row lo, columns 4 q + 0..3.
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) *reinterpret_cast<f32x4*>(&sums[wave][i][j][lo * kPitch + q * 4]) = acc[i][j];
+    __syncthreads();
+    const int t = threadIdx.x, half = t & 1, j = (t >> 1) % JB, i = t / (2 * JB);  // 16 MB rows of 2 JB pieces
+    const int col = j0 + j * 16 + half * 8;
+    if (i >= g.m || i >= 16 * MB || col >= g.n) return;
+    float v[1][8] = {{0, 0, 0, 0, 0, 0, 0, 0}};
+#pragma unroll
+    for (int p = 0; p < kFewWaves; ++p) {
+        const float* s = &sums[p][i >> 4][j][(i & 15) * kPitch + half * 8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[0][u] += s[u];
+    }
+    epilogue8<1>(g.e, i, 0, g.m, col, g.n - col, 1.0f, mask_offset(g.e.mask), v);
+}
+
 // ---------------------------------------------------------------- host
 
 template <int BM, int BN, int WI, int WJ, int KW>
@@ -449,8 +562,24 @@ int32_t launch_mx4(Mx4Product& g, hipStream_t stream, const char* who) {
     return launched(who);
 }
 
+template <int MB>
+int32_t run_mx4_few(const Mx4Product& g, hipStream_t stream, const char* who) {
+    const int features = mx4_few_features(g.m, g.n);
+    const int64_t blocks = ceil_div(g.n, 16 * features);
+    if (blocks > kMaxBlocks) return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
+    const dim3 grid(static_cast<uint32_t>(blocks)), block(kFewWaves * 64);
+    switch (features) {
+        case 1: mx4_few_rows_kernel<MB, 1><<<grid, block, 0, stream>>>(g); break;
+        case 2: mx4_few_rows_kernel<MB, 2><<<grid, block, 0, stream>>>(g); break;
+        case 3: mx4_few_rows_kernel<MB, 3><<<grid, block, 0, stream>>>(g); break;
+        default: mx4_few_rows_kernel<MB, 4><<<grid, block, 0, stream>>>(g);
+    }
+    return launched(who);
+}
+
 // The product whole, or its two parts after a cut.
 int32_t run_mx4(Mx4Product& g, const Space& space, hipStream_t stream, const char* who) {
+    if (mx4_few(g.m)) return g.m <= 16 ? run_mx4_few<1>(g, stream, who) : run_mx4_few<2>(g, stream, who);
     const Way best = mx4_best_way(g.extent(), space);
     if (best.us == kNoWay) return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
     const Parts p = mx4_parts_of(g.k, best.splits);
