@@ -220,15 +220,20 @@ inline Parts parts_of(int64_t k, int64_t splits) {
 }
 
 // The least estimate for the whole product.
-template <bool BL>
-inline Way best_way(const Extent& g, const Space& space) {
-    Way best = way_of<BL>(256, 1, g);
+using Estimate = Way(int tile, int64_t splits, const Extent& g);
+template <Estimate WAY>
+inline Way best_way_by(const Extent& g, const Space& space) {
+    Way best = WAY(256, 1, g);
     for (int tile : {128, 64})
         for (int64_t fill : {int64_t(0), int64_t(kCus), int64_t(2 * kCus)}) {
-            const Way w = way_of<BL>(tile, splits_for(tile, fill, g, space), g);
+            const Way w = WAY(tile, splits_for(tile, fill, g, space), g);
             if (w.us < best.us) best = w;
         }
     return best;
+}
+template <bool BL>
+inline Way best_way(const Extent& g, const Space& space) {
+    return best_way_by<way_of<BL>>(g, space);
 }
 
 // Where to cut `along` output rows (columns) into whole rounds of 256-tiles and
@@ -252,23 +257,27 @@ inline Extent rows_of(const Extent& g, int64_t m) { return {static_cast<int32_t>
 struct Cut {
     int64_t columns, rows;  // the first part's (a multiple of 256), or 0; at most one is set
 };
-template <bool BL>
-inline Cut cut_of(const Extent& g, const Way& best, const Space& space) {
+template <Estimate WAY>
+inline Cut cut_by(const Extent& g, const Way& best, const Space& space) {
     const int64_t cj = round_cut(g.n, g.m), ci = round_cut(g.m, g.n);
     double us = 0.96 * best.us;
     Cut cut{0, 0};
     if (cj > 0) {
-        const double c = best_way<BL>(columns_of(g, cj), space).us + best_way<BL>(columns_of(g, g.n - cj), space).us;
+        const double c = best_way_by<WAY>(columns_of(g, cj), space).us + best_way_by<WAY>(columns_of(g, g.n - cj), space).us;
         if (c < us) {
             us = c;
             cut = {cj, 0};
         }
     }
     if (ci > 0) {
-        const double c = best_way<BL>(rows_of(g, ci), space).us + best_way<BL>(rows_of(g, g.m - ci), space).us;
+        const double c = best_way_by<WAY>(rows_of(g, ci), space).us + best_way_by<WAY>(rows_of(g, g.m - ci), space).us;
         if (c < us) cut = {0, ci};
     }
     return cut;
+}
+template <bool BL>
+inline Cut cut_of(const Extent& g, const Way& best, const Space& space) {
+    return cut_by<way_of<BL>>(g, best, space);
 }
 
 // Whether the forward product takes the way for few tokens.  Up to 16 tokens,

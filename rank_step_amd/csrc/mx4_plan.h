@@ -47,8 +47,35 @@ inline Parts mx4_parts_of(int64_t k, int64_t splits) {
     return {static_cast<int32_t>(ceil_div(turns, per)), static_cast<int32_t>(per * 2 * kBK)};
 }
 
-// Whether the product takes the way for few rows of A.
-inline bool mx4_few(int64_t m) { return m <= 32; }
+// What a product takes in microseconds, as way_of in linear_plan.h: from times
+// measured over products of one 64 x 64 tile to 8192 x 11008 x 4096, within a
+// sixth of them but for the smallest.
+//   256: a step takes 1.1 us on a near empty chip, 1.6 on a full one, where
+//     power sets the clock.  4096 x 4096 x 4096: 39.5 us, by 128-tiles 45.2.
+//   128: two workgroups a CU, 1.08 us a step for both; alone 0.37 to 0.67.
+//     2048 x 2048 x 4096: 14.1 us, by 256-tiles 31.4, by 64-tiles 28.0.
+//   64: four waves on four parts of a step.  1024 x 1024 x 4096: 7.5 us, by
+//     128-tiles 11.9.  64 x 64 x 16384: 13.2 us, split in four 9.7.
+inline Way mx4_way_of(int tile, int64_t splits, const Extent& g) {
+    const double tiles = static_cast<double>(ceil_div(g.m, tile)) * ceil_div(g.n, tile) * splits;
+    const double steps = static_cast<double>(ceil_div(ceil_div(g.k, kBK), splits)), fill = std::min(1.0, tiles / kCus);
+    double us;
+    if (tile == 256) us = 3 + std::ceil(tiles / kCus) * (10 + (1.1 + 0.5 * fill) * steps);
+    else if (tile == 64) us = 0.5 + std::ceil(tiles / kCus) * (4.4 + 0.135 * steps);
+    else if (tiles <= kCus) us = 5.5 + (0.37 + 0.3 * fill) * steps;
+    else us = 1 + std::ceil(tiles / (2 * kCus)) * (4.6 + 1.08 * steps);
+    if (splits > 1) us += 3 + std::max(8.0 * splits * g.m * g.pitch / 6e6, 0.1 * (splits - 24));
+    return Way{tile, splits, tiles > kMaxBlocks ? kNoWay : us};
+}
+
+inline Way mx4_best_way(const Extent& g, const Space& space) { return best_way_by<mx4_way_of>(g, space); }
+
+inline Cut mx4_cut_of(const Extent& g, const Way& best, const Space& space) { return cut_by<mx4_way_of>(g, best, space); }
+
+// Whether the product takes the way for few rows of A: what one matrix
+// instruction takes.  32 rows by it and by tiles: [11008, 4096] 8.6 and 7.1 us,
+// [28672, 8192] 40.9 and 24.6, [4096, 4096] 6.3 and 7.0.
+inline bool mx4_few(int64_t m) { return m <= 16; }
 
 // The columns of a workgroup of that way: A is read again by each, B's rows
 // once, and the CU with the most workgroups ends last; so the least rounds *
@@ -65,8 +92,6 @@ inline int mx4_few_features(int64_t m, int64_t n) {
     }
     return best;
 }
-
-inline Way mx4_best_way(const Extent& g, const Space& space) { return best_way<true>(g, space); }
 
 }  // namespace linear
 }  // namespace fsdp

@@ -435,41 +435,36 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
     }
 }
 
-// The product for at most 16 * MB rows of A: bound by reading B once.  As
+// The product for at most 16 rows of A: bound by reading B once.  As
 // few_rows_kernel, with the eight waves taking every eighth 512 contraction
 // elements, 256 bytes of a row and 16 scales, from memory straight into the
 // fragments: lane group q takes blocks 4q to 4q + 3, whose scales are one word.
-template <int MB, int JB>
+template <int JB>
 __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_rows_kernel(Mx4Product g) {
     typedef int i32x8 __attribute__((ext_vector_type(8)));
     constexpr int kPitch = 20;  // floats of 16, padded against bank conflicts
-    __shared__ __attribute__((aligned(16))) float sums[kFewWaves][MB][JB][16 * kPitch];
+    __shared__ __attribute__((aligned(16))) float sums[kFewWaves][JB][16 * kPitch];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lo = lane & 15, q = lane >> 4;
     const int j0 = blockIdx.x * (16 * JB);
     // Rows past the end are read as the last one; what they give is not stored.
-    const uint8_t *a[MB], *as[MB], *b[JB], *bs[JB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-        const int64_t row = min(i * 16 + lo, g.m - 1);
-        a[i] = static_cast<const uint8_t*>(g.a) + row * g.lda * 2 + q * 64;
-        as[i] = g.sa + row * g.ldsa + q * 4;
-    }
+    const int64_t ra = min(lo, g.m - 1);
+    const uint8_t* const a = static_cast<const uint8_t*>(g.a) + ra * g.lda * 2 + q * 64;
+    const uint8_t* const as = g.sa + ra * g.ldsa + q * 4;
+    const uint8_t *b[JB], *bs[JB];
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
         const int64_t row = min(j0 + j * 16 + lo, g.n - 1);
         b[j] = static_cast<const uint8_t*>(g.b) + row * g.ldb * 2 + q * 64;
         bs[j] = g.sb + row * g.ldsb + q * 4;
     }
-    f32x4 acc[MB][JB];
+    f32x4 acc[JB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < JB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < JB; ++j) acc[j] = f32x4{0, 0, 0, 0};
 
     struct Chunk {
-        u32x4 a[MB][4], b[JB][4];
-        int as[MB], bs[JB];
+        u32x4 a[4], b[JB][4];
+        int as, bs[JB];
     };
     const int blocks = g.k / 8, full = blocks / 16, all = (blocks + 15) / 16;
     // END: the chunk may end behind the rows' end (its scales are there all the same).
@@ -484,12 +479,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_rows_kernel(Mx4Product
 #pragma unroll
             for (int t = 0; t < 4; ++t) c.b[j][t] = block(b[j], t);
         }
+        c.as = *reinterpret_cast<const int*>(as + at * 16);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
-            c.as[i] = *reinterpret_cast<const int*>(as[i] + at * 16);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) c.a[i][t] = block(a[i], t);
-        }
+        for (int t = 0; t < 4; ++t) c.a[t] = block(a, t);
     };
     auto multiply = [&](const Chunk& c) {
         auto operand = [](const u32x4& v) {
@@ -498,11 +490,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_rows_kernel(Mx4Product
         for_constants<4>([&](auto which) {
             constexpr int t = decltype(which)::value;
 #pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int j = 0; j < JB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(c.b[j][t]), operand(c.a[i][t]), acc[i][j],
-                                                                                 4, 4, t, c.bs[j], t, c.as[i]);
+            for (int j = 0; j < JB; ++j)
+                acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(c.b[j][t]), operand(c.a[t]), acc[j], 4, 4, t,
+                                                                          c.bs[j], t, c.as);
         });
     };
     int c = wave;
@@ -517,7 +507,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_rows_kernel(Mx4Product
             for (int u = 0; u < kN; ++u) multiply(r[u]);
         }
     };
-    if constexpr (MB + JB <= 2) batches(std::integral_constant<int, 4>{});
+    if constexpr (JB == 1) batches(std::integral_constant<int, 4>{});
     batches(std::integral_constant<int, 2>{});
     for (; c < all; c += kFewWaves) {
         Chunk r;
@@ -528,17 +518,15 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_rows_kernel(Mx4Product
     }
     // Lane: row lo, columns 4 q + 0..3.
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < JB; ++j) *reinterpret_cast<f32x4*>(&sums[wave][i][j][lo * kPitch + q * 4]) = acc[i][j];
+    for (int j = 0; j < JB; ++j) *reinterpret_cast<f32x4*>(&sums[wave][j][lo * kPitch + q * 4]) = acc[j];
     __syncthreads();
-    const int t = threadIdx.x, half = t & 1, j = (t >> 1) % JB, i = t / (2 * JB);  // 16 MB rows of 2 JB pieces
+    const int t = threadIdx.x, half = t & 1, j = (t >> 1) % JB, i = t / (2 * JB);  // 16 rows of 2 JB pieces
     const int col = j0 + j * 16 + half * 8;
-    if (i >= g.m || i >= 16 * MB || col >= g.n) return;
+    if (i >= g.m || col >= g.n) return;
     float v[1][8] = {{0, 0, 0, 0, 0, 0, 0, 0}};
 #pragma unroll
     for (int p = 0; p < kFewWaves; ++p) {
-        const float* s = &sums[p][i >> 4][j][(i & 15) * kPitch + half * 8];
+        const float* s = &sums[p][j][i * kPitch + half * 8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[0][u] += s[u];
     }
@@ -562,26 +550,47 @@ int32_t launch_mx4(Mx4Product& g, hipStream_t stream, const char* who) {
     return launched(who);
 }
 
-template <int MB>
 int32_t run_mx4_few(const Mx4Product& g, hipStream_t stream, const char* who) {
     const int features = mx4_few_features(g.m, g.n);
     const int64_t blocks = ceil_div(g.n, 16 * features);
     if (blocks > kMaxBlocks) return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
     const dim3 grid(static_cast<uint32_t>(blocks)), block(kFewWaves * 64);
     switch (features) {
-        case 1: mx4_few_rows_kernel<MB, 1><<<grid, block, 0, stream>>>(g); break;
-        case 2: mx4_few_rows_kernel<MB, 2><<<grid, block, 0, stream>>>(g); break;
-        case 3: mx4_few_rows_kernel<MB, 3><<<grid, block, 0, stream>>>(g); break;
-        default: mx4_few_rows_kernel<MB, 4><<<grid, block, 0, stream>>>(g);
+        case 1: mx4_few_rows_kernel<1><<<grid, block, 0, stream>>>(g); break;
+        case 2: mx4_few_rows_kernel<2><<<grid, block, 0, stream>>>(g); break;
+        case 3: mx4_few_rows_kernel<3><<<grid, block, 0, stream>>>(g); break;
+        default: mx4_few_rows_kernel<4><<<grid, block, 0, stream>>>(g);
     }
     return launched(who);
 }
 
+// Columns [j0, j0 + n) and rows [i0, i0 + m) of the product.
+Mx4Product mx4_columns(const Mx4Product& g, int64_t j0, int64_t n) {
+    Mx4Product s = g;
+    static_cast<Product&>(s) = columns<true>(g, false, j0, n);
+    s.sb += j0 * g.ldsb;
+    return s;
+}
+Mx4Product mx4_rows(const Mx4Product& g, int64_t i0, int64_t m) {
+    Mx4Product s = g;
+    static_cast<Product&>(s) = rows<true>(g, i0, m);
+    s.sa += i0 * g.ldsa;
+    return s;
+}
+
 // The product whole, or its two parts after a cut.
 int32_t run_mx4(Mx4Product& g, const Space& space, hipStream_t stream, const char* who) {
-    if (mx4_few(g.m)) return g.m <= 16 ? run_mx4_few<1>(g, stream, who) : run_mx4_few<2>(g, stream, who);
+    if (mx4_few(g.m)) return run_mx4_few(g, stream, who);
     const Way best = mx4_best_way(g.extent(), space);
     if (best.us == kNoWay) return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
+    const Cut cut = mx4_cut_of(g.extent(), best, space);
+    if (cut.columns + cut.rows > 0) {
+        const int64_t cj = cut.columns, ci = cut.rows;
+        Mx4Product p = cj > 0 ? mx4_columns(g, 0, cj) : mx4_rows(g, 0, ci);
+        Mx4Product q = cj > 0 ? mx4_columns(g, cj, g.n - cj) : mx4_rows(g, ci, g.m - ci);
+        const int32_t st = run_mx4(p, space, stream, who);
+        return st != FSDP_OK ? st : run_mx4(q, space, stream, who);
+    }
     const Parts p = mx4_parts_of(g.k, best.splits);
     g.splits = p.n;
     g.kper = p.k;
