@@ -25,10 +25,22 @@ using namespace fsdp::linear;
 
 // ---------------------------------------------------------------- sums over a row
 
+// The sum over the wave, in every lane: within quads, eights and 16s by DPP
+// moves, then over the four 16s by the lane swaps; both lanes of a pair add the
+// same two values, so all lanes hold the same bits.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+    auto dpp = [](float x, auto ctrl) {
+        return __uint_as_float(static_cast<uint32_t>(
+            __builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(x)), decltype(ctrl)::value, 0xf, 0xf, true)));
+    };
+    v += dpp(v, std::integral_constant<int, 0xB1>());   // quad_perm 1 0 3 2
+    v += dpp(v, std::integral_constant<int, 0x4E>());   // quad_perm 2 3 0 1
+    v += dpp(v, std::integral_constant<int, 0x141>());  // row_half_mirror
+    v += dpp(v, std::integral_constant<int, 0x140>());  // row_mirror
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // The sums of N values over a row's waves, in the waves' order.  `s` is not
@@ -53,40 +65,78 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*s)[WAVES]) {
     }
 }
 
-// `cnt` (at most N) parameters from p on in fp32, `none` where there are none.
+// N parameters from element j on in fp32, `none` where there is no vector.  Of a
+// row's last, shorter chunk (back > 0) the N that end with the row are read and
+// moved down, as stream_load does; of rows shorter than a chunk (back < 0) each.
 template <int N>
-__device__ __forceinline__ void load_params(const void* p, int f32, int64_t j, int cnt, float none, float (&v)[N]) {
+__device__ __forceinline__ void load_params(const void* p, int f32, int64_t j, int cnt, int back, float none, float (&v)[N]) {
 #pragma unroll
     for (int q = 0; q < N; ++q) v[q] = none;
-    if (!p) return;
+    if (!p || cnt <= 0) return;
+    if (back < 0) {
 #pragma unroll
-    for (int q = 0; q < N; ++q)
-        if (q < cnt) v[q] = f32 ? static_cast<const float*>(p)[j + q] : widen(static_cast<const uint16_t*>(p)[j + q]);
+        for (int q = 0; q < N; ++q)
+            if (q < cnt) v[q] = f32 ? static_cast<const float*>(p)[j + q] : widen(static_cast<const uint16_t*>(p)[j + q]);
+        return;
+    }
+    struct __attribute__((packed, aligned(4))) Floats { float v[N]; };
+    struct __attribute__((packed, aligned(2))) Halves { uint16_t v[N]; };
+    if (f32) {
+        const Floats w = *reinterpret_cast<const Floats*>(static_cast<const float*>(p) + j - back);
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = w.v[q];
+    } else {
+        const Halves w = *reinterpret_cast<const Halves*>(static_cast<const uint16_t*>(p) + j - back);
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = widen(w.v[q]);
+    }
+    if (back > 0) {
+#pragma unroll
+        for (int d = N / 2; d > 0; d /= 2)
+            if (back & d)
+#pragma unroll
+                for (int q = 0; q + d < N; ++q) v[q] = v[q + d];
+    }
 }
 
 // A thread's chunks of a row: chunk c starts at element (c * 64 WAVES + t) * E.
-template <typename T, int WAVES, int C>
+// TAIL: the row's last chunk may be shorter.
+template <typename T, int WAVES, int C, bool TAIL>
 struct Row {
     static constexpr int kEach = 16 / sizeof(T);
-    int64_t j[C];
-    int cnt[C], back[C];  // elements of the chunk inside the row, at most 0 outside
+    int first;  // of the thread's first chunk
+    int n;
 
-    __device__ __forceinline__ void init(int t, int64_t n) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            j[c] = (static_cast<int64_t>(c) * (64 * WAVES) + t) * kEach;
-            cnt[c] = static_cast<int>(max(static_cast<int64_t>(0), min(n - j[c], static_cast<int64_t>(kEach))));
-            back[c] = chunk_back<T>(cnt[c], n);
-        }
+    __device__ __forceinline__ void init(int t, int64_t len) {
+        first = t * kEach;
+        n = static_cast<int>(len);
     }
+    __device__ __forceinline__ int at(int c) const { return first + c * (64 * WAVES * kEach); }
+    __device__ __forceinline__ bool has(int c) const { return at(c) < n; }
+    // elements of a chunk that the row has
+    __device__ __forceinline__ int cnt(int c) const { return TAIL ? min(n - at(c), kEach) : kEach; }
+    __device__ __forceinline__ int back(int c) const { return TAIL ? chunk_back<T>(cnt(c), n) : 0; }
     __device__ __forceinline__ void load(const T* row, u32x4 (&w)[C]) const {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             w[c] = u32x4{0, 0, 0, 0};
-            if (cnt[c] > 0) w[c] = stream_load(row + j[c], cnt[c], back[c]);
+            if (has(c)) w[c] = stream_load(row + at(c), cnt(c), back(c));
         }
     }
+    // Chunk c's values, zeros behind the row's end.
+    __device__ __forceinline__ void values(const u32x4 (&w)[C], int c, float (&v)[kEach]) const {
+        arrange(w[c], TAIL && has(c) ? back(c) : 0, v);
+    }
+    __device__ __forceinline__ bool inside(int c, int q) const { return TAIL ? at(c) + q < n : has(c); }
 };
+
+// Packed chunks whose widened values are not kept from here on: the compiler
+// would rather hold them, at twice the registers of bf16, than widen again.
+template <int C>
+__device__ __forceinline__ void widen_again(u32x4 (&w)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(w[c])::"memory");
+}
 
 // ---------------------------------------------------------------- forward
 
@@ -102,48 +152,49 @@ struct ForwardArgs {
     int32_t w_f32, rms, wt;
 };
 
-// A row by WAVES waves of C chunks of 16 bytes a lane.
-template <typename T, int WAVES, int C>
+// A row by WAVES waves of C chunks of 16 bytes a lane, which stay packed in
+// registers and are widened for each pass over them.  Bound by memory: 8192 x
+// 4096 bf16 with one wave a row, whose 8 KB need no barrier, XXX us; by four waves
+// 42, as a workgroup then has little on its way while it waits for its sums.
+template <typename T, int WAVES, int C, bool TAIL>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_kernel(ForwardArgs a) {
     constexpr int kEach = 16 / sizeof(T), kRows = WAVES == 1 ? 4 : 1;
     __shared__ float s0[1][WAVES], s1[2][WAVES];
     const int t = threadIdx.x % (64 * WAVES);
-    Row<T, WAVES, C> row;
+    Row<T, WAVES, C, TAIL> row;
     row.init(t, a.n);
-    float w[C][kEach], b[C][kEach];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        load_params(a.w, a.w_f32, row.j[c], row.cnt[c], 1.0f, w[c]);
-        load_params(a.b, a.w_f32, row.j[c], row.cnt[c], 0.0f, b[c]);
-    }
     const float n = static_cast<float>(a.n);
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / (64 * WAVES); i < a.m;
          i += static_cast<int64_t>(gridDim.x) * kRows) {
         u32x4 raw[C];
         row.load(static_cast<const T*>(a.x) + i * a.ldx, raw);
-        float v[C][kEach];
-#pragma unroll
-        for (int c = 0; c < C; ++c) arrange(raw[c], row.back[c], v[c]);
         float mean = 0.0f;
         if (!a.rms) {
             float sum[1] = {0.0f};
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int c = 0; c < C; ++c) {
+                float v[kEach];
+                row.values(raw, c, v);
 #pragma unroll
-                for (int q = 0; q < kEach; ++q) sum[0] += v[c][q];
+                for (int q = 0; q < kEach; ++q) sum[0] += v[q];
+            }
             row_sum<WAVES>(sum, s0);
             mean = sum[0] / n;
+            widen_again(raw);
         }
         // About that mean, whose own rounding and sum the first moment corrects.
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            float v[kEach];
+            row.values(raw, c, v);
 #pragma unroll
             for (int q = 0; q < kEach; ++q) {
-                const float d = q < row.cnt[c] ? v[c][q] - mean : 0.0f;
+                const float d = row.inside(c, q) ? v[q] - mean : 0.0f;
                 sum[0] += d;
                 sum[1] = fmaf(d, d, sum[1]);
             }
+        }
         row_sum<WAVES>(sum, s1);
         float var = sum[1] / n;
         if (!a.rms) {
@@ -157,12 +208,17 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_ke
             if (a.mean) a.mean[i] = mean;
             if (a.rstd) a.rstd[i] = rstd;
         }
+        widen_again(raw);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (row.cnt[c] <= 0) continue;
+            if (!row.has(c)) continue;
+            float v[kEach], w[kEach], b[kEach];
+            load_params(a.w, a.w_f32, row.at(c), row.cnt(c), row.back(c), 1.0f, w);
+            load_params(a.b, a.w_f32, row.at(c), row.cnt(c), row.back(c), 0.0f, b);
+            row.values(raw, c, v);
 #pragma unroll
-            for (int q = 0; q < kEach; ++q) v[c][q] = fmaf((v[c][q] - mean) * rstd, w[c][q], b[c][q]);
-            stream_store(static_cast<T*>(a.y) + i * a.ldy + row.j[c], row.cnt[c], a.wt, v[c]);
+            for (int q = 0; q < kEach; ++q) v[q] = fmaf((v[q] - mean) * rstd, w[q], b[q]);
+            stream_store(static_cast<T*>(a.y) + i * a.ldy + row.at(c), row.cnt(c), a.wt, v);
         }
         // s0's and s1's next writes come behind a barrier of the other; alone, behind this one.
         if (WAVES > 1 && a.rms) __syncthreads();
@@ -210,8 +266,8 @@ __global__ __launch_bounds__(kLongBlock) void norm_forward_long_kernel(ForwardAr
         }
         for (int64_t j = threadIdx.x; j < a.n; j += kLongBlock) {
             float w[1], b[1];
-            load_params(a.w, a.w_f32, j, 1, 1.0f, w);
-            load_params(a.b, a.w_f32, j, 1, 0.0f, b);
+            load_params(a.w, a.w_f32, j, 1, 0, 1.0f, w);
+            load_params(a.b, a.w_f32, j, 1, 0, 0.0f, b);
             const float v = fmaf((value(j) - mean) * rstd, w[0], b[0]);
             if constexpr (sizeof(T) == 2) y[j] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
             else y[j] = v;
@@ -236,61 +292,80 @@ struct BackwardArgs {
 };
 
 // dx, and the column sums of the rows that a thread passes, which it holds for
-// the columns of its chunks.
-template <typename T, int WAVES, int C>
+// the columns of its chunks.  Rows stay packed in registers, and the next one is
+// on its way while one is summed.
+template <typename T, int WAVES, int C, bool TAIL>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_backward_kernel(BackwardArgs a) {
     constexpr int kEach = 16 / sizeof(T), kRows = WAVES == 1 ? 4 : 1;
     __shared__ float s[2][2][WAVES];
     const int t = threadIdx.x % (64 * WAVES);
-    Row<T, WAVES, C> row;
+    Row<T, WAVES, C, TAIL> row;
     row.init(t, a.n);
     float w[C][kEach], dw[C][kEach], db[C][kEach];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        load_params(a.w, a.w_f32, row.j[c], row.cnt[c], 1.0f, w[c]);
+        load_params(a.w, a.w_f32, row.at(c), row.has(c) ? row.cnt(c) : 0, row.back(c), 1.0f, w[c]);
 #pragma unroll
         for (int q = 0; q < kEach; ++q) dw[c][q] = db[c][q] = 0.0f;
     }
     const float n = static_cast<float>(a.n);
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / (64 * WAVES);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    struct Rows {
+        u32x4 x[C], dy[C], res[C];
+        float mean, rstd;
+    };
+    auto load = [&](int64_t i, Rows& r) {
+        row.load(static_cast<const T*>(a.dy) + i * a.lddy, r.dy);
+        row.load(static_cast<const T*>(a.x) + i * a.ldx, r.x);
+        if (a.res) row.load(static_cast<const T*>(a.res) + i * a.ldr, r.res);
+        r.mean = a.rms ? 0.0f : a.mean[i];
+        r.rstd = a.rstd[i];
+    };
     int turn = 0;
-    for (int64_t i = first; i < a.m; i += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
-        u32x4 rx[C], rdy[C], rres[C];
-        row.load(static_cast<const T*>(a.dy) + i * a.lddy, rdy);
-        row.load(static_cast<const T*>(a.x) + i * a.ldx, rx);
-        if (a.res) row.load(static_cast<const T*>(a.res) + i * a.ldr, rres);
-        const float mean = a.rms ? 0.0f : a.mean[i], rstd = a.rstd[i];
-        float x[C][kEach], g[C][kEach];
+    Rows r;
+    if (first < a.m) load(first, r);
+    for (int64_t i = first; i < a.m; i += step, turn ^= 1) {
+        Rows next;
+        const bool more = i + step < a.m;
+        if (more) load(i + step, next);
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            arrange(rx[c], row.back[c], x[c]);
-            arrange(rdy[c], row.back[c], g[c]);
+            float x[kEach], g[kEach];
+            row.values(r.x, c, x);
+            row.values(r.dy, c, g);
 #pragma unroll
             for (int q = 0; q < kEach; ++q) {
-                x[c][q] = q < row.cnt[c] ? (x[c][q] - mean) * rstd : 0.0f;
-                dw[c][q] = fmaf(g[c][q], x[c][q], dw[c][q]);
-                db[c][q] += g[c][q];
-                g[c][q] *= w[c][q];
-                sum[0] += g[c][q];
-                sum[1] = fmaf(g[c][q], x[c][q], sum[1]);
+                const float xhat = row.inside(c, q) ? (x[q] - r.mean) * r.rstd : 0.0f;
+                dw[c][q] = fmaf(g[q], xhat, dw[c][q]);
+                db[c][q] += g[q];
+                const float gw = g[q] * w[c][q];
+                sum[0] += gw;
+                sum[1] = fmaf(gw, xhat, sum[1]);
             }
         }
-        if (!a.dx) continue;
-        row_sum<WAVES>(sum, s[turn]);
-        const float m1 = a.rms ? 0.0f : sum[0] / n, m2 = sum[1] / n;
+        if (a.dx) {
+            row_sum<WAVES>(sum, s[turn]);
+            const float m1 = a.rms ? 0.0f : sum[0] / n, m2 = sum[1] / n;
+            widen_again(r.x);
+            widen_again(r.dy);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (row.cnt[c] <= 0) continue;
-            float r[kEach];
-            if (a.res) arrange(rres[c], row.back[c], r);
+            for (int c = 0; c < C; ++c) {
+                if (!row.has(c)) continue;
+                float x[kEach], g[kEach], res[kEach];
+                row.values(r.x, c, x);
+                row.values(r.dy, c, g);
+                if (a.res) row.values(r.res, c, res);
 #pragma unroll
-            for (int q = 0; q < kEach; ++q) {
-                const float v = rstd * (g[c][q] - m1 - x[c][q] * m2);
-                g[c][q] = a.res ? v + r[q] : v;
+                for (int q = 0; q < kEach; ++q) {
+                    const float xhat = (x[q] - r.mean) * r.rstd, v = r.rstd * (g[q] * w[c][q] - m1 - xhat * m2);
+                    g[q] = a.res ? v + res[q] : v;
+                }
+                stream_store(static_cast<T*>(a.dx) + i * a.lddx + row.at(c), row.cnt(c), a.wt, g);
             }
-            stream_store(static_cast<T*>(a.dx) + i * a.lddx + row.j[c], row.cnt[c], a.wt, g[c]);
         }
+        if (more) r = next;
     }
     if (!a.part) return;
     float* p = a.part + first * 2 * a.n;
@@ -298,9 +373,9 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_backward_k
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int q = 0; q < kEach; ++q)
-            if (q < row.cnt[c]) {
-                p[row.j[c] + q] = dw[c][q];
-                p[a.n + row.j[c] + q] = db[c][q];
+            if (row.inside(c, q)) {
+                p[row.at(c) + q] = dw[c][q];
+                p[a.n + row.at(c) + q] = db[c][q];
             }
 }
 
@@ -318,7 +393,7 @@ __global__ __launch_bounds__(kLongBlock) void norm_backward_long_kernel(Backward
         };
         auto terms = [&](int64_t j, float& xhat) {
             float w[1];
-            load_params(a.w, a.w_f32, j, 1, 1.0f, w);
+            load_params(a.w, a.w_f32, j, 1, 0, 1.0f, w);
             xhat = (value(a.x, i * a.ldx + j) - mean) * rstd;
             return value(a.dy, i * a.lddy + j) * w[0];
         };
@@ -426,45 +501,46 @@ int elem_of(int32_t dtype) { return dtype == FSDP_DT_BF16 ? 2 : 4; }
 struct Division {
     int waves, chunks;
 };
-// The backward pass holds five values an element, which 16 waves of 4 chunks
-// have no registers for.
-Division division_of(int64_t n, int elem, bool backward) {
+
+// By its length alone, so that a row's result is the same among any others.
+Division forward_division(int64_t n, int elem) {
     const int64_t chunks = ceil_div(n, 16 / elem);
-    for (const Division d : {Division{1, 1}, {1, 2}, {4, 1}, {4, 2}, {4, 4}, {16, 2}, {16, 4}})
-        if (chunks <= int64_t(64) * d.waves * d.chunks) return backward && d.waves * d.chunks > 32 ? Division{0, 0} : d;
+    for (const Division d : {Division{1, 1}, {1, 2}, {1, 4}, {1, 8}, {4, 4}, {16, 2}, {16, 4}})
+        if (chunks <= int64_t(64) * d.waves * d.chunks) return d;
     return {0, 0};
 }
 
-// Workgroups for m rows: enough to fill the chip, each with several rows of a long batch.
-int64_t blocks_for(const Division& d, int64_t m) {
-    return d.waves == 1 ? std::min<int64_t>(ceil_div(m, 4), 8 * kCus) : std::min<int64_t>(m, (d.waves == 4 ? 8 : 2) * kCus);
+// The backward pass holds the column sums and two rows as well.
+Division backward_division(int64_t n, int elem) {
+    const int64_t chunks = ceil_div(n, 16 / elem);
+    for (const Division d : {Division{1, 1}, {1, 2}, {4, 1}, {4, 2}, {4, 4}})
+        if (chunks <= int64_t(64) * d.waves * d.chunks) return d;
+    return {0, 0};
 }
 
 // f(waves, chunks) with constants
-template <bool LONGEST, typename F>
-void with_division(const Division& d, F&& f) {
-    using std::integral_constant;
-    if (d.waves == 1 && d.chunks == 1) f(integral_constant<int, 1>(), integral_constant<int, 1>());
-    else if (d.waves == 1) f(integral_constant<int, 1>(), integral_constant<int, 2>());
-    else if (d.waves == 4 && d.chunks == 1) f(integral_constant<int, 4>(), integral_constant<int, 1>());
-    else if (d.waves == 4 && d.chunks == 2) f(integral_constant<int, 4>(), integral_constant<int, 2>());
-    else if (d.waves == 4) f(integral_constant<int, 4>(), integral_constant<int, 4>());
-    else if (d.chunks == 2) f(integral_constant<int, 16>(), integral_constant<int, 2>());
-    else if constexpr (LONGEST) f(integral_constant<int, 16>(), integral_constant<int, 4>());
+template <int W, int C, typename F>
+bool with(const Division& d, F&& f) {
+    if (d.waves != W || d.chunks != C) return false;
+    f(std::integral_constant<int, W>(), std::integral_constant<int, C>());
+    return true;
 }
 
 template <typename T>
 void launch_forward(const ForwardArgs& a, hipStream_t stream) {
-    const Division d = division_of(a.n, sizeof(T), false);
-    if (d.waves == 0) {
-        const uint32_t blocks = static_cast<uint32_t>(std::min<int64_t>(a.m, 2 * kCus));
-        norm_forward_long_kernel<T><<<dim3(blocks), dim3(kLongBlock), 0, stream>>>(a);
-        return;
-    }
-    with_division<true>(d, [&](auto waves, auto chunks) {
+    const Division d = forward_division(a.n, sizeof(T));
+    auto run = [&](auto waves, auto chunks) {
         constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
-        norm_forward_kernel<T, W, C><<<dim3(static_cast<uint32_t>(blocks_for(d, a.m))), dim3(W == 1 ? 256 : W * 64), 0, stream>>>(a);
-    });
+        const int64_t blocks = std::min<int64_t>(W == 1 ? ceil_div(a.m, 4) : a.m, kMaxBlocks);
+        const dim3 grid(static_cast<uint32_t>(blocks)), block(W == 1 ? 256 : W * 64);
+        if (a.n % (16 / sizeof(T)) == 0) norm_forward_kernel<T, W, C, false><<<grid, block, 0, stream>>>(a);
+        else norm_forward_kernel<T, W, C, true><<<grid, block, 0, stream>>>(a);
+    };
+    if (with<1, 1>(d, run) || with<1, 2>(d, run) || with<1, 4>(d, run) || with<1, 8>(d, run) || with<4, 4>(d, run) ||
+        with<16, 2>(d, run) || with<16, 4>(d, run))
+        return;
+    const uint32_t blocks = static_cast<uint32_t>(std::min<int64_t>(a.m, 2 * kCus));
+    norm_forward_long_kernel<T><<<dim3(blocks), dim3(kLongBlock), 0, stream>>>(a);
 }
 
 int32_t forward_impl(void* y, int64_t ldy, float* mean, float* rstd, const void* x, int64_t ldx, int32_t dtype,
@@ -512,9 +588,9 @@ template <typename T>
 int32_t launch_backward(BackwardArgs a, const Sums& out, float* workspace, int64_t bytes, hipStream_t stream,
                         const char* who) {
     const bool sums = out.dw || out.db;
-    const Division d = division_of(a.n, sizeof(T), true);
+    const Division d = backward_division(a.n, sizeof(T));
     const int64_t room = std::min(bytes, FSDP_NORM_WORKSPACE_BYTES) / (8 * a.n);  // rows of sums
-    int64_t blocks = blocks_for(d, a.m);
+    int64_t blocks = std::min<int64_t>(d.waves == 1 ? ceil_div(a.m, 4) : a.m, 2 * kCus);
     const int64_t each = d.waves == 1 ? 4 : 1;  // rows of sums that a block writes
     if (d.waves > 0 && (a.dx || sums)) {
         // with fewer parts than a quarter of the chip the sums are taken apart
@@ -524,10 +600,13 @@ int32_t launch_backward(BackwardArgs a, const Sums& out, float* workspace, int64
             a.part = workspace;
         }
         if (together || a.dx) {
-            with_division<false>(d, [&](auto waves, auto chunks) {
+            auto run = [&](auto waves, auto chunks) {
                 constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
-                norm_backward_kernel<T, W, C><<<dim3(static_cast<uint32_t>(blocks)), dim3(W == 1 ? 256 : W * 64), 0, stream>>>(a);
-            });
+                const dim3 grid(static_cast<uint32_t>(blocks)), block(W == 1 ? 256 : W * 64);
+                if (a.n % (16 / sizeof(T)) == 0) norm_backward_kernel<T, W, C, false><<<grid, block, 0, stream>>>(a);
+                else norm_backward_kernel<T, W, C, true><<<grid, block, 0, stream>>>(a);
+            };
+            with<1, 1>(d, run) || with<1, 2>(d, run) || with<4, 1>(d, run) || with<4, 2>(d, run) || with<4, 4>(d, run);
             TRY(launched(who));
         }
         if (together) {
