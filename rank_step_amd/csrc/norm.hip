@@ -65,69 +65,66 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*s)[WAVES]) {
     }
 }
 
-// N parameters from element j on in fp32, `none` where there is no vector.  Of a
-// row's last, shorter chunk (back > 0) the N that end with the row are read and
-// moved down, as stream_load does; of rows shorter than a chunk (back < 0) each.
+// N parameters from element j on in fp32, `none` where there is no vector.
 template <int N>
-__device__ __forceinline__ void load_params(const void* p, int f32, int64_t j, int cnt, int back, float none, float (&v)[N]) {
-#pragma unroll
-    for (int q = 0; q < N; ++q) v[q] = none;
-    if (!p || cnt <= 0) return;
-    if (back < 0) {
-#pragma unroll
-        for (int q = 0; q < N; ++q)
-            if (q < cnt) v[q] = f32 ? static_cast<const float*>(p)[j + q] : widen(static_cast<const uint16_t*>(p)[j + q]);
-        return;
-    }
+__device__ __forceinline__ void load_params(const void* p, int f32, int64_t j, float none, float (&v)[N]) {
     struct __attribute__((packed, aligned(4))) Floats { float v[N]; };
     struct __attribute__((packed, aligned(2))) Halves { uint16_t v[N]; };
-    if (f32) {
-        const Floats w = *reinterpret_cast<const Floats*>(static_cast<const float*>(p) + j - back);
+    if (!p) {
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = none;
+    } else if (f32) {
+        const Floats w = *reinterpret_cast<const Floats*>(static_cast<const float*>(p) + j);
 #pragma unroll
         for (int q = 0; q < N; ++q) v[q] = w.v[q];
     } else {
-        const Halves w = *reinterpret_cast<const Halves*>(static_cast<const uint16_t*>(p) + j - back);
+        const Halves w = *reinterpret_cast<const Halves*>(static_cast<const uint16_t*>(p) + j);
 #pragma unroll
         for (int q = 0; q < N; ++q) v[q] = widen(w.v[q]);
     }
-    if (back > 0) {
-#pragma unroll
-        for (int d = N / 2; d > 0; d /= 2)
-            if (back & d)
-#pragma unroll
-                for (int q = 0; q + d < N; ++q) v[q] = v[q + d];
-    }
+}
+__device__ __forceinline__ float load_param(const void* p, int f32, int64_t j, float none) {
+    float v[1];
+    load_params(p, f32, j, none, v);
+    return v[0];
 }
 
-// A thread's chunks of a row: chunk c starts at element (c * 64 WAVES + t) * E.
-// TAIL: the row's last chunk may be shorter.
+// A thread's part of a row: of the whole chunks of 16 bytes, chunk c from element
+// (c * 64 WAVES + t) * E on; and with TAIL one of the fewer than E elements
+// behind them, or none.  (A last chunk read as the E elements that end with the
+// row, and moved, cost twice the registers for all chunks.)
 template <typename T, int WAVES, int C, bool TAIL>
 struct Row {
     static constexpr int kEach = 16 / sizeof(T);
-    int first;  // of the thread's first chunk
-    int n;
+    int first;  // element of the thread's first chunk
+    int whole;  // elements in whole chunks
+    int last;   // the element behind them, or -1
 
-    __device__ __forceinline__ void init(int t, int64_t len) {
+    __device__ __forceinline__ void init(int t, int64_t n) {
         first = t * kEach;
-        n = static_cast<int>(len);
+        whole = static_cast<int>(n) / kEach * kEach;
+        last = TAIL && whole + t < n ? whole + t : -1;
     }
     __device__ __forceinline__ int at(int c) const { return first + c * (64 * WAVES * kEach); }
-    __device__ __forceinline__ bool has(int c) const { return at(c) < n; }
-    // elements of a chunk that the row has
-    __device__ __forceinline__ int cnt(int c) const { return TAIL ? min(n - at(c), kEach) : kEach; }
-    __device__ __forceinline__ int back(int c) const { return TAIL ? chunk_back<T>(cnt(c), n) : 0; }
-    __device__ __forceinline__ void load(const T* row, u32x4 (&w)[C]) const {
+    __device__ __forceinline__ bool has(int c) const { return at(c) < whole; }
+    __device__ __forceinline__ bool tail() const { return TAIL && last >= 0; }
+    __device__ __forceinline__ void load(const T* row, u32x4 (&w)[C], float& end) const {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             w[c] = u32x4{0, 0, 0, 0};
-            if (has(c)) w[c] = stream_load(row + at(c), cnt(c), back(c));
+            if (has(c)) w[c] = stream_load(row + at(c), kEach, 0);
         }
+        end = 0.0f;
+        if (tail()) end = element(row);
     }
-    // Chunk c's values, zeros behind the row's end.
-    __device__ __forceinline__ void values(const u32x4 (&w)[C], int c, float (&v)[kEach]) const {
-        arrange(w[c], TAIL && has(c) ? back(c) : 0, v);
+    __device__ __forceinline__ float element(const T* row) const {
+        if constexpr (sizeof(T) == 2) return widen(row[last]);
+        else return row[last];
     }
-    __device__ __forceinline__ bool inside(int c, int q) const { return TAIL ? at(c) + q < n : has(c); }
+    __device__ __forceinline__ void store_element(T* row, float v) const {
+        if constexpr (sizeof(T) == 2) row[last] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+        else row[last] = v;
+    }
 };
 
 // Packed chunks whose widened values are not kept from here on: the compiler
@@ -153,9 +150,10 @@ struct ForwardArgs {
 };
 
 // A row by WAVES waves of C chunks of 16 bytes a lane, which stay packed in
-// registers and are widened for each pass over them.  Bound by memory: 8192 x
-// 4096 bf16 with one wave a row, whose 8 KB need no barrier, XXX us; by four waves
-// 42, as a workgroup then has little on its way while it waits for its sums.
+// registers and are widened for each pass over them.  Bound by memory, a
+// workgroup a row (four where a wave takes one), so that some rows load while
+// others store: 8192 x 4096 bf16 26.8 us (5.0 TB/s; a copy's 20.7).  With rows held
+// widened and workgroups that stay for several 42, one wave a row 30, eight 32.
 template <typename T, int WAVES, int C, bool TAIL>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_kernel(ForwardArgs a) {
     constexpr int kEach = 16 / sizeof(T), kRows = WAVES == 1 ? 4 : 1;
@@ -167,14 +165,15 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_ke
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / (64 * WAVES); i < a.m;
          i += static_cast<int64_t>(gridDim.x) * kRows) {
         u32x4 raw[C];
-        row.load(static_cast<const T*>(a.x) + i * a.ldx, raw);
+        float end;
+        row.load(static_cast<const T*>(a.x) + i * a.ldx, raw, end);
         float mean = 0.0f;
         if (!a.rms) {
-            float sum[1] = {0.0f};
+            float sum[1] = {end};
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 float v[kEach];
-                row.values(raw, c, v);
+                arrange(raw[c], 0, v);
 #pragma unroll
                 for (int q = 0; q < kEach; ++q) sum[0] += v[q];
             }
@@ -184,13 +183,17 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_ke
         }
         // About that mean, whose own rounding and sum the first moment corrects.
         float sum[2] = {0.0f, 0.0f};
+        if (row.tail()) {
+            sum[0] = end - mean;
+            sum[1] = sum[0] * sum[0];
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float v[kEach];
-            row.values(raw, c, v);
+            arrange(raw[c], 0, v);
 #pragma unroll
             for (int q = 0; q < kEach; ++q) {
-                const float d = row.inside(c, q) ? v[q] - mean : 0.0f;
+                const float d = row.has(c) ? v[q] - mean : 0.0f;
                 sum[0] += d;
                 sum[1] = fmaf(d, d, sum[1]);
             }
@@ -209,17 +212,21 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_ke
             if (a.rstd) a.rstd[i] = rstd;
         }
         widen_again(raw);
+        T* const y = static_cast<T*>(a.y) + i * a.ldy;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if (!row.has(c)) continue;
             float v[kEach], w[kEach], b[kEach];
-            load_params(a.w, a.w_f32, row.at(c), row.cnt(c), row.back(c), 1.0f, w);
-            load_params(a.b, a.w_f32, row.at(c), row.cnt(c), row.back(c), 0.0f, b);
-            row.values(raw, c, v);
+            load_params(a.w, a.w_f32, row.at(c), 1.0f, w);
+            load_params(a.b, a.w_f32, row.at(c), 0.0f, b);
+            arrange(raw[c], 0, v);
 #pragma unroll
             for (int q = 0; q < kEach; ++q) v[q] = fmaf((v[q] - mean) * rstd, w[q], b[q]);
-            stream_store(static_cast<T*>(a.y) + i * a.ldy + row.at(c), row.cnt(c), a.wt, v);
+            stream_store(y + row.at(c), kEach, a.wt, v);
         }
+        if (row.tail())
+            row.store_element(y, fmaf((end - mean) * rstd, load_param(a.w, a.w_f32, row.last, 1.0f),
+                                      load_param(a.b, a.w_f32, row.last, 0.0f)));
         // s0's and s1's next writes come behind a barrier of the other; alone, behind this one.
         if (WAVES > 1 && a.rms) __syncthreads();
     }
@@ -265,10 +272,7 @@ __global__ __launch_bounds__(kLongBlock) void norm_forward_long_kernel(ForwardAr
             if (a.rstd) a.rstd[i] = rstd;
         }
         for (int64_t j = threadIdx.x; j < a.n; j += kLongBlock) {
-            float w[1], b[1];
-            load_params(a.w, a.w_f32, j, 1, 0, 1.0f, w);
-            load_params(a.b, a.w_f32, j, 1, 0, 0.0f, b);
-            const float v = fmaf((value(j) - mean) * rstd, w[0], b[0]);
+            const float v = fmaf((value(j) - mean) * rstd, load_param(a.w, a.w_f32, j, 1.0f), load_param(a.b, a.w_f32, j, 0.0f));
             if constexpr (sizeof(T) == 2) y[j] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
             else y[j] = v;
         }
@@ -286,39 +290,118 @@ struct BackwardArgs {
     const void* w;
     const float* mean;
     const float* rstd;
-    float* part;  // [rows of sums][2][n], or null: no column sums
+    float* part;  // [rows of sums][2][n]; norm_columns_kernel: null with one row of them
     int64_t lddx, lddy, ldx, ldr, m, n;
     int32_t w_f32, rms, wt;
 };
 
+// dx of row i by WAVES waves, which read it once.
+template <typename T, int WAVES, int C, bool TAIL>
+__device__ __forceinline__ void dx_row(const BackwardArgs& a, int64_t i, int t, float (*s)[WAVES]) {
+    constexpr int kEach = 16 / sizeof(T);
+    Row<T, WAVES, C, TAIL> row;
+    row.init(t, a.n);
+    u32x4 rx[C], rdy[C];
+    float ex, edy;
+    row.load(static_cast<const T*>(a.dy) + i * a.lddy, rdy, edy);
+    row.load(static_cast<const T*>(a.x) + i * a.ldx, rx, ex);
+    const float mean = a.rms ? 0.0f : a.mean[i], rstd = a.rstd[i], n = static_cast<float>(a.n);
+    float sum[2] = {0.0f, 0.0f};
+    if (row.tail()) {
+        sum[0] = edy *= load_param(a.w, a.w_f32, row.last, 1.0f);
+        sum[1] = edy * (ex = (ex - mean) * rstd);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (!row.has(c)) continue;
+        float x[kEach], g[kEach], w[kEach];
+        load_params(a.w, a.w_f32, row.at(c), 1.0f, w);
+        arrange(rx[c], 0, x);
+        arrange(rdy[c], 0, g);
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const float gw = g[q] * w[q];
+            sum[0] += gw;
+            sum[1] = fmaf(gw, (x[q] - mean) * rstd, sum[1]);
+        }
+    }
+    row_sum<WAVES>(sum, s);
+    const float m1 = a.rms ? 0.0f : sum[0] / n, m2 = sum[1] / n;
+    widen_again(rx);
+    widen_again(rdy);
+    const T* const res = static_cast<const T*>(a.res) + (a.res ? i * a.ldr : 0);
+    T* const dx = static_cast<T*>(a.dx) + i * a.lddx;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (!row.has(c)) continue;
+        float x[kEach], g[kEach], w[kEach], r[kEach];
+        if (a.res) arrange(stream_load(res + row.at(c), kEach, 0), 0, r);
+        load_params(a.w, a.w_f32, row.at(c), 1.0f, w);
+        arrange(rx[c], 0, x);
+        arrange(rdy[c], 0, g);
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const float xhat = (x[q] - mean) * rstd, v = rstd * (g[q] * w[q] - m1 - xhat * m2);
+            g[q] = a.res ? v + r[q] : v;
+        }
+        stream_store(dx + row.at(c), kEach, a.wt, g);
+    }
+    if (row.tail()) {
+        const float v = rstd * (edy - m1 - ex * m2);
+        row.store_element(dx, a.res ? v + row.element(res) : v);
+    }
+}
+
+// dx alone: without column sums, or beside norm_columns_kernel for rows whose
+// sums registers do not hold.
+template <typename T, int WAVES, int C, bool TAIL>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_dx_kernel(BackwardArgs a) {
+    constexpr int kRows = WAVES == 1 ? 4 : 1;
+    __shared__ float s[2][2][WAVES];
+    int turn = 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / (64 * WAVES); i < a.m;
+         i += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1)
+        dx_row<T, WAVES, C, TAIL>(a, i, threadIdx.x % (64 * WAVES), s[turn]);
+}
+
+// Rows of a workgroup of the backward pass at a time.
+constexpr int backward_rows(int waves) { return waves == 1 ? 8 : 1; }
+
 // dx, and the column sums of the rows that a thread passes, which it holds for
 // the columns of its chunks.  Rows stay packed in registers, and the next one is
-// on its way while one is summed.
+// on its way while one is summed (two ahead: 20 % slower).  Bound by memory: 8192
+// x 4096 bf16 with a residual and both sums 58 us, of which 5 for joining the
+// workgroups' sums (floor 41).  A workgroup leaves one row of sums, and two a CU
+// stay for all rows: three a CU 69 us, four 73, for more sums to write and read;
+// one 69, for fewer loads on their way.
 template <typename T, int WAVES, int C, bool TAIL>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_backward_kernel(BackwardArgs a) {
-    constexpr int kEach = 16 / sizeof(T), kRows = WAVES == 1 ? 4 : 1;
+__global__ __launch_bounds__(backward_rows(WAVES) * WAVES * 64) void norm_backward_kernel(BackwardArgs a) {
+    constexpr int kEach = 16 / sizeof(T), kRows = backward_rows(WAVES);
     __shared__ float s[2][2][WAVES];
+    __shared__ float joined[kRows > 1 ? 2 : 1][kRows > 1 ? C * kEach + TAIL : 1][64];
     const int t = threadIdx.x % (64 * WAVES);
     Row<T, WAVES, C, TAIL> row;
     row.init(t, a.n);
     float w[C][kEach], dw[C][kEach], db[C][kEach];
+    float ew = 0.0f, edw = 0.0f, edb = 0.0f;  // the tail's
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        load_params(a.w, a.w_f32, row.at(c), row.has(c) ? row.cnt(c) : 0, row.back(c), 1.0f, w[c]);
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) dw[c][q] = db[c][q] = 0.0f;
+        for (int q = 0; q < kEach; ++q) w[c][q] = dw[c][q] = db[c][q] = 0.0f;
+        if (row.has(c)) load_params(a.w, a.w_f32, row.at(c), 1.0f, w[c]);
     }
+    if (row.tail()) ew = load_param(a.w, a.w_f32, row.last, 1.0f);
     const float n = static_cast<float>(a.n);
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / (64 * WAVES);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
     struct Rows {
         u32x4 x[C], dy[C], res[C];
-        float mean, rstd;
+        float ex, edy, eres, mean, rstd;
     };
     auto load = [&](int64_t i, Rows& r) {
-        row.load(static_cast<const T*>(a.dy) + i * a.lddy, r.dy);
-        row.load(static_cast<const T*>(a.x) + i * a.ldx, r.x);
-        if (a.res) row.load(static_cast<const T*>(a.res) + i * a.ldr, r.res);
+        row.load(static_cast<const T*>(a.dy) + i * a.lddy, r.dy, r.edy);
+        row.load(static_cast<const T*>(a.x) + i * a.ldx, r.x, r.ex);
+        if (a.res) row.load(static_cast<const T*>(a.res) + i * a.ldr, r.res, r.eres);
         r.mean = a.rms ? 0.0f : a.mean[i];
         r.rstd = a.rstd[i];
     };
@@ -330,14 +413,21 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_backward_k
         const bool more = i + step < a.m;
         if (more) load(i + step, next);
         float sum[2] = {0.0f, 0.0f};
+        if (row.tail()) {
+            r.ex = (r.ex - r.mean) * r.rstd;
+            edw = fmaf(r.edy, r.ex, edw);
+            edb += r.edy;
+            sum[0] = r.edy *= ew;
+            sum[1] = r.edy * r.ex;
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float x[kEach], g[kEach];
-            row.values(r.x, c, x);
-            row.values(r.dy, c, g);
+            arrange(r.x[c], 0, x);
+            arrange(r.dy[c], 0, g);
 #pragma unroll
             for (int q = 0; q < kEach; ++q) {
-                const float xhat = row.inside(c, q) ? (x[q] - r.mean) * r.rstd : 0.0f;
+                const float xhat = row.has(c) ? (x[q] - r.mean) * r.rstd : 0.0f;
                 dw[c][q] = fmaf(g[q], xhat, dw[c][q]);
                 db[c][q] += g[q];
                 const float gw = g[q] * w[c][q];
@@ -345,38 +435,63 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_backward_k
                 sum[1] = fmaf(gw, xhat, sum[1]);
             }
         }
-        if (a.dx) {
-            row_sum<WAVES>(sum, s[turn]);
-            const float m1 = a.rms ? 0.0f : sum[0] / n, m2 = sum[1] / n;
-            widen_again(r.x);
-            widen_again(r.dy);
+        row_sum<WAVES>(sum, s[turn]);
+        const float m1 = a.rms ? 0.0f : sum[0] / n, m2 = sum[1] / n;
+        widen_again(r.x);
+        widen_again(r.dy);
+        T* const dx = static_cast<T*>(a.dx) + i * a.lddx;
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                if (!row.has(c)) continue;
-                float x[kEach], g[kEach], res[kEach];
-                row.values(r.x, c, x);
-                row.values(r.dy, c, g);
-                if (a.res) row.values(r.res, c, res);
+        for (int c = 0; c < C; ++c) {
+            if (!row.has(c)) continue;
+            float x[kEach], g[kEach], res[kEach];
+            arrange(r.x[c], 0, x);
+            arrange(r.dy[c], 0, g);
+            if (a.res) arrange(r.res[c], 0, res);
 #pragma unroll
-                for (int q = 0; q < kEach; ++q) {
-                    const float xhat = (x[q] - r.mean) * r.rstd, v = r.rstd * (g[q] * w[c][q] - m1 - xhat * m2);
-                    g[q] = a.res ? v + res[q] : v;
-                }
-                stream_store(static_cast<T*>(a.dx) + i * a.lddx + row.at(c), row.cnt(c), a.wt, g);
+            for (int q = 0; q < kEach; ++q) {
+                const float xhat = (x[q] - r.mean) * r.rstd, v = r.rstd * (g[q] * w[c][q] - m1 - xhat * m2);
+                g[q] = a.res ? v + res[q] : v;
             }
+            stream_store(dx + row.at(c), kEach, a.wt, g);
+        }
+        if (row.tail()) {
+            const float v = r.rstd * (r.edy - m1 - r.ex * m2);
+            row.store_element(dx, a.res ? v + r.eres : v);
         }
         if (more) r = next;
     }
-    if (!a.part) return;
-    float* p = a.part + first * 2 * a.n;
+    if constexpr (kRows > 1) {
+        // the waves' sums one after the other, into the last one's registers
+        const int wave = threadIdx.x >> 6;
+        for (int turn = 0; turn < kRows; ++turn) {
+            if (wave == turn) {
+                auto join = [&](int at, float& x, float& y) {
+                    x = joined[0][at][t] = turn ? joined[0][at][t] + x : x;
+                    y = joined[1][at][t] = turn ? joined[1][at][t] + y : y;
+                };
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int q = 0; q < kEach; ++q) join(c * kEach + q, dw[c][q], db[c][q]);
+                if (TAIL) join(C * kEach, edw, edb);
+            }
+            __syncthreads();
+        }
+        if (wave != kRows - 1) return;
+    }
+    float* p = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.n;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int q = 0; q < kEach; ++q)
-            if (row.inside(c, q)) {
+            if (row.has(c)) {
                 p[row.at(c) + q] = dw[c][q];
                 p[a.n + row.at(c) + q] = db[c][q];
             }
+    if (row.tail()) {
+        p[row.last] = edw;
+        p[a.n + row.last] = edb;
+    }
 }
 
 // dx of a row that registers do not hold.
@@ -392,10 +507,8 @@ __global__ __launch_bounds__(kLongBlock) void norm_backward_long_kernel(Backward
             else return static_cast<const T*>(p)[at];
         };
         auto terms = [&](int64_t j, float& xhat) {
-            float w[1];
-            load_params(a.w, a.w_f32, j, 1, 0, 1.0f, w);
             xhat = (value(a.x, i * a.ldx + j) - mean) * rstd;
-            return value(a.dy, i * a.lddy + j) * w[0];
+            return value(a.dy, i * a.lddy + j) * load_param(a.w, a.w_f32, j, 1.0f);
         };
         float sum[2] = {0.0f, 0.0f}, xhat;
         for (int64_t j = threadIdx.x; j < a.n; j += kLongBlock) {
@@ -467,23 +580,73 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(BackwardArgs a, Sums 
     }
 }
 
-// dw and db from `rows` rows of sums: 64 columns a block, 16 threads a column,
+// Few rows, everything in one launch: the first workgroups take 8 chunks of
+// columns each over all rows, 32 at a time, for the column sums; each of the
+// others one row, for dx.  Both read dy and x, which are small.
+constexpr int kFewChunks = 4;  // a lane
+template <typename T>
+__global__ __launch_bounds__(256) void norm_backward_few_kernel(BackwardArgs a, Sums out, int32_t cblocks) {
+    constexpr int kEach = 16 / sizeof(T);
+    __shared__ float sums[2][32][8 * kEach + 1], row_sums[2][4];
+    const int tid = threadIdx.x;
+    if (static_cast<int>(blockIdx.x) < cblocks) {
+        const int lane = tid & 7, place = tid >> 3;
+        const int64_t j0 = static_cast<int64_t>(blockIdx.x) * (8 * kEach), j = j0 + lane * kEach;
+        const int cnt = static_cast<int>(max(static_cast<int64_t>(0), min(a.n - j, static_cast<int64_t>(kEach))));
+        const int back = chunk_back<T>(cnt, a.n);
+        float dw[kEach], db[kEach];
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) dw[q] = db[q] = 0.0f;
+        const int64_t end = cnt > 0 ? a.m : 0;
+#pragma unroll 4
+        for (int64_t i = place; i < end; i += 32) {
+            float x[kEach], g[kEach];
+            const u32x4 wx = stream_load(static_cast<const T*>(a.x) + i * a.ldx + j, cnt, back);
+            const u32x4 wg = stream_load(static_cast<const T*>(a.dy) + i * a.lddy + j, cnt, back);
+            const float mean = a.rms ? 0.0f : a.mean[i], rstd = a.rstd[i];
+            arrange(wx, back, x);
+            arrange(wg, back, g);
+#pragma unroll
+            for (int q = 0; q < kEach; ++q) {
+                dw[q] = fmaf(g[q], (x[q] - mean) * rstd, dw[q]);
+                db[q] += g[q];
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            sums[0][place][lane * kEach + q] = dw[q];
+            sums[1][place][lane * kEach + q] = db[q];
+        }
+        __syncthreads();
+        const int which = tid / (8 * kEach), at = tid % (8 * kEach);
+        void* const to = which == 0 ? out.dw : which == 1 ? out.db : nullptr;
+        if (!to || j0 + at >= a.n) return;
+        float v = sums[which][0][at];
+#pragma unroll
+        for (int p = 1; p < 32; ++p) v += sums[which][p][at];
+        put_sum(to, out.f32, out.accumulate, j0 + at, v);
+        return;
+    }
+    dx_row<T, 4, kFewChunks, true>(a, static_cast<int64_t>(blockIdx.x) - cblocks, tid, row_sums);
+}
+
+// dw and db from `rows` rows of sums: 32 columns a block, 32 threads a column,
 // their sums added in order.
-constexpr int kSumBlock = 1024;
+constexpr int kSumBlock = 1024, kSumColumns = 32;
 __global__ __launch_bounds__(kSumBlock) void norm_sum_kernel(const float* part, int64_t n, int64_t rows, Sums out) {
-    __shared__ float sums[16][64];
-    const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + c;
+    __shared__ float sums[kSumBlock / kSumColumns][kSumColumns + 1];
+    const int c = threadIdx.x % kSumColumns, q = threadIdx.x / kSumColumns;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * kSumColumns + c;
     float s = 0;
     if (col < 2 * n) {
 #pragma unroll 8
-        for (int64_t r = q; r < rows; r += 16) s += part[r * 2 * n + col];
+        for (int64_t r = q; r < rows; r += kSumBlock / kSumColumns) s += part[r * 2 * n + col];
     }
     sums[q][c] = s;
     __syncthreads();
     if (q != 0 || col >= 2 * n) return;
 #pragma unroll
-    for (int r = 1; r < 16; ++r) s += sums[r][c];
+    for (int r = 1; r < kSumBlock / kSumColumns; ++r) s += sums[r][c];
     void* const to = col < n ? out.dw : out.db;
     if (to) put_sum(to, out.f32, out.accumulate, col < n ? col : col - n, s);
 }
@@ -502,18 +665,21 @@ struct Division {
     int waves, chunks;
 };
 
-// By its length alone, so that a row's result is the same among any others.
-Division forward_division(int64_t n, int elem) {
+// A row by itself: by its length alone, so that its result is the same among any
+// other rows.  fp32 rows of 11007 (8192 of them) 175 us by 16 waves of 4 chunks, by
+// 8 of 8 194; bf16 rows of 2048 by one wave 14.4, by four 14.9.
+Division row_division(int64_t n, int elem) {
     const int64_t chunks = ceil_div(n, 16 / elem);
-    for (const Division d : {Division{1, 1}, {1, 2}, {1, 4}, {1, 8}, {4, 4}, {16, 2}, {16, 4}})
+    for (const Division d : {Division{1, 1}, {1, 2}, {1, 4}, {4, 2}, {4, 4}, {8, 4}, {16, 4}})
         if (chunks <= int64_t(64) * d.waves * d.chunks) return d;
     return {0, 0};
 }
 
-// The backward pass holds the column sums and two rows as well.
-Division backward_division(int64_t n, int elem) {
+// With column sums, which are held as well, and the next row.  8192 x 8192 bf16
+// with a residual: 110 us by 16 waves of one chunk, by 4 of 4 151.
+Division sums_division(int64_t n, int elem) {
     const int64_t chunks = ceil_div(n, 16 / elem);
-    for (const Division d : {Division{1, 1}, {1, 2}, {4, 1}, {4, 2}, {4, 4}})
+    for (const Division d : {Division{1, 1}, {1, 2}, {4, 1}, {8, 1}, {16, 1}})
         if (chunks <= int64_t(64) * d.waves * d.chunks) return d;
     return {0, 0};
 }
@@ -528,7 +694,7 @@ bool with(const Division& d, F&& f) {
 
 template <typename T>
 void launch_forward(const ForwardArgs& a, hipStream_t stream) {
-    const Division d = forward_division(a.n, sizeof(T));
+    const Division d = row_division(a.n, sizeof(T));
     auto run = [&](auto waves, auto chunks) {
         constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
         const int64_t blocks = std::min<int64_t>(W == 1 ? ceil_div(a.m, 4) : a.m, kMaxBlocks);
@@ -536,8 +702,8 @@ void launch_forward(const ForwardArgs& a, hipStream_t stream) {
         if (a.n % (16 / sizeof(T)) == 0) norm_forward_kernel<T, W, C, false><<<grid, block, 0, stream>>>(a);
         else norm_forward_kernel<T, W, C, true><<<grid, block, 0, stream>>>(a);
     };
-    if (with<1, 1>(d, run) || with<1, 2>(d, run) || with<1, 4>(d, run) || with<1, 8>(d, run) || with<4, 4>(d, run) ||
-        with<16, 2>(d, run) || with<16, 4>(d, run))
+    if (with<1, 1>(d, run) || with<1, 2>(d, run) || with<1, 4>(d, run) || with<4, 2>(d, run) || with<4, 4>(d, run) ||
+        with<8, 4>(d, run) || with<16, 4>(d, run))
         return;
     const uint32_t blocks = static_cast<uint32_t>(std::min<int64_t>(a.m, 2 * kCus));
     norm_forward_long_kernel<T><<<dim3(blocks), dim3(kLongBlock), 0, stream>>>(a);
@@ -584,53 +750,68 @@ int32_t forward_impl(void* y, int64_t ldy, float* mean, float* rstd, const void*
     return launched(who);
 }
 
+// Rows up to which the column sums are taken beside dx in one launch.  333 x 1365
+// fp32: 10.1 us, by two launches 11.4; 512 x 4096 bf16 15 and 21; 600 x 4096 17.5
+// and 21.8.
+constexpr int64_t kFewRows = 1024;
+
 template <typename T>
 int32_t launch_backward(BackwardArgs a, const Sums& out, float* workspace, int64_t bytes, hipStream_t stream,
                         const char* who) {
-    const bool sums = out.dw || out.db;
-    const Division d = backward_division(a.n, sizeof(T));
+    constexpr int64_t kEach = 16 / sizeof(T);
+    const bool sums = out.dw || out.db, whole = a.n % kEach == 0;
+    if (sums && a.m <= kFewRows && a.n <= 256 * kFewChunks * kEach) {
+        const int64_t cblocks = ceil_div(a.n, 8 * kEach);
+        norm_backward_few_kernel<T><<<dim3(static_cast<uint32_t>(cblocks + (a.dx ? a.m : 0))), dim3(256), 0, stream>>>(
+            a, out, static_cast<int32_t>(cblocks));
+        return launched(who);
+    }
     const int64_t room = std::min(bytes, FSDP_NORM_WORKSPACE_BYTES) / (8 * a.n);  // rows of sums
-    int64_t blocks = std::min<int64_t>(d.waves == 1 ? ceil_div(a.m, 4) : a.m, 2 * kCus);
-    const int64_t each = d.waves == 1 ? 4 : 1;  // rows of sums that a block writes
-    if (d.waves > 0 && (a.dx || sums)) {
-        // with fewer parts than a quarter of the chip the sums are taken apart
-        const bool together = sums && room >= std::min<int64_t>(a.m, each * kCus / 4);
-        if (together) {
-            blocks = std::min(blocks, room / each);
-            a.part = workspace;
+    auto join = [&](int64_t rows) {
+        norm_sum_kernel<<<dim3(static_cast<uint32_t>(ceil_div(2 * a.n, kSumColumns))), dim3(kSumBlock), 0, stream>>>(
+            workspace, a.n, rows, out);
+        return launched(who);
+    };
+    const Division d = sums_division(a.n, sizeof(T));
+    // with room for fewer parts than a quarter of the chip the sums are taken apart
+    if (sums && a.dx && d.waves > 0 && room >= kCus / 4) {
+        const int64_t blocks = std::min(std::min<int64_t>(ceil_div(a.m, backward_rows(d.waves)), (d.waves <= 8 ? 2 : 1) * kCus), room);
+        a.part = workspace;
+        auto run = [&](auto waves, auto chunks) {
+            constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
+            const dim3 grid(static_cast<uint32_t>(blocks)), block(backward_rows(W) * W * 64);
+            if (whole) norm_backward_kernel<T, W, C, false><<<grid, block, 0, stream>>>(a);
+            else norm_backward_kernel<T, W, C, true><<<grid, block, 0, stream>>>(a);
+        };
+        with<1, 1>(d, run) || with<1, 2>(d, run) || with<4, 1>(d, run) || with<8, 1>(d, run) || with<16, 1>(d, run);
+        TRY(launched(who));
+        return join(blocks);
+    }
+    if (a.dx) {
+        const Division r = row_division(a.n, sizeof(T));
+        auto run = [&](auto waves, auto chunks) {
+            constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
+            const int64_t blocks = std::min<int64_t>(W == 1 ? ceil_div(a.m, 4) : a.m, kMaxBlocks);
+            const dim3 grid(static_cast<uint32_t>(blocks)), block(W == 1 ? 256 : W * 64);
+            if (whole) norm_dx_kernel<T, W, C, false><<<grid, block, 0, stream>>>(a);
+            else norm_dx_kernel<T, W, C, true><<<grid, block, 0, stream>>>(a);
+        };
+        if (!(with<1, 1>(r, run) || with<1, 2>(r, run) || with<1, 4>(r, run) || with<4, 2>(r, run) || with<4, 4>(r, run) ||
+              with<8, 4>(r, run) || with<16, 4>(r, run))) {
+            const uint32_t blocks = static_cast<uint32_t>(std::min<int64_t>(a.m, 2 * kCus));
+            norm_backward_long_kernel<T><<<dim3(blocks), dim3(kLongBlock), 0, stream>>>(a);
         }
-        if (together || a.dx) {
-            auto run = [&](auto waves, auto chunks) {
-                constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
-                const dim3 grid(static_cast<uint32_t>(blocks)), block(W == 1 ? 256 : W * 64);
-                if (a.n % (16 / sizeof(T)) == 0) norm_backward_kernel<T, W, C, false><<<grid, block, 0, stream>>>(a);
-                else norm_backward_kernel<T, W, C, true><<<grid, block, 0, stream>>>(a);
-            };
-            with<1, 1>(d, run) || with<1, 2>(d, run) || with<4, 1>(d, run) || with<4, 2>(d, run) || with<4, 4>(d, run);
-            TRY(launched(who));
-        }
-        if (together) {
-            norm_sum_kernel<<<dim3(static_cast<uint32_t>(ceil_div(2 * a.n, 64))), dim3(kSumBlock), 0, stream>>>(
-                workspace, a.n, blocks * each, out);
-            return launched(who);
-        }
-    } else if (a.dx) {
-        const uint32_t long_blocks = static_cast<uint32_t>(std::min<int64_t>(a.m, 2 * kCus));
-        norm_backward_long_kernel<T><<<dim3(long_blocks), dim3(kLongBlock), 0, stream>>>(a);
         TRY(launched(who));
     }
     if (!sums) return FSDP_OK;
-    const int64_t cblocks = ceil_div(a.n, 64 * (16 / static_cast<int64_t>(sizeof(T))));
+    const int64_t cblocks = ceil_div(a.n, 64 * kEach);
     const int64_t want = std::max<int64_t>(1, std::min(8 * kCus / cblocks, room));
     const int64_t rows = ceil_div(ceil_div(a.m, 4), want) * 4, rblocks = ceil_div(a.m, rows);
     a.part = rblocks > 1 ? workspace : nullptr;
     norm_columns_kernel<T><<<dim3(static_cast<uint32_t>(cblocks * rblocks)), dim3(256), 0, stream>>>(
         a, out, static_cast<int32_t>(cblocks), rows);
     TRY(launched(who));
-    if (rblocks == 1) return FSDP_OK;
-    norm_sum_kernel<<<dim3(static_cast<uint32_t>(ceil_div(2 * a.n, 64))), dim3(kSumBlock), 0, stream>>>(workspace, a.n,
-                                                                                                       rblocks, out);
-    return launched(who);
+    return rblocks == 1 ? FSDP_OK : join(rblocks);
 }
 
 // dw and db of no rows.

@@ -388,6 +388,13 @@ def test_offsets_past_32_bits(gpu, space):
     dx = torch.empty_like(x)
     B.fsdp_norm_backward(dx, y, x, m, n, mean=mean, rstd=rstd, db=db, workspace=space)
     assert bool((db == m).all())
+    # the last rows' dx, which rounding alone makes other than 0: few rows may be summed in another order
     dsmall = torch.empty_like(tail)
     B.fsdp_norm_backward(dsmall, torch.ones_like(tail), tail, 64, n, mean=sm, rstd=sr)
-    assert torch.equal(dx[-64:], dsmall)
+    tv, mv, rv = (t.double().cpu().numpy() for t in (tail, sm, sr))
+    want = ON.backward(np.ones_like(tv), tv, mv, rv)[0]
+    xhat = np.abs(tv - mv[:, None]) * rv[:, None]
+    m2 = xhat.mean(axis=1, keepdims=True)
+    e = rv[:, None] * ((64 + n / 1024 + 8) * U * (1 + xhat * m2) + 6 * U * (2 + xhat * m2))
+    close(dx[-64:].double().cpu().numpy(), want, e, "bf16", "dx")
+    close(dsmall.double().cpu().numpy(), want, e, "bf16", "dx of few rows")
