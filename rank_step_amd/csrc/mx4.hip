@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fsdp_mx4.h"
 #include "internal.h"
@@ -79,37 +80,173 @@ __global__ __launch_bounds__(kElemBlock) void quantize_rows_kernel(RowsArgs a) {
     }
 }
 
-// ---------------------------------------------------------------- blocks along columns
+// ---------------------------------------------------------------- blocks along columns, and both
 
-// One column's 32 rows a thread.
+// Eight waves take 256 rows of 128 columns, each wave 32 rows, a lane two
+// columns of them: 32 loads on their way, 256 bytes of a row (bf16) each.  A
+// column's block is a lane's own; a row's block is 16 lanes', whose largest
+// magnitude four DPP steps find.  So x is read once for both copies, without LDS.
+// A column's codes go out as 16 bytes a lane, which the eight waves' neighbouring
+// blocks complete to a line in L2; a row's as words, after the four lanes of a quad
+// have exchanged bytes of four rows.
+struct TileArgs {
+    uint8_t* codes;    // blocks along rows, or null
+    uint8_t* scales;
+    uint8_t* codes_t;  // along columns
+    uint8_t* scales_t;
+    const void* x;
+    int64_t ldc, lds, ldct, ldst, ldx, rows, cols;
+    int64_t ctiles, tiles;
+};
+
+// Two columns of a row: their bits, and their codes as byte WHICH of w.
 template <typename T>
-__global__ __launch_bounds__(kElemBlock) void quantize_columns_kernel(RowsArgs a, int64_t cblocks) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t blocks = (a.rows + 31) / 32, padded = (blocks + 15) / 16 * 16;
-    const int64_t j = static_cast<int64_t>(blockIdx.x % cblocks) * 64 + lane;
-    const int64_t block = static_cast<int64_t>(blockIdx.x / cblocks) * 4 + wave;
-    if (j >= a.cols || block >= padded) return;
-    if (block >= blocks) {
-        a.scales[j * a.lds + block] = 0;
-        return;
+struct Two;
+template <>
+struct Two<uint16_t> {
+    uint32_t v;  // bf16 in each half
+    __device__ __forceinline__ void load(const uint16_t* p, int cnt) {
+        typedef uint32_t word __attribute__((aligned(2)));
+        v = cnt >= 2 ? __builtin_nontemporal_load(reinterpret_cast<const word*>(p)) : static_cast<uint32_t>(*p);
     }
-    float v[4][8];
-    uint32_t top = 0;
+    __device__ __forceinline__ uint32_t low() const { return v << 16; }
+    __device__ __forceinline__ uint32_t high() const { return v & 0xffff0000u; }
+    template <int WHICH>
+    __device__ __forceinline__ uint32_t encode(uint32_t w, float s) const {
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, v), s, WHICH);
+    }
+    // column c of this row and the next one
+    template <int WHICH>
+    __device__ __forceinline__ uint32_t encode_down(const Two& next, int c, uint32_t w, float s) const {
+        const uint32_t p = c ? __builtin_amdgcn_perm(next.v, v, 0x07060302) : __builtin_amdgcn_perm(next.v, v, 0x05040100);
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, p), s, WHICH);
+    }
+};
+template <>
+struct Two<float> {
+    float v[2];
+    __device__ __forceinline__ void load(const float* p, int cnt) {
+        typedef u32x2 pair __attribute__((aligned(4)));
+        const u32x2 w = cnt >= 2 ? __builtin_nontemporal_load(reinterpret_cast<const pair*>(p)) : u32x2{__float_as_uint(*p), 0};
+        v[0] = __uint_as_float(w[0]);
+        v[1] = __uint_as_float(w[1]);
+    }
+    __device__ __forceinline__ uint32_t low() const { return __float_as_uint(v[0]); }
+    __device__ __forceinline__ uint32_t high() const { return __float_as_uint(v[1]); }
+    template <int WHICH>
+    __device__ __forceinline__ uint32_t encode(uint32_t w, float s) const {
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, WHICH);
+    }
+    template <int WHICH>
+    __device__ __forceinline__ uint32_t encode_down(const Two& next, int c, uint32_t w, float s) const {
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[c], next.v[c], s, WHICH);
+    }
+};
+
+__device__ __forceinline__ uint32_t magnitude(uint32_t bits) { return bits & 0x7fffffffu; }
+
+// The largest over the 16 lanes of a row's block, in all of them.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    auto step = [](uint32_t x, auto ctrl) {
+        return max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), decltype(ctrl)::value, 0xf, 0xf, true)));
+    };
+    v = step(v, std::integral_constant<int, 0xB1>());   // quad_perm 1 0 3 2
+    v = step(v, std::integral_constant<int, 0x4E>());   // quad_perm 2 3 0 1
+    v = step(v, std::integral_constant<int, 0x141>());  // row_half_mirror
+    return step(v, std::integral_constant<int, 0x140>());  // row_mirror
+}
+
+// Lane l of a quad gets byte l of each of its four lanes' words, in their order.
+__device__ __forceinline__ uint32_t transpose_quad(uint32_t w, uint32_t pick) {
+    auto from = [&](auto ctrl) {
+        return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    const uint32_t w0 = from(std::integral_constant<int, 0x00>()), w1 = from(std::integral_constant<int, 0x55>());
+    const uint32_t w2 = from(std::integral_constant<int, 0xAA>()), w3 = from(std::integral_constant<int, 0xFF>());
+    // pick: byte l of the first operand (7..4) and of the second (3..0)
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w3, w2, pick), __builtin_amdgcn_perm(w1, w0, pick), 0x05040100);
+}
+
+constexpr int kTileBlock = 512;
+template <typename T, bool ROWS>
+__global__ __launch_bounds__(kTileBlock) void quantize_tile_kernel(TileArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // neighbouring tiles of a row of tiles on one XCD, whose L2 joins their halves of lines
+    const int64_t per = (a.tiles + kXcds - 1) / kXcds;
+    const int64_t tile = static_cast<int64_t>(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+    if (tile >= a.tiles) return;
+    const int64_t ct = tile % a.ctiles, block = tile / a.ctiles * 8 + wave, r0 = block * 32, j = ct * 128 + lane * 2;
+    const int64_t blocks = (a.cols + 31) / 32, blocks_t = (a.rows + 31) / 32;
+    const T* const x = static_cast<const T*>(a.x) + r0 * a.ldx + j;
+    Two<T> v[32];
+    if (r0 + 32 <= a.rows && ct * 128 + 128 <= a.cols) {
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-        const int64_t i = block * 32 + r;
-        float x = 0.0f;
-        if (i < a.rows) {
-            if constexpr (sizeof(T) == 2) x = widen(static_cast<const T*>(a.x)[i * a.ldx + j]);
-            else x = static_cast<const T*>(a.x)[i * a.ldx + j];
+        for (int r = 0; r < 32; ++r) v[r].load(x + r * a.ldx, 2);
+    } else {
+        const int cnt = static_cast<int>(max(static_cast<int64_t>(0), min(a.cols - j, static_cast<int64_t>(2))));
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            v[r] = Two<T>{};
+            if (r0 + r < a.rows && cnt > 0) v[r].load(x + r * a.ldx, cnt);
         }
-        v[r / 8][r % 8] = x;
-        top = max(top, __float_as_uint(x) & 0x7fffffffu);
     }
-    const uint32_t scale = scale_byte(top);
-    *reinterpret_cast<u32x4*>(a.codes + j * a.ldc + block * 16) =
-        u32x4{encode8(v[0], scale), encode8(v[1], scale), encode8(v[2], scale), encode8(v[3], scale)};
-    a.scales[j * a.lds + block] = static_cast<uint8_t>(scale);
+    {
+        uint32_t top[2] = {0, 0};
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            top[0] = max(top[0], magnitude(v[r].low()));
+            top[1] = max(top[1], magnitude(v[r].high()));
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (j + c >= a.cols) continue;
+            const uint32_t scale = scale_byte(top[c]);
+            const float s = __uint_as_float(scale << 23);
+            u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                w[q] = v[q * 8].template encode_down<0>(v[q * 8 + 1], c, w[q], s);
+                w[q] = v[q * 8 + 2].template encode_down<1>(v[q * 8 + 3], c, w[q], s);
+                w[q] = v[q * 8 + 4].template encode_down<2>(v[q * 8 + 5], c, w[q], s);
+                w[q] = v[q * 8 + 6].template encode_down<3>(v[q * 8 + 7], c, w[q], s);
+            }
+            if (scale == 255) w = u32x4{0, 0, 0, 0};
+            if (block < blocks_t) *reinterpret_cast<u32x4*>(a.codes_t + (j + c) * a.ldct + block * 16) = w;
+            if (block < (blocks_t + 15) / 16 * 16) a.scales_t[(j + c) * a.ldst + block] = static_cast<uint8_t>(scale);
+        }
+    }
+    if constexpr (ROWS) {
+        const int in = lane & 15;
+        const int64_t row_block = ct * 4 + (lane >> 4);
+        const uint32_t pick = 0x01010101u * (lane & 3) + 0x00000400u;  // bytes l and 4 + l
+        uint32_t kept[2] = {0, 0};                                     // the scales of rows `in` and 16 + in
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            uint32_t w = 0;
+            auto encode = [&](auto which) {
+                constexpr int k = decltype(which)::value;
+                const int r = g * 4 + k;
+                const uint32_t scale = scale_byte(max16(max(magnitude(v[r].low()), magnitude(v[r].high()))));
+                const bool finite = scale != 255;
+                w = (finite ? v[r] : Two<T>{}).template encode<k>(w, __uint_as_float(finite ? scale << 23 : 0x3f800000u));
+                if (in == (r & 15)) kept[r >> 4] = scale;
+            };
+            encode(std::integral_constant<int, 0>());
+            encode(std::integral_constant<int, 1>());
+            encode(std::integral_constant<int, 2>());
+            encode(std::integral_constant<int, 3>());
+            const uint32_t t = transpose_quad(w, pick);
+            const int64_t row = r0 + g * 4 + (lane & 3);
+            if (row < a.rows && row_block < blocks)
+                *reinterpret_cast<uint32_t*>(a.codes + row * a.ldc + ct * 64 + (lane >> 2) * 4) = t;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t row = r0 + h * 16 + in;
+            if (row < a.rows && row_block < (blocks + 15) / 16 * 16)
+                a.scales[row * a.lds + row_block] = static_cast<uint8_t>(kept[h]);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- values
@@ -123,34 +260,47 @@ struct ValuesArgs {
     int32_t wt;
 };
 
-// 16 bytes of values a lane.
+// 16 bytes of values a lane, of four rows whose codes are on their way together.
 template <typename T>
 __global__ __launch_bounds__(kElemBlock) void dequantize_kernel(ValuesArgs a) {
-    constexpr int kEach = 16 / sizeof(T);
+    constexpr int kEach = 16 / sizeof(T), kRows = 4;
     const int tid = threadIdx.x, per = kElemBlock >> a.g.tx;
     const int64_t rb = blockIdx.x / a.g.cblocks;
     const int64_t j = ((static_cast<int64_t>(blockIdx.x % a.g.cblocks) << a.g.tx) + (tid & ((1 << a.g.tx) - 1))) * kEach;
     if (j >= a.cols) return;
     const int cnt = static_cast<int>(min(a.cols - j, static_cast<int64_t>(kEach)));
     const int64_t end = min(a.rows, (rb + 1) * a.g.rows);
-    for (int64_t i = rb * a.g.rows + (tid >> a.g.tx); i < end; i += per) {
-        const uint8_t* const p = a.codes + i * a.ldc + j / 2;
-        const float s = __uint_as_float(static_cast<uint32_t>(a.scales[i * a.lds + j / 32]) << 23);
-        const uint32_t c = kEach == 8 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-        float v[kEach];
-        auto pair = [&](int q, auto which) {
-            typedef float f32x2 __attribute__((ext_vector_type(2)));
-            const f32x2 f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, decltype(which)::value);
-            v[2 * q] = f[0];
-            v[2 * q + 1] = f[1];
-        };
-        pair(0, std::integral_constant<int, 0>());
-        pair(1, std::integral_constant<int, 1>());
-        if constexpr (kEach == 8) {
-            pair(2, std::integral_constant<int, 2>());
-            pair(3, std::integral_constant<int, 3>());
+    for (int64_t i = rb * a.g.rows + (tid >> a.g.tx); i < end; i += kRows * per) {
+        uint32_t c[kRows], s[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            c[r] = s[r] = 0;
+            if (i + r * per >= end) continue;
+            const uint8_t* const p = a.codes + (i + r * per) * a.ldc + j / 2;
+            c[r] = kEach == 8 ? __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p))
+                              : static_cast<uint32_t>(__builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(p)));
+            s[r] = a.scales[(i + r * per) * a.lds + j / 32];
         }
-        stream_store(static_cast<T*>(a.y) + i * a.ldy + j, cnt, a.wt, v);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (i + r * per >= end) continue;
+            const float scale = __uint_as_float(s[r] << 23);
+            float v[kEach];
+            auto pair = [&](auto which) {
+                typedef float f32x2 __attribute__((ext_vector_type(2)));
+                constexpr int q = decltype(which)::value;
+                const f32x2 f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[r], scale, q);
+                v[2 * q] = f[0];
+                v[2 * q + 1] = f[1];
+            };
+            pair(std::integral_constant<int, 0>());
+            pair(std::integral_constant<int, 1>());
+            if constexpr (kEach == 8) {
+                pair(std::integral_constant<int, 2>());
+                pair(std::integral_constant<int, 3>());
+            }
+            stream_store(static_cast<T*>(a.y) + (i + r * per) * a.ldy + j, cnt, a.wt, v);
+        }
     }
 }
 
@@ -173,27 +323,30 @@ int32_t quantize_impl(uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds,
     TRY(check_overlaps({q.codes, q.scales, t.codes, t.scales, mx}, who, [](const Matrix&, const Matrix&) { return false; }));
     if (rows == 0 || cols == 0) return FSDP_OK;
     if (!codes && !codes_t) return fail(FSDP_E_ARG, "%s: null codes and codes_t", who);
-    RowsArgs r{codes, scales, x, ldc, lds, ldx, rows, cols, {}};
-    int64_t blocks;
-    r.g = elementwise_grid(rows, FSDP_MX4_SCALE_BYTES(cols) * 4, 16 * kCus / ceil_div(FSDP_MX4_SCALE_BYTES(cols) * 4, 64), &blocks);
-    blocks *= r.g.cblocks;
-    RowsArgs c{codes_t, scales_t, x, ldct, ldst, ldx, rows, cols, {}};
-    const int64_t cblocks = ceil_div(cols, 64), columns = cblocks * (FSDP_MX4_SCALE_BYTES(rows) / 4);
-    if ((codes && blocks > kMaxBlocks) || (codes_t && columns > kMaxBlocks))
-        return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
-    if (codes) {
+    if (!codes_t) {
+        RowsArgs r{codes, scales, x, ldc, lds, ldx, rows, cols, {}};
+        const int64_t chunks = FSDP_MX4_SCALE_BYTES(cols) * 4;
+        int64_t blocks;
+        r.g = elementwise_grid(rows, chunks, 16 * kCus / ceil_div(chunks, 64), &blocks);
+        blocks *= r.g.cblocks;
+        if (blocks > kMaxBlocks) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
         const dim3 grid(static_cast<uint32_t>(blocks));
         if (e == 2) quantize_rows_kernel<uint16_t><<<grid, dim3(kElemBlock), 0, stream>>>(r);
         else quantize_rows_kernel<float><<<grid, dim3(kElemBlock), 0, stream>>>(r);
-        TRY(launched(who));
+        return launched(who);
     }
-    if (codes_t) {
-        const dim3 grid(static_cast<uint32_t>(columns));
-        if (e == 2) quantize_columns_kernel<uint16_t><<<grid, dim3(kElemBlock), 0, stream>>>(c, cblocks);
-        else quantize_columns_kernel<float><<<grid, dim3(kElemBlock), 0, stream>>>(c, cblocks);
-        TRY(launched(who));
-    }
-    return FSDP_OK;
+    // tiles to the end of the scale rows' padding
+    TileArgs a{codes, scales, codes_t, scales_t, x, ldc, lds, ldct, ldst, ldx, rows, cols, 0, 0};
+    a.ctiles = codes ? FSDP_MX4_SCALE_BYTES(cols) / 4 : ceil_div(cols, 128);
+    a.tiles = a.ctiles * (FSDP_MX4_SCALE_BYTES(rows) / 8);
+    const int64_t blocks = round_up(a.tiles, kXcds);
+    if (blocks > kMaxBlocks) return fail(FSDP_E_CAPACITY, "%s: more blocks than one launch holds", who);
+    const dim3 grid(static_cast<uint32_t>(blocks)), block(kTileBlock);
+    if (e == 2 && codes) quantize_tile_kernel<uint16_t, true><<<grid, block, 0, stream>>>(a);
+    else if (e == 2) quantize_tile_kernel<uint16_t, false><<<grid, block, 0, stream>>>(a);
+    else if (codes) quantize_tile_kernel<float, true><<<grid, block, 0, stream>>>(a);
+    else quantize_tile_kernel<float, false><<<grid, block, 0, stream>>>(a);
+    return launched(who);
 }
 
 int32_t dequantize_impl(void* y, int64_t ldy, int32_t y_dtype, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
