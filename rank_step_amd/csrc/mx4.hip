@@ -54,7 +54,8 @@ struct RowsArgs {
     Grid g;
 };
 
-// Eight elements a lane, four lanes a block.
+// Eight elements a lane, four lanes a block.  Bound by memory: 8192 x 4096 bf16 13.9
+// us (6.1 TB/s).
 template <typename T>
 __global__ __launch_bounds__(kElemBlock) void quantize_rows_kernel(RowsArgs a) {
     const int tid = threadIdx.x, per = kElemBlock >> a.g.tx;
@@ -85,10 +86,14 @@ __global__ __launch_bounds__(kElemBlock) void quantize_rows_kernel(RowsArgs a) {
 // Eight waves take 256 rows of 128 columns, each wave 32 rows, a lane two
 // columns of them: 32 loads on their way, 256 bytes of a row (bf16) each.  A
 // column's block is a lane's own; a row's block is 16 lanes', whose largest
-// magnitude four DPP steps find.  So x is read once for both copies, without LDS.
-// A column's codes go out as 16 bytes a lane, which the eight waves' neighbouring
-// blocks complete to a line in L2; a row's as words, after the four lanes of a quad
-// have exchanged bytes of four rows.
+// magnitude four DPP steps find.  So x is read once for both copies, from registers.
+// The codes of a column's eight blocks are a line, which goes through LDS to be
+// stored as one; a row's go out as words, after the four lanes of a quad have
+// exchanged bytes of four rows.  8192 x 4096 bf16 about 25 us (4.1 TB/s; floor 16);
+// with 16 bytes of a column stored by each lane 30, by a launch for each copy 48.
+// What is left is the vector unit beside memory: about 12 operations an element.
+// Workgroups that stay and fetch their next tile meanwhile: 6 to 15 % slower; four
+// waves: 2 to 5 %; ordinary loads: 13 %.
 struct TileArgs {
     uint8_t* codes;    // blocks along rows, or null
     uint8_t* scales;
@@ -177,6 +182,8 @@ __global__ __launch_bounds__(kTileBlock) void quantize_tile_kernel(TileArgs a) {
     if (tile >= a.tiles) return;
     const int64_t ct = tile % a.ctiles, block = tile / a.ctiles * 8 + wave, r0 = block * 32, j = ct * 128 + lane * 2;
     const int64_t blocks = (a.cols + 31) / 32, blocks_t = (a.rows + 31) / 32;
+    __shared__ u32x4 line[128][8];  // a column's codes of the eight waves' blocks
+    __shared__ __attribute__((aligned(8))) uint8_t bytes[128][8];
     const T* const x = static_cast<const T*>(a.x) + r0 * a.ldx + j;
     Two<T> v[32];
     if (r0 + 32 <= a.rows && ct * 128 + 128 <= a.cols) {
@@ -199,7 +206,6 @@ __global__ __launch_bounds__(kTileBlock) void quantize_tile_kernel(TileArgs a) {
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            if (j + c >= a.cols) continue;
             const uint32_t scale = scale_byte(top[c]);
             const float s = __uint_as_float(scale << 23);
             u32x4 w = {0, 0, 0, 0};
@@ -211,10 +217,21 @@ __global__ __launch_bounds__(kTileBlock) void quantize_tile_kernel(TileArgs a) {
                 w[q] = v[q * 8 + 6].template encode_down<3>(v[q * 8 + 7], c, w[q], s);
             }
             if (scale == 255) w = u32x4{0, 0, 0, 0};
-            if (block < blocks_t) *reinterpret_cast<u32x4*>(a.codes_t + (j + c) * a.ldct + block * 16) = w;
-            if (block < (blocks_t + 15) / 16 * 16) a.scales_t[(j + c) * a.ldst + block] = static_cast<uint8_t>(scale);
+            line[lane * 2 + c][wave ^ (lane & 7)] = w;
+            bytes[lane * 2 + c][wave] = static_cast<uint8_t>(scale);
         }
     }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int id = k * kTileBlock + threadIdx.x, col = id >> 3, at = id & 7;
+        const int64_t to = tile / a.ctiles * 8 + at;
+        if (ct * 128 + col < a.cols && to < blocks_t)
+            *reinterpret_cast<u32x4*>(a.codes_t + (ct * 128 + col) * a.ldct + to * 16) = line[col][at ^ (col >> 1 & 7)];
+    }
+    if (threadIdx.x < 128 && ct * 128 + threadIdx.x < a.cols)
+        *reinterpret_cast<u32x2*>(a.scales_t + (ct * 128 + threadIdx.x) * a.ldst + tile / a.ctiles * 8) =
+            *reinterpret_cast<const u32x2*>(bytes[threadIdx.x]);
     if constexpr (ROWS) {
         const int in = lane & 15;
         const int64_t row_block = ct * 4 + (lane >> 4);
@@ -260,7 +277,9 @@ struct ValuesArgs {
     int32_t wt;
 };
 
-// 16 bytes of values a lane, of four rows whose codes are on their way together.
+// 16 bytes of values a lane, of four rows whose codes are on their way together
+// (of one at a time 18.5 us for 8192 x 4096 as bf16, this way 16.2, 5.2 TB/s; of
+// eight no faster).  Bound by the stores.
 template <typename T>
 __global__ __launch_bounds__(kElemBlock) void dequantize_kernel(ValuesArgs a) {
     constexpr int kEach = 16 / sizeof(T), kRows = 4;
