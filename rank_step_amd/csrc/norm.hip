@@ -135,6 +135,17 @@ __device__ __forceinline__ void widen_again(u32x4 (&w)[C]) {
     for (int c = 0; c < C; ++c) asm volatile("" : "+v"(w[c])::"memory");
 }
 
+// The variance about the true mean, which lies `off` from the first estimate
+// by the sum of the differences; and the mean itself where it is large against the
+// spread.  Elsewhere the first estimate is the better one: of bf16 values a sum is
+// nearly exact, where the differences' roundings are alike for all values of a
+// binade and do not cancel (3e-8 of the spread).
+__device__ __forceinline__ void correct(float off, float& mean, float& var) {
+    if (mean * mean > 16.0f * var) mean += off;
+    var = fmaf(-off, off, var);
+    var = var < 0.0f ? 0.0f : var;  // NaN stays
+}
+
 // ---------------------------------------------------------------- forward
 
 struct ForwardArgs {
@@ -181,7 +192,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_ke
             mean = sum[0] / n;
             widen_again(raw);
         }
-        // About that mean, whose own rounding and sum the first moment corrects.
+        // About that mean.
         float sum[2] = {0.0f, 0.0f};
         if (row.tail()) {
             sum[0] = end - mean;
@@ -201,10 +212,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_ke
         row_sum<WAVES>(sum, s1);
         float var = sum[1] / n;
         if (!a.rms) {
-            const float off = sum[0] / n;
-            mean += off;
-            var = fmaf(-off, off, var);
-            var = var < 0.0f ? 0.0f : var;  // NaN stays
+            correct(sum[0] / n, mean, var);
         }
         const float rstd = 1.0f / sqrtf(var + a.eps);
         if (t == 0) {
@@ -261,10 +269,7 @@ __global__ __launch_bounds__(kLongBlock) void norm_forward_long_kernel(ForwardAr
         row_sum<kLongWaves>(sum, s1);
         float var = sum[1] / n;
         if (!a.rms) {
-            const float off = sum[0] / n;
-            mean += off;
-            var = fmaf(-off, off, var);
-            var = var < 0.0f ? 0.0f : var;  // NaN stays
+            correct(sum[0] / n, mean, var);
         }
         const float rstd = 1.0f / sqrtf(var + a.eps);
         if (threadIdx.x == 0) {

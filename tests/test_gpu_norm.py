@@ -8,8 +8,9 @@ Tolerances, with u = 2^-24 (half an fp32 step) and L = 64 + n / 1024, which no
 chain of a row's additions is longer than (32 in a lane, 6 over a wave, 16 over
 waves; rows that registers do not hold: n / 1024 in a thread):
 
-* mean: taken about a first estimate, so L u of the mean distance from it, and
-  2u of itself;
+* mean: its first estimate is off by L u of the mean magnitude and u of itself;
+  where it exceeds four times the spread it is corrected by the mean distance
+  from that, so L u of the spread, and 2u of itself;
 * variance: (L + 8) u of itself (and of the square of the mean's error), so
   half of that in rstd, with 4u for eps, the root and the quotient;
 * y: those, 4u of the value for its four operations;
@@ -72,7 +73,8 @@ def check_forward(m, n, dtype="bf16", kind="layer", wt="bf16", weight=True, bias
     var = ((xv - mv[:, None]) ** 2).mean(axis=1)  # of the values: 1 / rstd^2 - eps cancels where eps is the larger
     if kind == "layer":
         first = long * U * np.abs(xv).mean(axis=1) + U * np.abs(mv)  # the first estimate's error
-        em = 2 * U * np.abs(mv) + (long + 3) * U * (np.sqrt(var) + first)
+        near = mv * mv < 17 * var
+        em = 2 * U * np.abs(mv) + (long + 3) * U * (np.sqrt(var) + first) + np.where(near, first, 0)
     else:
         first, em = 0 * mv, 0 * mv
     er = rv * (0.5 * (long + 8) * U * (var + first ** 2 + em ** 2) * rv ** 2 + 4 * U)
