@@ -216,7 +216,8 @@ struct Epilogue {
 // and residual; the gradients use the division, the accumulation and the
 // store.  Every row's residual is read before the first row is stored, so that
 // the reads wait once (the output may be the residual, element for element).
-template <int NB>
+// HALVES: fp32 outputs with ordinary stores, whose halves of lines L2 joins.
+template <int NB, bool HALVES = false>
 __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int step, int64_t m, int64_t j, int cnt,
                                           float recip, uint64_t off, float (&v)[NB][8]) {
     float r[NB][8];
@@ -266,7 +267,8 @@ __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int st
     for (int b = 0; b < NB; ++b) {
         const int64_t i = row + b * step;
         if (i < m) {
-            if (e.out_f32) output8(static_cast<float*>(e.out) + i * e.ldo + j, cnt, v[b]);
+            if (e.out_f32 && HALVES) store8(static_cast<float*>(e.out) + i * e.ldo + j, cnt, v[b]);
+            else if (e.out_f32) output8(static_cast<float*>(e.out) + i * e.ldo + j, cnt, v[b]);
             else output8(static_cast<uint16_t*>(e.out) + i * e.ldo + j, cnt, v[b]);
         }
     }
