@@ -1,6 +1,6 @@
 // Host logic of the 4-bit matrices (include/fsdp_mx4.h): their checks, and by
-// which launches a product is computed.  Plain
-// C++ without device code.
+// which launches a product is computed.  Plain C++ without device code, so that
+// host tests reach it.
 #pragma once
 
 #include "fsdp_mx4.h"
