@@ -292,7 +292,7 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
         ta.init(g.a, g.lda, i0, g.m, lbeg, lend, tid);
         tb.init(g.b, g.ldb, j0, g.n, lbeg, lend, tid);
         ts.init(g, i0, j0, lbeg, lend, filler, lane);
-        constexpr int kSlots = kFI * kFJ, kLag = kSlots / 8;
+        constexpr int kSlots = kFI * kFJ, kEarly = kSlots / 8, kLag = kSlots / 4, kStop = kSlots * 5 / 4;
 
         // A's fragments of a step's first half, and of the second half of this step
         // and the next; B's of both halves; the scales of this step and the next.
@@ -315,30 +315,41 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
         };
         // The step of parity p in a0 and b0 (or whichever are `a` and `bb`); the next one
         // is in `na` and `nb`, with its scales the half h of `scales`.
-        //   first half   reads B of the second, and the next step's scales; A's stage,
-        //                read whole before, is filled with the step after the next
-        //   second half  reads all of A and the first half of B of the next step; B's
-        //                stage is filled
-        // So the loads, which take half a step's time to pass, are spread over all of
-        // it, each at least half a step before its use.  Before a stage is filled all
-        // waves have read it: a barrier stands between the halves, and one early in the
-        // first, when the reads at the end of the step before have come.
+        //   first half   reads B of the second, at once, then the next step's scales
+        //   second half  reads all of A and the first half of B of the next step
+        // Before the step's two stages are filled with the step after the next all waves
+        // have read them: a barrier stands at slot kLag, when the reads at the end of the
+        // step before and those of B have come; another between the halves, where the
+        // next step's stages are there.  The loads are spread over the slots from kLag to
+        // kStop of the step's 2 kSlots: packed more densely they pass no faster, the last
+        // ones later come late (8192 x 28672 x 8192 851 us; to the end of the first half
+        // 855, to the middle of the second 859, to its end 863).
         auto step = [&](Lds* a, Lds* bb, Lds* na, Lds* nb, int p, const Lds* scales, int h, auto fill, Lds* more) {
-            constexpr int kFills = tb.kLoads + (decltype(fill)::value ? ts.kLoads : 0), kScales = kFI + kFJ;
+            constexpr int kScales = kFI + kFJ, kAll = ta.kLoads + tb.kLoads + (decltype(fill)::value ? ts.kLoads : 0);
+            auto load = [&](auto slot) {  // of the step's
+                for_slot<kAll, decltype(slot)::value, kStop - kLag>([&](auto i) {
+                    constexpr int q = decltype(i)::value;
+                    if constexpr (q < ta.kLoads) ta.load(a, filler, q);
+                    else if constexpr (q < ta.kLoads + tb.kLoads) tb.load(bb, filler, q - ta.kLoads);
+                    else ts.load(more, filler, q - ta.kLoads - tb.kLoads);
+                });
+            };
             multiply(std::integral_constant<int, 0>(), p, [&](auto slot) {
                 constexpr int t = decltype(slot)::value;
-                for_slot<kFJ + kScales, t, kSlots>([&](auto i) {
-                    constexpr int q = decltype(i)::value;
-                    if constexpr (q < kFJ) b[1][q] = fb.get(bb, q, 1);
-                    else if constexpr (q < 2 * kFJ) sb[1 - p][q - kFJ] = fb.get_scale(scales, q - kFJ, h);
-                    else sa[1 - p][q - 2 * kFJ] = fa.get_scale(scales, q - 2 * kFJ, h);
-                });
+                if constexpr (t < kEarly) for_slot<kFJ, t, kEarly>([&](auto q) { b[1][decltype(q)::value] = fb.get(bb, decltype(q)::value, 1); });
                 if constexpr (t == kLag) mx4_read<kShared>();
-                if constexpr (t >= kLag)
-                    for_slot<ta.kLoads, t - kLag, kSlots - kLag>([&](auto q) { ta.load(a, filler, decltype(q)::value); });
+                if constexpr (t >= kLag) {
+                    for_slot<kScales, t - kLag, kSlots - kLag>([&](auto i) {
+                        constexpr int q = decltype(i)::value;
+                        if constexpr (q < kFJ) sb[1 - p][q] = fb.get_scale(scales, q, h);
+                        else sa[1 - p][q - kFJ] = fa.get_scale(scales, q - kFJ, h);
+                    });
+                    if constexpr (t < kStop) load(std::integral_constant<int, t - kLag>());
+                }
             });
-            // (the scales are the newest reads, B the oldest)
-            mx4_arrive<kShared, ta.kLoads, kScales < 15 ? kScales : 15>();
+            // (the scales are the newest reads)
+            constexpr int kIssued = kStop > kSlots ? (kSlots - kLag) * kAll / (kStop - kLag) : kAll;
+            mx4_arrive<kShared, kIssued, kScales < 15 ? kScales : 15>();
             multiply(std::integral_constant<int, 1>(), p, [&](auto slot) {
                 constexpr int t = decltype(slot)::value;
                 for_slot<2 * kFI + kFJ, t, kSlots>([&](auto i) {
@@ -347,11 +358,7 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
                     else if constexpr (q < 2 * kFI) y[1 - p][q - kFI] = fa.get(na, q - kFI, 1);
                     else b[0][q - 2 * kFI] = fb.get(nb, q - 2 * kFI, 0);
                 });
-                for_slot<kFills, t, kSlots>([&](auto i) {
-                    constexpr int q = decltype(i)::value;
-                    if constexpr (q < tb.kLoads) tb.load(bb, filler, q);
-                    else ts.load(more, filler, q - tb.kLoads);
-                });
+                if constexpr (t + kSlots < kStop) load(std::integral_constant<int, t + kSlots - kLag>());
             });
         };
 
