@@ -429,9 +429,11 @@ constexpr int backward_rows(int waves) { return waves == 1 ? 8 : 1; }
 // x 4096 bf16 with a residual and both sums 58 us, of which 5 for joining the
 // workgroups' sums (floor 41).  A workgroup leaves one row of sums, and two a CU
 // stay for all rows: three a CU 69 us, four 73, for more sums to write and read;
-// one 69, for fewer loads on their way.
+// one 69, for fewer loads on their way.  The registers allow two a CU with one
+chunk a lane only (8192 x 1000: two of which one waits 24 us, one 18), and there
+they are held to it (8192 x 4095: 113 us without, this way 84).
 template <typename T, int WAVES, int C, bool TAIL>
-__global__ __launch_bounds__(backward_rows(WAVES) * WAVES * 64) void norm_backward_kernel(BackwardArgs a) {
+__global__ __launch_bounds__(backward_rows(WAVES) * WAVES * 64, C == 1 ? 4 : 2) void norm_backward_kernel(BackwardArgs a) {
     constexpr int kEach = 16 / sizeof(T), kRows = backward_rows(WAVES);
     __shared__ float s[2][2][WAVES];
     __shared__ float joined[kRows > 1 ? 2 : 1][kRows > 1 ? C * kEach + TAIL : 1][64];
@@ -840,7 +842,9 @@ int32_t launch_backward(BackwardArgs a, const Sums& out, float* workspace, int64
     const Division d = sums_division(a.n, sizeof(T));
     // with room for fewer parts than a quarter of the chip the sums are taken apart
     if (sums && a.dx && d.waves > 0 && room >= kCus / 4) {
-        const int64_t blocks = std::min(std::min<int64_t>(ceil_div(a.m, backward_rows(d.waves)), (d.waves <= 8 ? 2 : 1) * kCus), room);
+        // as many as a CU holds at a time
+        const int64_t per_cu = d.waves <= 8 && d.chunks == 1 ? 2 : 1;
+        const int64_t blocks = std::min(std::min<int64_t>(ceil_div(a.m, backward_rows(d.waves)), per_cu * kCus), room);
         a.part = workspace;
         auto run = [&](auto waves, auto chunks) {
             constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
