@@ -430,8 +430,8 @@ constexpr int backward_rows(int waves) { return waves == 1 ? 8 : 1; }
 // workgroups' sums (floor 41).  A workgroup leaves one row of sums, and two a CU
 // stay for all rows: three a CU 69 us, four 73, for more sums to write and read;
 // one 69, for fewer loads on their way.  The registers allow two a CU with one
-chunk a lane only (8192 x 1000: two of which one waits 24 us, one 18), and there
-they are held to it (8192 x 4095: 113 us without, this way 84).
+// chunk a lane only (8192 x 1000: two of which one waits 24 us, one 18), and there
+// they are held to it (8192 x 4095: 113 us without, this way 84).
 template <typename T, int WAVES, int C, bool TAIL>
 __global__ __launch_bounds__(backward_rows(WAVES) * WAVES * 64, C == 1 ? 4 : 2) void norm_backward_kernel(BackwardArgs a) {
     constexpr int kEach = 16 / sizeof(T), kRows = backward_rows(WAVES);
