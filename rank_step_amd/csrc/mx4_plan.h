@@ -51,11 +51,11 @@ inline Parts mx4_parts_of(int64_t k, int64_t splits) {
 // measured over products of one 64 x 64 tile to 8192 x 11008 x 4096, within a
 // sixth of them but for the smallest.
 //   256: a step takes 1.1 us on a near empty chip, 1.6 on a full one, where
-//     power sets the clock.  4096 x 4096 x 4096: 39.5 us, by 128-tiles 45.2.
+//     power sets the clock.  4096 x 4096 x 4096: 37.5 us, by 128-tiles 45.2.
 //   128: two workgroups a CU, 1.08 us a step for both; alone 0.37 to 0.67.
-//     2048 x 2048 x 4096: 14.1 us, by 256-tiles 31.4, by 64-tiles 28.0.
-//   64: four waves on four parts of a step.  1024 x 1024 x 4096: 7.5 us, by
-//     128-tiles 11.9.  64 x 64 x 16384: 13.2 us, split in four 9.7.
+//     2048 x 2048 x 4096: 13.1 us, by 256-tiles 31.4, by 64-tiles 28.0.
+//   64: four waves on four parts of a step.  1024 x 1024 x 4096: 7.6 us, by
+//     128-tiles 11.9.  64 x 64 x 16384: 13.2 us, split in four 9.7, in seven 9.2.
 inline Way mx4_way_of(int tile, int64_t splits, const Extent& g) {
     const double tiles = static_cast<double>(ceil_div(g.m, tile)) * ceil_div(g.n, tile) * splits;
     const double steps = static_cast<double>(ceil_div(ceil_div(g.k, kBK), splits)), fill = std::min(1.0, tiles / kCus);

@@ -842,8 +842,10 @@ int32_t launch_backward(BackwardArgs a, const Sums& out, float* workspace, int64
     const Division d = sums_division(a.n, sizeof(T));
     // with room for fewer parts than a quarter of the chip the sums are taken apart
     if (sums && a.dx && d.waves > 0 && room >= kCus / 4) {
-        // as many as a CU holds at a time
-        const int64_t per_cu = d.waves <= 8 && d.chunks == 1 ? 2 : 1;
+        // as many as a CU holds at a time; of four waves, two, or three for many rows
+        // (30000 x 2048 bf16 101 us by two, 91 by three; 8192 x 2001 59 and 52; 2000 x 2048
+        // 18 and 22)
+        const int64_t per_cu = d.waves > 8 || d.chunks > 1 ? 1 : d.waves == 4 && a.m >= 32 * kCus ? 3 : 2;
         const int64_t blocks = std::min(std::min<int64_t>(ceil_div(a.m, backward_rows(d.waves)), per_cu * kCus), room);
         a.part = workspace;
         auto run = [&](auto waves, auto chunks) {
