@@ -55,7 +55,7 @@ struct RowsArgs {
 };
 
 // Eight elements a lane, four lanes a block.  Bound by memory: 8192 x 4096 bf16 13.9
-// us (6.1 TB/s).
+// us (6.1 TB/s), fp32 23.
 template <typename T>
 __global__ __launch_bounds__(kElemBlock) void quantize_rows_kernel(RowsArgs a) {
     const int tid = threadIdx.x, per = kElemBlock >> a.g.tx;
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(kElemBlock) void quantize_rows_kernel(RowsArgs a) {
 // magnitude four DPP steps find.  So x is read once for both copies, from registers.
 // The codes of a column's eight blocks are a line, which goes through LDS to be
 // stored as one; a row's go out as words, after the four lanes of a quad have
-// exchanged bytes of four rows.  8192 x 4096 bf16 about 25 us (4.1 TB/s; floor 16);
+// exchanged bytes of four rows.  8192 x 4096 bf16 26 us (3.9 TB/s; floor 16);
 // with 16 bytes of a column stored by each lane 30, by a launch for each copy 48.
 // What is left is the vector unit beside memory: about 12 operations an element.
 // Workgroups that stay and fetch their next tile meanwhile: 6 to 15 % slower; four

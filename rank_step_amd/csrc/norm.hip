@@ -409,7 +409,7 @@ __device__ __forceinline__ void dx_row(const BackwardArgs& a, int64_t i, int t, 
 }
 
 // dx alone: without column sums, or beside norm_columns_kernel for rows whose
-// sums registers do not hold.
+// sums registers do not hold.  Bound by memory: 8192 x 4096 bf16 35 us (5.8 TB/s).
 template <typename T, int WAVES, int C, bool TAIL>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_dx_kernel(BackwardArgs a) {
     constexpr int kRows = WAVES == 1 ? 4 : 1;
@@ -597,7 +597,8 @@ __global__ __launch_bounds__(kLongBlock) void norm_backward_long_kernel(Backward
 }
 
 // The column sums alone: 64 chunks of columns by 4 rows at a time, `rows` rows a
-// block, into a row of `part` each; with one row block, into the results.
+// block, into a row of `part` each; with one row block, into the results.  The
+// second read of dy and x makes 8192 x 11008 bf16 208 us in all, of which dx 108.
 struct Sums {
     void* dw;
     void* db;
@@ -698,7 +699,7 @@ __global__ __launch_bounds__(256) void norm_backward_few_kernel(BackwardArgs a, 
 }
 
 // dw and db from `rows` rows of sums: 32 columns a block, 32 threads a column,
-// their sums added in order.
+// their sums added in order.  512 rows of 8192 columns: 4.8 us.
 constexpr int kSumBlock = 1024, kSumColumns = 32;
 __global__ __launch_bounds__(kSumBlock) void norm_sum_kernel(const float* part, int64_t n, int64_t rows, Sums out) {
     __shared__ float sums[kSumBlock / kSumColumns][kSumColumns + 1];
