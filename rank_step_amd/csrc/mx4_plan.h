@@ -47,21 +47,28 @@ inline Parts mx4_parts_of(int64_t k, int64_t splits) {
     return {static_cast<int32_t>(ceil_div(turns, per)), static_cast<int32_t>(per * 2 * kBK)};
 }
 
+// The waves that share the contraction of a 64-tile, in `blocks` workgroups: four,
+// one workgroup a CU; or where there are more workgroups than CUs two, and two
+// workgroups a CU.  1024 x 2048 x 4096: 10.6 us, by four 13.7; 1024 x 1365 x 2047: 8.3
+// and 11.5; 1024 x 1024 x 4096, 256 workgroups: 8.0 and 7.6.
+inline int mx4_waves(double blocks) { return blocks > kCus ? 2 : 4; }
+
 // What a product takes in microseconds, as way_of in linear_plan.h: from times
 // measured over products of one 64 x 64 tile to 8192 x 11008 x 4096, within a
 // sixth of them but for the smallest.
 //   256: a step takes 1.1 us on a near empty chip, 1.6 on a full one, where
 //     power sets the clock.  4096 x 4096 x 4096: 37.5 us, by 128-tiles 45.2.
 //   128: two workgroups a CU, 1.08 us a step for both; alone 0.37 to 0.67.
-//     2048 x 2048 x 4096: 13.1 us, by 256-tiles 31.4, by 64-tiles 28.0.
-//   64: four waves on four parts of a step.  1024 x 1024 x 4096: 7.6 us, by
-//     128-tiles 11.9.  64 x 64 x 16384: 13.2 us, split in four 9.7, in seven 9.2.
+//     2048 x 2048 x 4096: 13.1 us, by 256-tiles 31.4, by 64-tiles 21.8.
+//   64: waves on parts of a step.  1024 x 1024 x 4096: 7.6 us, by 128-tiles 11.7;
+//     1024 x 2048 x 4096: 10.6 and 12.0; 1024 x 2048 x 11008: 24.1 and 27.2.  64 x 64 x 16384: 13.2 us, split in four 9.7, in seven 9.2.
 inline Way mx4_way_of(int tile, int64_t splits, const Extent& g) {
     const double tiles = static_cast<double>(ceil_div(g.m, tile)) * ceil_div(g.n, tile) * splits;
     const double steps = static_cast<double>(ceil_div(ceil_div(g.k, kBK), splits)), fill = std::min(1.0, tiles / kCus);
     double us;
     if (tile == 256) us = 3 + std::ceil(tiles / kCus) * (10 + (1.1 + 0.5 * fill) * steps);
-    else if (tile == 64) us = 0.5 + std::ceil(tiles / kCus) * (4.4 + 0.135 * steps);
+    else if (tile == 64 && mx4_waves(tiles) == 2) us = 0.5 + std::ceil(tiles / (2 * kCus)) * (4.9 + 0.37 * steps);
+    else if (tile == 64) us = 4.9 + 0.135 * steps;
     else if (tiles <= kCus) us = 5.5 + (0.37 + 0.3 * fill) * steps;
     else us = 1 + std::ceil(tiles / (2 * kCus)) * (4.6 + 1.08 * steps);
     if (splits > 1) us += 3 + std::max(8.0 * splits * g.m * g.pitch / 6e6, 0.1 * (splits - 24));

@@ -556,6 +556,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_rows_kernel(Mx4Product
 
 // ---------------------------------------------------------------- host
 
+// Named, since the compiler otherwise leaves out the host's part of one of the two.
+template __global__ void mx4_product_kernel<64, 64, 1, 1, 2>(Mx4Product g);
+template __global__ void mx4_product_kernel<64, 64, 1, 1, 4>(Mx4Product g);
+
 template <int BM, int BN, int WI, int WJ, int KW>
 int32_t launch_mx4(Mx4Product& g, hipStream_t stream, const char* who) {
     g.tm = static_cast<int32_t>(ceil_div(g.m, BM));
@@ -618,7 +622,9 @@ int32_t run_mx4(Mx4Product& g, const Space& space, hipStream_t stream, const cha
     g.part = reinterpret_cast<float*>(space.p);
     if (best.tile == 256) return launch_mx4<256, 256, 2, 2, 1>(g, stream, who);
     if (best.tile == 128) return launch_mx4<128, 128, 2, 2, 1>(g, stream, who);
-    return launch_mx4<64, 64, 1, 1, 4>(g, stream, who);
+    const int64_t blocks = ceil_div(g.m, 64) * ceil_div(g.n, 64) * g.splits;
+    if (mx4_waves(static_cast<double>(blocks)) == 4) return launch_mx4<64, 64, 1, 1, 4>(g, stream, who);
+    return launch_mx4<64, 64, 1, 1, 2>(g, stream, who);
 }
 
 int32_t mx4_product_impl(const fsdp_mx4_operands* a, hipStream_t stream) {

@@ -43,7 +43,9 @@ static bool walk(const Extent& g, const Space& space, char* out, size_t room, in
         return walk(q, space, out + used + 1, room - used - 1, depth + 1);
     }
     const Parts s = mx4_parts_of(g.k, best.splits);
-    snprintf(out, room, "%d/%d", best.tile, s.n);
+    const double blocks = std::ceil(g.m / 64.0) * std::ceil(g.n / 64.0) * s.n;
+    if (best.tile == 64) snprintf(out, room, "64x%d/%d", mx4_waves(blocks), s.n);
+    else snprintf(out, room, "%d/%d", best.tile, s.n);
     // whole pairs of steps, none empty, all covered; sums within the workspace; a possible launch
     const int64_t k = g.k, per = s.k;
     if (s.n < 1 || per % (2 * kBK) || per * s.n < k || (s.n > 1 && per * (s.n - 1) >= k) || s.n > best.splits) return false;

@@ -47,5 +47,5 @@ def test_every_way_is_in_the_gpu_tests(exe):
     wrong = [(r, g) for r, g in zip(ROUTES, got) if r[4] != g]
     assert not wrong, wrong
     ways = " ".join(r[4] for r in ROUTES)
-    for way in ("few 1", "few 2", "few 3", "few 4", "64/1", "64/4", "64/16", "128/1", "256/1", "columns", "rows"):
+    for way in ("few 1", "few 2", "few 3", "few 4", "64x4/1", "64x4/4", "64x4/16", "64x2/1", "128/1", "256/1", "columns", "rows"):
         assert way in ways
