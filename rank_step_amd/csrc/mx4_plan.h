@@ -80,9 +80,12 @@ inline Way mx4_best_way(const Extent& g, const Space& space) { return best_way_b
 inline Cut mx4_cut_of(const Extent& g, const Way& best, const Space& space) { return cut_by<mx4_way_of>(g, best, space); }
 
 // Whether the product takes the way for few rows of A: what one matrix
-// instruction takes.  32 rows by it and by tiles: [11008, 4096] 8.6 and 7.1 us,
-// [28672, 8192] 40.9 and 24.6, [4096, 4096] 6.3 and 7.0.
-inline bool mx4_few(int64_t m) { return m <= 16; }
+// instruction takes, where 64-tiles would not give more than every CU one.  By it
+// and by tiles: 16 rows, [4096, 4096] 5.6 and 7.0 us, [8192, 8192] 9.0 and 10.7,
+// [16384, 4096] 8.2 and 8.6, [28672, 8192] 26.9 and 21.5, [32000, 4096] 16.4 and 14.0;
+// one row, [28672, 8192] 27.1 and 21.0; 32 rows, [11008, 4096] 8.6 and 7.2, [4096, 4096]
+// 6.3 and 7.0.
+inline bool mx4_few(int64_t m, int64_t n) { return m <= 16 && n <= 64 * kCus; }
 
 // The columns of a workgroup of that way: A is read again by each, B's rows
 // once, and the CU with the most workgroups ends last; so the least rounds *

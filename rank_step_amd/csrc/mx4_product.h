@@ -238,7 +238,7 @@ __device__ __forceinline__ void mx4_finish(const Product& g, f32x4 (&acc)[FI][FJ
 // buffer of their own, of which there are two as well.
 //
 // Bound by power, and next by the way of the operands to LDS.  8192 x 28672 x 8192
-// as bf16 834 to 858 us (4.5 to 4.6 PFLOP/s); matrix instructions of random codes
+// as bf16 823 to 858 us (4.5 to 4.7 PFLOP/s); matrix instructions of random codes
 // from registers alone reach 7.2, of zeros 9.8.  A step of a full chip takes 1.49 us
 // of random codes, at 1.97 GHz, and 1.15 of zeros, at 2.4: 2750 cycles, of which 2048
 // are the matrix instructions'.  With the loads left out it is 1.20 and 0.94; from
@@ -454,12 +454,12 @@ __global__ __launch_bounds__(WI* WJ* KW * 64) void mx4_product_kernel(Mx4Product
     }
 }
 
-// The product for at most 16 rows of A: bound by reading B once, and by a launch's
-// start and end for small ones: 1 x 28672 x 8192 27.0 us (4.6 TB/s), 16 x 11008 x
-// 4096 7.9, 1 x 4096 x 4096 6.9 (of which 4.6 on the card).  As
-// few_rows_kernel, with the eight waves taking every eighth 512 contraction
-// elements, 256 bytes of a row and 16 scales, from memory straight into the
-// fragments: lane group q takes blocks 4q to 4q + 3, whose scales are one word.
+// The product for at most 16 rows of A and not very many of B: bound by reading B
+// once, and by a launch's start and end for small ones: 1 x 8192 x 8192 7.3 us (4.9
+// TB/s), 16 x 11008 x 4096 7.2 to 7.9, 1 x 4096 x 4096 5.5 to 6.9 (of which 4.6 on the
+// card).  As few_rows_kernel, with the eight waves taking every eighth 512
+// contraction elements, 256 bytes of a row and 16 scales, from memory straight into
+// the fragments: lane group q takes blocks 4q to 4q + 3, whose scales are one word.
 template <int JB>
 __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_rows_kernel(Mx4Product g) {
     typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -605,7 +605,7 @@ Mx4Product mx4_rows(const Mx4Product& g, int64_t i0, int64_t m) {
 
 // The product whole, or its two parts after a cut.
 int32_t run_mx4(Mx4Product& g, const Space& space, hipStream_t stream, const char* who) {
-    if (mx4_few(g.m)) return run_mx4_few(g, stream, who);
+    if (mx4_few(g.m, g.n)) return run_mx4_few(g, stream, who);
     const Way best = mx4_best_way(g.extent(), space);
     if (best.us == kNoWay) return fail(FSDP_E_CAPACITY, "%s: more output tiles than one launch holds", who);
     const Cut cut = mx4_cut_of(g.extent(), best, space);

@@ -19,7 +19,7 @@ static Extent extent(int64_t m, int64_t n, int64_t k) {
 
 // What run_mx4 does, as text; false if a bound does not hold.
 static bool walk(const Extent& g, const Space& space, char* out, size_t room, int depth) {
-    if (mx4_few(g.m)) {
+    if (mx4_few(g.m, g.n)) {
         const int f = mx4_few_features(g.m, g.n);
         snprintf(out, room, "few %d", f);
         return f >= 1 && f <= 4;

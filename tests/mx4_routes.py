@@ -14,6 +14,8 @@ ROUTES = [
     (16, 2 * 16 * 256 - 5, 700, 0, "few 2"),
     (9, 3 * 16 * 256 - 5, 1100, 0, "few 3"),
     (16, 4 * 16 * 256 - 5, 300, 0, "few 4"),
+    (1, 20000, 700, 0, "64x2/1"),
+    (16, 16 * 1024 + 1, 300, 0, "64x2/1"),
     (17, 300, 900, 64 * MIB, "64x4/1"),
     (1000, 1000, 2050, 64 * MIB, "64x4/1"),
     (64, 64, 16385, 64 * MIB, "64x4/7"),
