@@ -434,6 +434,12 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_dx_kernel(
 // Rows of a workgroup of the backward pass at a time.
 constexpr int backward_rows(int waves) { return waves == 1 ? 8 : 1; }
 
+// Rows that a thread adds in fp32, one after the other; the sums of as many are
+// joined in 64 bits.  In one chain the roundings of terms that are alike go one
+// way, and a sum stops growing at 2^24 times them: over 2^17 equal rows chains of
+// 2^11 were off by 3e-5, of 2^15 by 4e-4, for at most 9e-6 this way.
+constexpr int kChain = 64;
+
 // dx, and the column sums of the rows that a thread passes, which it holds for
 // the columns of its chunks.  Rows stay packed in registers, and the next one is
 // on its way while one is summed (two ahead: 20 % slower).  Bound by memory: 8192
@@ -442,12 +448,15 @@ constexpr int backward_rows(int waves) { return waves == 1 ? 8 : 1; }
 // stay for all rows: three a CU 69 us, four 73, for more sums to write and read;
 // one 69, for fewer loads on their way.  The registers allow two a CU with one
 // chunk a lane only (8192 x 1000: two of which one waits 24 us, one 18), and there
-// they are held to it (8192 x 4095: 113 us without, this way 84).
-template <typename T, int WAVES, int C, bool TAIL>
+// they are held to it (8192 x 4095: 113 us without, this way 84).  LONG: a wave
+// passes more than kChain rows; their sums wait in LDS, 16 bytes a column, which
+// leaves room for as many workgroups.
+template <typename T, int WAVES, int C, bool TAIL, bool LONG>
 __global__ __launch_bounds__(backward_rows(WAVES) * WAVES * 64, C == 1 ? 4 : 2) void norm_backward_kernel(BackwardArgs a) {
     constexpr int kEach = 16 / sizeof(T), kRows = backward_rows(WAVES);
     __shared__ float s[2][2][WAVES];
     __shared__ float joined[kRows > 1 ? 2 : 1][kRows > 1 ? C * kEach + TAIL : 1][64];
+    __shared__ double2 chains[LONG ? C * kEach + TAIL : 1][LONG ? kRows * WAVES * 64 : 1];  // each thread's own
     const int t = threadIdx.x % (64 * WAVES);
     Row<T, WAVES, C, TAIL> row;
     row.init(t, a.n);
@@ -474,7 +483,15 @@ __global__ __launch_bounds__(backward_rows(WAVES) * WAVES * 64, C == 1 ? 4 : 2) 
         r.mean = a.rms ? 0.0f : a.mean[i];
         r.rstd = a.rstd[i];
     };
-    int turn = 0;
+    // f(number, dw, db) of each pair of the thread's sums
+    auto each_sum = [&](auto&& f) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int q = 0; q < kEach; ++q) f(c * kEach + q, dw[c][q], db[c][q]);
+        if (TAIL) f(C * kEach, edw, edb);
+    };
+    int turn = 0, added = 0;
     Rows r;
     if (first < a.m) load(first, r);
     for (int64_t i = first; i < a.m; i += step, turn ^= 1) {
@@ -528,22 +545,29 @@ __global__ __launch_bounds__(backward_rows(WAVES) * WAVES * 64, C == 1 ? 4 : 2) 
             row.store_element(dx, a.res ? v + r.eres : v);
         }
         if (more) r = next;
+        if constexpr (LONG) {
+            if (++added % kChain == 0)
+                each_sum([&](int at, float& x, float& y) {
+                    double2& sum = chains[at][threadIdx.x];
+                    sum = added > kChain ? double2{sum.x + x, sum.y + y} : double2{x, y};
+                    x = y = 0.0f;
+                });
+        }
     }
+    if (LONG && added >= kChain)
+        each_sum([&](int at, float& x, float& y) {
+            x = static_cast<float>(chains[at][threadIdx.x].x + x);
+            y = static_cast<float>(chains[at][threadIdx.x].y + y);
+        });
     if constexpr (kRows > 1) {
         // the waves' sums one after the other, into the last one's registers
         const int wave = threadIdx.x >> 6;
         for (int turn = 0; turn < kRows; ++turn) {
-            if (wave == turn) {
-                auto join = [&](int at, float& x, float& y) {
+            if (wave == turn)
+                each_sum([&](int at, float& x, float& y) {
                     x = joined[0][at][t] = turn ? joined[0][at][t] + x : x;
                     y = joined[1][at][t] = turn ? joined[1][at][t] + y : y;
-                };
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int q = 0; q < kEach; ++q) join(c * kEach + q, dw[c][q], db[c][q]);
-                if (TAIL) join(C * kEach, edw, edb);
-            }
+                });
             __syncthreads();
         }
         if (wave != kRows - 1) return;
@@ -610,12 +634,13 @@ __global__ __launch_bounds__(kLongBlock) void norm_backward_long_kernel(Backward
 // The column sums alone: 64 chunks of columns by 4 rows at a time, `rows` rows a
 // block, into a row of `part` each; with one row block, into the results.  The
 // second read of dy and x makes 8192 x 11008 bf16 208 us in all, of which dx 108.
+// LONG: a place passes more than kChain rows.
 struct Sums {
     void* dw;
     void* db;
     int32_t f32, accumulate;
 };
-template <typename T>
+template <typename T, bool LONG>
 __global__ __launch_bounds__(256) void norm_columns_kernel(BackwardArgs a, Sums out, int32_t cblocks, int64_t rows) {
     constexpr int kEach = 16 / sizeof(T);
     __shared__ float sums[2][4][64][kEach + 1];
@@ -627,6 +652,8 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(BackwardArgs a, Sums 
     float dw[kEach], db[kEach];
 #pragma unroll
     for (int q = 0; q < kEach; ++q) dw[q] = db[q] = 0.0f;
+    double chains[LONG ? 2 : 1][LONG ? kEach : 1] = {};
+    int added = 0;
     const int64_t end = cnt > 0 ? min(a.m, (rb + 1) * rows) : 0;
     for (int64_t i = rb * rows + place; i < end; i += 4) {
         float x[kEach], g[kEach];
@@ -640,11 +667,20 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(BackwardArgs a, Sums 
             dw[q] = fmaf(g[q], (x[q] - mean) * rstd, dw[q]);
             db[q] += g[q];
         }
+        if constexpr (LONG) {
+            if (++added % kChain != 0) continue;
+#pragma unroll
+            for (int q = 0; q < kEach; ++q) {
+                chains[0][q] += dw[q];
+                chains[1][q] += db[q];
+                dw[q] = db[q] = 0.0f;
+            }
+        }
     }
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-        sums[0][place][lane][q] = dw[q];
-        sums[1][place][lane][q] = db[q];
+        sums[0][place][lane][q] = LONG ? static_cast<float>(chains[0][q] + dw[q]) : dw[q];
+        sums[1][place][lane][q] = LONG ? static_cast<float>(chains[1][q] + db[q]) : db[q];
     }
     __syncthreads();
     for (int t = threadIdx.x; t < 2 * 64 * kEach; t += 256) {
@@ -864,8 +900,11 @@ int32_t launch_backward(BackwardArgs a, const Sums& out, float* workspace, int64
         auto run = [&](auto waves, auto chunks) {
             constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
             const dim3 grid(static_cast<uint32_t>(blocks)), block(backward_rows(W) * W * 64);
-            if (whole) norm_backward_kernel<T, W, C, false><<<grid, block, 0, stream>>>(a);
-            else norm_backward_kernel<T, W, C, true><<<grid, block, 0, stream>>>(a);
+            const bool chains = a.m > kChain * backward_rows(W) * blocks;
+            if (whole && !chains) norm_backward_kernel<T, W, C, false, false><<<grid, block, 0, stream>>>(a);
+            else if (whole) norm_backward_kernel<T, W, C, false, true><<<grid, block, 0, stream>>>(a);
+            else if (!chains) norm_backward_kernel<T, W, C, true, false><<<grid, block, 0, stream>>>(a);
+            else norm_backward_kernel<T, W, C, true, true><<<grid, block, 0, stream>>>(a);
         };
         with<1, 1>(d, run) || with<1, 2>(d, run) || with<4, 1>(d, run) || with<8, 1>(d, run) || with<16, 1>(d, run);
         TRY(launched(who));
@@ -892,8 +931,9 @@ int32_t launch_backward(BackwardArgs a, const Sums& out, float* workspace, int64
     const int64_t want = std::max<int64_t>(1, std::min(8 * kCus / cblocks, room));
     const int64_t rows = ceil_div(ceil_div(a.m, 4), want) * 4, rblocks = ceil_div(a.m, rows);
     a.part = rblocks > 1 ? workspace : nullptr;
-    norm_columns_kernel<T><<<dim3(static_cast<uint32_t>(cblocks * rblocks)), dim3(256), 0, stream>>>(
-        a, out, static_cast<int32_t>(cblocks), rows);
+    const dim3 grid(static_cast<uint32_t>(cblocks * rblocks));
+    if (rows > 4 * kChain) norm_columns_kernel<T, true><<<grid, dim3(256), 0, stream>>>(a, out, static_cast<int32_t>(cblocks), rows);
+    else norm_columns_kernel<T, false><<<grid, dim3(256), 0, stream>>>(a, out, static_cast<int32_t>(cblocks), rows);
     TRY(launched(who));
     return rblocks == 1 ? FSDP_OK : join(rblocks);
 }
