@@ -41,8 +41,10 @@ typedef enum {
  *   bias      w_dtype [n], or NULL for zeros
  *   eps       at least 0, finite in fp32.  With 0 a row without variance gives NaN.
  * The variance is summed about the mean, so a mean that is large against the
- * row's spread costs no more than the mean's own rounding to fp32.  For n = 0
- * nothing is written. */
+ * row's spread costs no more than the mean's own rounding to fp32.  A row whose
+ * sum, or sum of squares, is past fp32's range, or whose var + eps is under
+ * 2^-100, is summed in 64 bits (8192 rows of 4096 bf16: 0.13 ms, for 0.03), so y
+ * holds for all finite x.  For n = 0 nothing is written. */
 int32_t fsdp_norm_forward(void* y, int64_t ldy, float* mean, float* rstd, const void* x, int64_t ldx,
                           int32_t dtype, int32_t kind, const void* weight, const void* bias,
                           int32_t w_dtype, double eps, int64_t m, int64_t n, hipStream_t stream);
@@ -58,7 +60,9 @@ int32_t fsdp_norm_forward(void* y, int64_t ldy, float* mean, float* rstd, const 
  *   dy, x     [m, n] of dtype; x as the forward call read it
  *   weight    w_dtype [n], or NULL for ones
  *   mean      fp32 [m] as the forward call stored it; NULL for FSDP_NORM_RMS
- *   rstd      fp32 [m] as the forward call stored it
+ *   rstd      fp32 [m] as the forward call stored it.  It has fp32's digits for
+ *             rows with a spread from 2^-127 to 2^126, and x - mean must not
+ *             exceed fp32's range.
  *   residual  [m, n] of dtype, or NULL: the gradient that reaches x past the
  *             norm; may be dx itself
  *   workspace, workspace_bytes  as in fsdp_linear.h: device memory the call may

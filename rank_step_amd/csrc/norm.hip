@@ -167,25 +167,109 @@ struct ForwardArgs {
     float* mean;
     float* rstd;
     int64_t ldy, ldx, m, n;
-    float eps;
+    double eps;  // rounded to fp32 but in forward_row_wide
     int32_t w_f32, rms, wt;
 };
+
+// Whether fp32 held the sum of squares: not where it, or the row's sum, has passed
+// 2^128, nor where squares may have been lost below 2^-126.  The same in all the
+// row's lanes; false for NaN.
+__device__ __forceinline__ bool in_range(float var_eps) { return var_eps >= 0x1p-100f && var_eps < INFINITY; }
+
+__device__ __forceinline__ double wide(uint16_t v) { return widen(v); }
+__device__ __forceinline__ double wide(float v) { return v; }
+
+// Thread t's sum over the row's waves, as row_sum, with a shared `s` of its own for
+// each of a row's sums.
+template <int WAVES>
+__device__ __forceinline__ double row_sum(double v, double* s, int t) {
+#pragma unroll 1
+    for (int d = 1; d < 64; d <<= 1) {
+        const u32x2 w = __builtin_bit_cast(u32x2, v);
+        const int from = ((t ^ d) & 63) * 4;
+        v += __builtin_bit_cast(double, u32x2{static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(from, static_cast<int>(w[0]))),
+                                              static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(from, static_cast<int>(w[1])))});
+    }
+    if constexpr (WAVES > 1) {
+        if ((t & 63) == 0) s[t >> 6] = v;
+        __syncthreads();
+        v = s[0];
+#pragma unroll 1
+        for (int p = 1; p < WAVES; ++p) v += s[p];
+    }
+    return v;
+}
+
+// The thread's number among a row's threads, which the compiler takes for another
+// one each time: what depends on it is made where it is used, and holds no
+// registers across forward_row_wide.
+template <int WAVES>
+__device__ __forceinline__ int opaque_thread() {
+    int t = threadIdx.x % (64 * WAVES);
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+// Row i in 64 bits, read again for each sum: the few rows that fp32's range does
+// not hold, and those with an infinity or a NaN.  A thread reads and writes the
+// same elements, so y may be x.  8192 such rows of 4096 bf16: 131 us.
+template <typename T, int WAVES>
+__device__ __forceinline__ void forward_row_wide(const ForwardArgs& a, int64_t i, int t) {
+    __shared__ double s[2][WAVES];
+    int64_t cols = a.n;
+    asm volatile("" : "+s"(cols));  // as in opaque_thread
+    const T* const x = static_cast<const T*>(a.x) + i * a.ldx;
+    T* const y = static_cast<T*>(a.y) + i * a.ldy;
+    const double n = static_cast<double>(cols);
+    double mean = 0.0, var = 0.0;
+    if (!a.rms) {
+#pragma unroll 1
+        for (int64_t j = t; j < cols; j += 64 * WAVES) mean += wide(x[j]);
+        mean = row_sum<WAVES>(mean, s[0], t) / n;
+    }
+#pragma unroll 1
+    for (int64_t j = t; j < cols; j += 64 * WAVES) {
+        const double d = wide(x[j]) - mean;
+        var = fma(d, d, var);
+    }
+    const double rstd = 1.0 / sqrt(row_sum<WAVES>(var, s[1], t) / n + a.eps);
+    if (t == 0) {
+        if (a.mean) a.mean[i] = static_cast<float>(mean);
+        if (a.rstd) a.rstd[i] = static_cast<float>(rstd);
+    }
+#pragma unroll 1
+    for (int64_t j = t; j < cols; j += 64 * WAVES) {
+        const float w = load_param(a.w, a.w_f32, j, 1.0f), b = load_param(a.b, a.w_f32, j, 0.0f);
+        const float v = static_cast<float>(fma((wide(x[j]) - mean) * rstd, static_cast<double>(w), static_cast<double>(b)));
+        if constexpr (sizeof(T) == 2) y[j] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+        else y[j] = v;
+    }
+    if (WAVES > 1) __syncthreads();  // before the next row's sums
+}
 
 // A row by WAVES waves of C chunks of 16 bytes a lane, which stay packed in
 // registers and are widened for each pass over them.  Bound by memory, a
 // workgroup a row (four where a wave takes one), so that some rows load while
 // others store: 8192 x 4096 bf16 26.8 us (5.0 TB/s; a copy's 20.7).  With rows held
 // widened and workgroups that stay for several 42, one wave a row 30, eight 32.
+// The addresses and conditions of a lane's chunks are made for each row, which
+// takes up to half of the registers less than before the loop (8192 x 2048 bf16
+// 14.5 us for 17.5, 8192 x 11008 75.5 for 97, 8192 x 11007 fp32 140 for 171); but
+// before it (kAhead) where that was the faster way: 8192 x 4096 bf16 28.7 for 30.2,
+// fp32 48.6 for 51.7, 8192 x 4095 fp32 52.9 for 55.6.  With more than 80 scalar
+// registers a SIMD has not eight waves: 8192 x 1024 fp32 13.5 us, with 87 15.0.
 template <typename T, int WAVES, int C, bool TAIL>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_kernel(ForwardArgs a) {
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) __attribute__((amdgpu_num_sgpr(80)))
+void norm_forward_kernel(ForwardArgs a) {
     constexpr int kEach = 16 / sizeof(T), kRows = WAVES == 1 ? 4 : 1;
+    constexpr bool kAhead = WAVES == 4 && (sizeof(T) == 4 ? C == 4 : C == 2 && !TAIL);
     __shared__ float s0[1][WAVES], s1[2][WAVES];
-    const int t = threadIdx.x % (64 * WAVES);
-    Row<T, WAVES, C, TAIL> row;
-    row.init(t, a.n);
-    const float n = static_cast<float>(a.n);
+    const float n = static_cast<float>(a.n), eps = static_cast<float>(a.eps);
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / (64 * WAVES); i < a.m;
          i += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int t = kAhead ? threadIdx.x % (64 * WAVES) : opaque_thread<WAVES>();
+        Row<T, WAVES, C, TAIL> row;
+        row.init(t, a.n);
         u32x4 raw[C];
         float end;
         row.load(static_cast<const T*>(a.x) + i * a.ldx, raw, end);
@@ -223,7 +307,11 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_forward_ke
         row_sum<WAVES>(sum, s1);
         float var = sum[1] / n;
         if (!a.rms) correct(sum[0] / n, mean, var);
-        const float rstd = 1.0f / sqrtf(var + a.eps);
+        if (__builtin_expect(!in_range(var + eps), 0)) {
+            forward_row_wide<T, WAVES>(a, i, opaque_thread<WAVES>());
+            continue;
+        }
+        const float rstd = 1.0f / sqrtf(var + eps);
         if (t == 0) {
             if (a.mean) a.mean[i] = mean;
             if (a.rstd) a.rstd[i] = rstd;
@@ -297,7 +385,7 @@ __device__ __forceinline__ void store_values(float* p, const Values<N>& x) {
 template <typename T>
 __global__ __launch_bounds__(kLongBlock) void norm_forward_long_kernel(ForwardArgs a) {
     __shared__ float s0[1][kLongWaves], s1[2][kLongWaves];
-    const float n = static_cast<float>(a.n);
+    const float n = static_cast<float>(a.n), eps = static_cast<float>(a.eps);
     for (int64_t i = blockIdx.x; i < a.m; i += gridDim.x) {
         const T* const x[1] = {static_cast<const T*>(a.x) + i * a.ldx};
         T* const y = static_cast<T*>(a.y) + i * a.ldy;
@@ -328,7 +416,11 @@ __global__ __launch_bounds__(kLongBlock) void norm_forward_long_kernel(ForwardAr
         row_sum<kLongWaves>(sum, s1);
         float var = sum[1] / n;
         if (!a.rms) correct(sum[0] / n, mean, var);
-        const float rstd = 1.0f / sqrtf(var + a.eps);
+        if (__builtin_expect(!in_range(var + eps), 0)) {
+            forward_row_wide<T, kLongWaves>(a, i, opaque_thread<kLongWaves>());
+            continue;
+        }
+        const float rstd = 1.0f / sqrtf(var + eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[i] = mean;
             if (a.rstd) a.rstd[i] = rstd;
@@ -857,7 +949,7 @@ int32_t forward_impl(void* y, int64_t ldy, float* mean, float* rstd, const void*
     a.ldx = ldx;
     a.m = m;
     a.n = n;
-    a.eps = static_cast<float>(eps);
+    a.eps = eps;
     a.w_f32 = we == 4;
     a.rms = kind == FSDP_NORM_RMS;
     a.wt = stream_ok(y, ldy, e);
