@@ -57,7 +57,9 @@ extern "C" {
  * -127) (0 for a block of zeros); each element becomes the nearest code, ties to
  * the even one, and what is above 6 times the scale becomes 6 times it.  A
  * block with a NaN or an infinity has scale 255 and codes 0.  rows and cols are
- * at most 2^30. */
+ * at most 2^30, and with codes_t a launch holds 2^22 - 1 tiles of 256 x 128
+ * elements, rows and (with codes) cols rounded up to 512, and refuses more with
+ * FSDP_E_CAPACITY (up to 512 columns, more than 2^28 - 512 rows). */
 int32_t fsdp_mx4_quantize(uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds, uint8_t* codes_t,
                           int64_t ldct, uint8_t* scales_t, int64_t ldst, const void* x, int64_t ldx,
                           int32_t x_dtype, int64_t rows, int64_t cols, hipStream_t stream);
@@ -80,7 +82,8 @@ int32_t fsdp_mx4_dequantize(void* y, int64_t ldy, int32_t y_dtype, const uint8_t
  *   dropout      NULL for none; act, dropout and residual as in fsdp_linear
  * Row strides: of a, a_scales, b and b_scales in bytes, at most 2^22 (else
  * FSDP_E_CAPACITY); of the others in elements, their rows from any element.
- * m, n and k are at most 2^30, and a launch holds at most 2^22 - 1 workgroups.
+ * m and n are at most 2^30, k at most 2^23 (whose row of codes is 2^22 bytes),
+ * and a launch holds at most 2^22 - 1 workgroups: else FSDP_E_CAPACITY.
  * The products of two elements are exact and are added in fp32 by the matrix
  * instructions; what follows is fp32, and each output is rounded once.  A NaN
  * block of A makes its row NaN, one of B its column.

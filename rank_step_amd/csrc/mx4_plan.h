@@ -13,6 +13,7 @@ namespace linear {
 // A product's rows lie no further apart: a tile's 256 of them are within the 31
 // bits of a buffer offset.
 constexpr int64_t kMaxMx4Stride = int64_t(1) << 22;
+constexpr int64_t kMaxMx4Contraction = 2 * kMaxMx4Stride;  // its codes are such a row
 
 // The two arrays of a 4-bit matrix, as matrices of bytes.
 struct Mx4Matrix {

@@ -649,6 +649,7 @@ int32_t mx4_product_impl(const fsdp_mx4_operands* a, hipStream_t stream) {
                         ma.codes, ma.scales, mb.codes, mb.scales, r, b, bytes_of(g.e.mask.offset_dev, 8, "offset_dev", false)},
                        who, [&](const Matrix& p, const Matrix& q) { return p.what == y.what && q.what == r.what; }));
     if (a->m == 0 || a->n == 0) return FSDP_OK;
+    if (a->k > kMaxMx4Contraction) return fail(FSDP_E_CAPACITY, "%s: k exceeds 2^23", who);
     // The stride of a single row says nothing; its length stands for it.
     const int64_t codes = FSDP_MX4_CODE_BYTES(a->k), scales = FSDP_MX4_SCALE_BYTES(a->k);
     const int64_t lda = a->m > 1 ? a->lda : codes, ldb = a->n > 1 ? a->ldb : codes;
