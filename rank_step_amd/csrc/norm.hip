@@ -381,7 +381,8 @@ __device__ __forceinline__ void store_values(float* p, const Values<N>& x) {
 
 // A row that registers do not hold, read once for each sum and once for y.  Its
 // length has no bound, so a thread joins its chunks' sums in 64 bits.
-// 1024 x 65536 bf16 78 us (a copy's 41): a row's second and third read come from L2.
+// 1024 x 65536 bf16 with weight, bias and statistics 95 us (a copy's 41): a row's
+// second and third read come from L2.
 template <typename T>
 __global__ __launch_bounds__(kLongBlock) void norm_forward_long_kernel(ForwardArgs a) {
     __shared__ float s0[1][kLongWaves], s1[2][kLongWaves];
@@ -874,8 +875,8 @@ struct Division {
 };
 
 // A row by itself: by its length alone, so that its result is the same among any
-// other rows.  fp32 rows of 11007 (8192 of them) 175 us by 16 waves of 4 chunks, by
-// 8 of 8 194; bf16 rows of 2048 by one wave 14.4, by four 14.9.
+// other rows.  8192 bf16 rows of 2048 13.5 to 14.5 us by one wave, by four 19.8;
+// fp32 rows of 11007 140 by 16 waves of 4 chunks, as by 8 of 8.
 Division row_division(int64_t n, int elem) {
     const int64_t chunks = ceil_div(n, 16 / elem);
     for (const Division d : {Division{1, 1}, {1, 2}, {1, 4}, {4, 2}, {4, 4}, {8, 4}, {16, 4}})
@@ -958,9 +959,18 @@ int32_t forward_impl(void* y, int64_t ldy, float* mean, float* rstd, const void*
     return launched(who);
 }
 
-// Rows up to which the column sums are taken beside dx in one launch.  333 x 1365
-// fp32: 10.1 us, by two launches 11.4; 512 x 4096 bf16 15 and 21; 600 x 4096 17.5
-// and 21.8.
+// Rows up to which the column sums are taken beside dx in one launch.  In one
+// launch and in two, with a residual, us:
+//   rows              400          600          820         1024
+//   bf16, 1024      9, 12.7     14, 12.7   20.3, 12.8   25.3, 12.6
+//   bf16, 2048   11.3, 15.1   17.3, 15.9   22.6, 16.3   26.8, 16.9
+//   bf16, 4096   13.0, 22.4   18.6, 26.1   25.0, 28.0   30.0, 28.5
+//   bf16, 8192   15.0, 24.6   21.0, 27.9   27.5, 30.8   32.2, 32.2
+//   fp32, 1024   10.6, 11.9   15.9, 12.3   21.0, 12.2   25.1, 12.4
+//   fp32, 2048   12.2, 13.0   17.5, 14.5   23.4, 16.0   28.2, 16.3
+//   fp32, 4096   14.2, 15.3   19.5, 18.3   26.2, 21.4   32.2, 22.3
+// so the bound is right for wide bf16 rows; others cross between 400 and 600 rows.
+// 333 x 1365 fp32: 10.2 and 11.4.
 constexpr int64_t kFewRows = 1024;
 
 template <typename T>
