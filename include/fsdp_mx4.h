@@ -7,7 +7,14 @@
  *   fsdp_mx4_product      y = D(act(A B^T + bias)) + residual of two copies
  * A third all-gather copy beside fsdp_step.h's bf16 and fp8 ones: a rank
  * quantises its rows of a weight, the gathered bytes are the whole weight's
- * copy, and the product takes them at up to four times bf16's rate.  A layer
+ * copy, and the product takes them at up to four times bf16's rate.  That holds
+ * for W, whose blocks lie along rows.  The blocks of its transpose lie across the
+ * ranks' rows, and each rank's piece [k, rows of a rank] has blocks and padding of
+ * its own, so gathered pieces are not one operand: the input gradient is either
+ * the product with a transpose that is quantised from the whole weight (the
+ * gathered bf16 copy, say), or one product a piece, with the columns of dz that
+ * are that rank's rows quantised by themselves, added in place (residual = y).
+ * A layer
  * y = x W^T in 4 bits is
  *   forward       product of x and W                    (blocks along the input features)
  *   input grad    product of dz and W's transpose       (along the output features)
