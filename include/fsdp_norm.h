@@ -73,7 +73,7 @@ int32_t fsdp_norm_forward(void* y, int64_t ldy, float* mean, float* rstd, const 
  *             8 n bytes are a part; 8192 rows of 4096 take 0.06 ms with room
  *             for 512 of them, 1.5 ms with none.
  * A column's rows are added in fp32 by at most 64 one after the other, and those
- * sums joined in 64 bits: the error of dw and db, at most 143 * 2^-24 of the sum
+ * sums joined in 64 bits: the error of a sum, at most 143 * 2^-24 of the sum
  * of their terms' magnitudes, does not grow with m. */
 #define FSDP_NORM_WORKSPACE_BYTES ((int64_t)64 << 20)
 
